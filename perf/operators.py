@@ -1,0 +1,506 @@
+"""Cases of the softmax-attention operators: rotary positions, attention forward and
+backward, the 8-bit paged key/value cache and the attention that reads it.
+
+`own` false computes each operator in its plain form (elementary torch operations in
+32 bits, rounded once at the end); `own` true calls the library.
+"""
+
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+F8 = torch.float8_e4m3fn
+DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+ESIZE = {"f32": 4, "bf16": 2}
+
+
+# ------------------------------------------------------------------ the cases
+
+def listed():
+    return [
+        # one decoded token of 256 sequences: the position encoding of its q and k (latency)
+        dict(name="rotary_step", op="rotary", B=256, T=1, H=32, HK=8, D=128, rot=128, dtype="bf16", interleaved=False,
+             inverse=False, scaling="none", far=65536),
+        # a prompt batch of the layer workload, half of each head rotated, scaled for a long context
+        dict(name="rotary_layer", op="rotary", B=4, T=4096, H=16, HK=4, D=128, rot=64, dtype="bf16", interleaved=True,
+             inverse=False, scaling="yarn", far=131072),
+        # the gradient (transposed rotation) of a small fp32 training step of odd length
+        dict(name="rotary_grad", op="rotary", B=2, T=1023, H=4, HK=2, D=64, rot=64, dtype="f32", interleaved=False,
+             inverse=True, scaling="linear", far=4096),
+        # prefill of the layer workload with shared key/value heads
+        dict(name="attn_fwd_layer", op="attn_fwd", B=4, Tq=4096, Tk=4096, H=16, HK=4, D=128, dtype="bf16", causal=True,
+             window=0, ragged=False),
+        # a small fp32 batch of unequal lengths, every key visible
+        dict(name="attn_fwd_ragged", op="attn_fwd", B=2, Tq=1023, Tk=1023, H=4, HK=4, D=64, dtype="f32", causal=False,
+             window=0, ragged=True),
+        # sixteen new tokens behind a long dense context
+        dict(name="attn_fwd_extend", op="attn_fwd", B=1, Tq=16, Tk=65536, H=32, HK=8, D=128, dtype="bf16", causal=True,
+             window=0, ragged=False),
+        # the training backward of the layer workload
+        dict(name="attn_bwd_layer", op="attn_bwd", B=4, Tq=4096, Tk=4096, H=16, HK=4, D=128, dtype="bf16", causal=True,
+             window=0, ragged=False),
+        # a small fp32 training step: sliding window, unequal lengths
+        dict(name="attn_bwd_window", op="attn_bwd", B=2, Tq=1024, Tk=1024, H=4, HK=2, D=64, dtype="f32", causal=True,
+             window=256, ragged=True),
+        # one decoded token of 256 sequences goes into the cache (latency)
+        dict(name="append_step", op="append", B=256, T=1, HK=8, D=128, page=64, dtype="bf16", max_len=1024),
+        # a prompt batch goes into the cache
+        dict(name="append_prompt", op="append", B=4, T=4096, HK=8, D=128, page=64, dtype="bf16", max_len=8192),
+        # one decoded token of 256 sequences of unequal lengths reads the cache
+        dict(name="step_decode", op="step", B=256, T=1, H=32, HK=8, D=128, page=64, dtype="bf16", max_len=4096, window=0),
+        # four drafted tokens of one sequence read a long cache (few rows, long axis)
+        dict(name="step_long", op="step", B=1, T=4, H=32, HK=8, D=128, page=128, dtype="bf16", max_len=65536, window=0),
+    ]
+
+
+def _log(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["rotary", "attn_fwd", "attn_bwd", "append", "step"])
+    dtype = rng.choice(["bf16", "bf16", "f32"])
+    D = rng.choice([16, 32, 64, 128, 128])
+    HK = rng.choice([1, 2, 4, 8])
+    G = rng.choice([1, 2, 4, 8])
+    c = dict(op=op, dtype=dtype, D=D, HK=HK)
+    if op == "rotary":
+        B = _log(rng, 1, 256)
+        T = _log(rng, 1, max(1, 16384 // B))
+        c.update(B=B, T=T, H=HK * rng.choice([1, 2, 4]), rot=2 * rng.randint(max(1, D // 8), D // 2),
+                 interleaved=rng.random() < 0.5, inverse=rng.random() < 0.5,
+                 scaling=rng.choice(["none", "linear", "ntk", "yarn"]), far=_log(rng, 1024, 1 << 20))
+    elif op in ("attn_fwd", "attn_bwd"):
+        B = _log(rng, 1, 8)
+        most = 4096 if dtype == "bf16" else 1024
+        Tk = _log(rng, 1, most)
+        Tq = Tk if op == "attn_bwd" or rng.random() < 0.5 else _log(rng, 1, Tk)
+        G = max(1, min(G, 16 // HK))
+        c.update(B=min(B, 4) if Tk > 2048 else B, Tq=Tq, Tk=Tk, H=HK * G, causal=rng.random() < 0.7,
+                 window=_log(rng, 1, Tk) if rng.random() < 0.3 else 0, ragged=rng.random() < 0.5)
+    elif op == "append":
+        B = _log(rng, 1, 256)
+        T = _log(rng, 1, max(1, 8192 // B))
+        c.update(B=B, T=T, page=rng.choice([16, 32, 64, 128]), max_len=T + _log(rng, 1, 1024))
+    else:
+        B = _log(rng, 1, 256)
+        T = _log(rng, 1, 16)
+        c.update(B=B, T=T, H=HK * G, page=rng.choice([16, 32, 64, 128]), max_len=T + _log(rng, 1, max(16, 262144 // B)),
+                 window=_log(rng, 1, 4096) if rng.random() < 0.3 else 0)
+    return c
+
+
+# ------------------------------------------------------------------ the inputs
+
+def _spread(B, least, most):
+    """Lengths of B sequences, evenly from `least` to `most`, the longest last."""
+    return [most if B == 1 else least + (most - least) * b // (B - 1) for b in range(B)]
+
+
+def _ints(values):
+    return torch.tensor(values, dtype=torch.int32, device="cuda")
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(int(seed))
+
+
+def _normal(g, shape, dtype, std=1.0):
+    return (torch.randn(shape, generator=g, device="cuda") * std).to(DTYPES[dtype])
+
+
+def _frequencies(rot, scaling, base=10000.0, factor=8.0, trained=8192):
+    """(inverse frequencies in 64 bits, scale of the rotated values)."""
+    i = np.arange(rot // 2, dtype=np.float64)
+    if scaling == "ntk" and rot > 2:
+        base = base * factor ** (rot / (rot - 2.0))
+    f = base ** (-2.0 * i / rot)
+    if scaling == "linear":
+        return f / factor, 1.0
+    if scaling == "yarn":
+        def index(turns):
+            return rot * math.log(trained / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
+        lo, hi = max(math.floor(index(32.0)), 0), min(math.ceil(index(1.0)), rot - 1)
+        ramp = np.clip((i - lo) / max(hi - lo, 1e-3), 0.0, 1.0)
+        return f / factor * ramp + f * (1.0 - ramp), 0.1 * math.log(factor) + 1.0
+    return f, 1.0
+
+
+def _pages(c):
+    return -(-c["max_len"] // c["page"])
+
+
+def _lengths(c):
+    """Tokens of each sequence before the call and new ones in it."""
+    after = _spread(c["B"], min(c["max_len"], c["T"] + c["max_len"] // 8), c["max_len"])
+    return [n - c["T"] for n in after], [c["T"]] * c["B"]
+
+
+def _attn_lengths(c):
+    if not c["ragged"]:
+        return [c["Tq"]] * c["B"], [c["Tk"]] * c["B"]
+    return _spread(c["B"], 1 + c["Tq"] // 3, c["Tq"]), _spread(c["B"], 1 + c["Tk"] // 2, c["Tk"])
+
+
+def _attn_inputs(c, g):
+    B, H, HK, D = c["B"], c["H"], c["HK"], c["D"]
+    if c["Tq"] == c["Tk"]:  # one packed projection, read in place
+        x = _normal(g, (B, c["Tq"], H + 2 * HK, D), c["dtype"])
+        return x[:, :, :H], x[:, :, H:H + HK], x[:, :, H + HK:]
+    return (_normal(g, (B, c["Tq"], H, D), c["dtype"]), _normal(g, (B, c["Tk"], HK, D), c["dtype"]),
+            _normal(g, (B, c["Tk"], HK, D), c["dtype"]))
+
+
+def _cache(c, g):
+    """A cache in use: codes of normal values, scales 2^-8 .. 2^-5, pages in random order."""
+    n, np_ = c["B"] * _pages(c) + 3, _pages(c)
+    kc = (torch.randn((n, c["HK"], c["page"], c["D"]), generator=g, device="cuda") * 100.0).clamp_(-448, 448).to(F8).view(torch.uint8)
+    vc = (torch.randn((n, c["HK"], c["D"], c["page"]), generator=g, device="cuda") * 100.0).clamp_(-448, 448).to(F8).view(torch.uint8)
+    ks, vs = (torch.exp2(torch.randint(-8, -4, (n, c["HK"]), generator=g, device="cuda").float()) for _ in range(2))
+    table = torch.randperm(n, generator=g, device="cuda")[:c["B"] * np_].view(c["B"], np_).to(torch.int32)
+    return kc, vc, ks, vs, table
+
+
+def prepare(case, seed):
+    c, g = case, _gen(seed)
+    s = {"c": c}
+    if c["op"] == "rotary":
+        B, T = c["B"], c["T"]
+        x = _normal(g, (B, T, c["H"] + c["HK"], c["D"]), c["dtype"])
+        f, scale = _frequencies(c["rot"], c["scaling"])
+        first = torch.randint(0, max(1, c["far"] - T), (B, 1), generator=g, device="cuda")
+        pos = (first + torch.arange(T, device="cuda")).to(torch.int32)
+        s.update(q=x[:, :, :c["H"]], k=x[:, :, c["H"]:], pos=pos, freqs=torch.from_numpy(f).cuda(), scale=scale)
+    elif c["op"] in ("attn_fwd", "attn_bwd"):
+        q, k, v = _attn_inputs(c, g)
+        ql, kl = _attn_lengths(c)
+        s.update(q=q, k=k, v=v, scale=c["D"] ** -0.5, q_len=_ints(ql) if c["ragged"] else None,
+                 kv_len=_ints(kl) if c["ragged"] else None)
+        if c["op"] == "attn_bwd":
+            s["dout"] = _normal(g, (c["B"], c["Tq"], c["H"], c["D"]), c["dtype"])
+            s["o"], s["lse"] = _plain_attn_fwd(s)  # what the forward pass left
+    elif c["op"] == "append":
+        s["kc"], s["vc"], s["ks"], s["vs"], s["table"] = _cache(c, g)
+        before, new = _lengths(c)
+        s["k"], s["v"] = (_normal(g, (c["B"], c["T"], c["HK"], c["D"]), c["dtype"], std) for std in (3.0, 1.0))
+        s["cache_len"] = _ints(before)
+    else:
+        s["kc"], s["vc"], s["ks"], s["vs"], s["table"] = _cache(c, g)
+        before, new = _lengths(c)
+        s["q"] = _normal(g, (c["B"], c["T"], c["H"], c["D"]), c["dtype"])
+        s["cache_len"], s["scale"] = _ints(before), c["D"] ** -0.5
+    return s
+
+
+# ------------------------------------------------------------------ plain forms
+
+def _rotate(x, cos, sin, c):
+    """The first `rot` channels of x [B,T,h,D] turned; cos, sin [B,T,1,rot/2]."""
+    r, y = c["rot"], x.float()
+    a, b = (y[..., 0:r:2], y[..., 1:r:2]) if c["interleaved"] else (y[..., :r // 2], y[..., r // 2:r])
+    a, b = a * cos - b * sin, a * sin + b * cos
+    turned = torch.stack((a, b), -1).flatten(-2) if c["interleaved"] else torch.cat((a, b), -1)
+    return torch.cat((turned, y[..., r:]), -1).to(x.dtype)
+
+
+def _plain_rotary(s):
+    c = s["c"]
+    angle = s["pos"].double()[:, :, None, None] * s["freqs"]
+    cos, sin = (torch.cos(angle) * s["scale"]).float(), (torch.sin(angle) * s["scale"]).float()
+    if c["inverse"]:
+        sin = -sin
+    return _rotate(s["q"], cos, sin, c), _rotate(s["k"], cos, sin, c)
+
+
+def _visible(s):
+    """Which keys each query sees: [B,1,1,Tq,Tk] truth values, and the rows in use [B,1,1,Tq,1]."""
+    c = s["c"]
+    i = torch.arange(c["Tq"], device="cuda")[:, None]
+    j = torch.arange(c["Tk"], device="cuda")[None]
+    ql = torch.full((c["B"],), c["Tq"], device="cuda") if s["q_len"] is None else s["q_len"]
+    kl = torch.full((c["B"],), c["Tk"], device="cuda") if s["kv_len"] is None else s["kv_len"]
+    ql, kl = ql.view(-1, 1, 1, 1, 1), kl.view(-1, 1, 1, 1, 1)
+    at = i + kl - ql
+    seen = (j < kl) & (i < ql)
+    if c["causal"]:
+        seen = seen & (j <= at)
+    if c["window"]:
+        seen = seen & (j > at - c["window"])
+    return seen
+
+
+def _grouped(x, HK):
+    """[B,T,h,D] as [B,HK,h/HK,T,D] in 32 bits."""
+    B, T, h, D = x.shape
+    return x.float().view(B, T, HK, h // HK, D).permute(0, 2, 3, 1, 4)
+
+
+def _probabilities(s):
+    c = s["c"]
+    q, k = _grouped(s["q"], c["HK"]), _grouped(s["k"], c["HK"])
+    B, HK, G, Tq, D = q.shape
+    S = torch.matmul((q * s["scale"]).reshape(B, HK, G * Tq, D), k[:, :, 0].transpose(-1, -2)).view(B, HK, G, Tq, -1)
+    S = S.masked_fill_(~_visible(s), -math.inf)
+    m = S.amax(-1, keepdim=True)
+    P = torch.exp_(S.sub_(torch.where(m == -math.inf, 0.0, m)))
+    total = P.sum(-1, keepdim=True)
+    return P.div_(torch.where(total > 0, total, 1.0)), (m + torch.log(total))[..., 0]
+
+
+def _heads(x, dtype):
+    """[B,HK,G,T,D] back to [B,T,HK G,D]."""
+    B, HK, G, T, D = x.shape
+    return x.permute(0, 3, 1, 2, 4).reshape(B, T, HK * G, D).to(dtype)
+
+
+def _plain_attn_fwd(s):
+    c = s["c"]
+    P, lse = _probabilities(s)
+    B, HK, G, Tq, Tk = P.shape
+    o = torch.matmul(P.view(B, HK, G * Tq, Tk), _grouped(s["v"], HK)[:, :, 0]).view(B, HK, G, Tq, -1)
+    return _heads(o, s["q"].dtype), lse.reshape(B, HK * G, Tq)
+
+
+def _plain_attn_bwd(s):
+    c, dt = s["c"], s["q"].dtype
+    P, _ = _probabilities(s)
+    B, HK, G, Tq, Tk = P.shape
+    q, k, v, do = (_grouped(s[n], HK) for n in ("q", "k", "v", "dout"))
+    flat = lambda x: x.reshape(B, HK, -1, x.shape[-1])  # noqa: E731
+    dv = torch.matmul(flat(P).transpose(-1, -2), flat(do))
+    dP = torch.matmul(flat(do), v[:, :, 0].transpose(-1, -2)).view(B, HK, G, Tq, Tk)
+    dP = dP.sub_((P * dP).sum(-1, keepdim=True)).mul_(P).mul_(s["scale"])
+    dq = torch.matmul(flat(dP), k[:, :, 0]).view(B, HK, G, Tq, -1)
+    dk = torch.matmul(flat(dP).transpose(-1, -2), flat(q))
+    return {"dq": _heads(dq, dt), "dk": _heads(dk[:, :, None], dt), "dv": _heads(dv[:, :, None], dt)}
+
+
+def _plain_append_one(s, x, codes, scales, keys):
+    """One of K (codes [page][D]) and V (codes [D][page]) goes into its pages."""
+    c = s["c"]
+    B, T, page = c["B"], c["T"], c["page"]
+    touched = (T + page - 1) // page + 1
+    before = s["cache_len"].long()[:, None]
+    number = before // page + torch.arange(touched, device="cuda")                # [B,touched] page of the sequence
+    inside = number < s["table"].shape[1]
+    at = s["table"].long().gather(1, number.clamp(max=s["table"].shape[1] - 1))   # page of the cache
+    pos = number[:, :, None] * page + torch.arange(page, device="cuda")           # [B,touched,page]
+    older, newer = pos < before[:, :, None], (pos >= before[:, :, None]) & (pos < before[:, :, None] + T)
+    t = (pos - before[:, :, None]).clamp(0, T - 1)
+    fresh = x.float()[torch.arange(B, device="cuda")[:, None, None], t].permute(0, 1, 3, 2, 4)  # [B,touched,HK,page,D]
+    fresh = fresh * newer[:, :, None, :, None]
+    mant, expo = torch.frexp(fresh.abs().amax((-1, -2)))
+    need = torch.where(mant <= 0.875, expo - 9, expo - 8).clamp(-100, 120)
+    need = torch.where(mant > 0, need, -100)
+    need = torch.ldexp(torch.ones_like(mant), need)
+    was = scales[at]                                                              # [B,touched,HK]
+    now = torch.where(older.any(-1)[:, :, None], torch.maximum(was, need), need)
+    there = codes[at]
+    stored = there if keys else there.transpose(-1, -2)
+    moved = stored.view(F8).float() * (was / now)[..., None, None]
+    value = torch.where(older[:, :, None, :, None], moved, fresh / now[..., None, None]).to(F8).view(torch.uint8)
+    merged = torch.where((older | newer)[:, :, None, :, None], value, stored)
+    write = inside & newer.any(-1)
+    codes[at[write]] = (merged if keys else merged.transpose(-1, -2))[write]
+    scales[at[write]] = now[write]
+    return codes.view(F8), scales
+
+
+def _plain_append(s):
+    kc, ks = _plain_append_one(s, s["k"], s["kc"], s["ks"], True)
+    vc, vs = _plain_append_one(s, s["v"], s["vc"], s["vs"], False)
+    return {"kc": kc, "ks": ks, "vc": vc, "vs": vs}
+
+
+def _plain_step(s):
+    c = s["c"]
+    B, T, H, HK, D, page = c["B"], c["T"], c["H"], c["HK"], c["D"], c["page"]
+    at = s["table"].long()
+    K = (s["kc"][at].view(F8).float() * s["ks"][at][..., None, None]).permute(0, 2, 1, 3, 4).reshape(B, HK, -1, D)
+    V = (s["vc"][at].view(F8).float() * s["vs"][at][..., None, None]).permute(0, 2, 3, 1, 4).reshape(B, HK, D, -1)
+    q = _grouped(s["q"], HK)
+    S = torch.matmul((q * s["scale"]).reshape(B, HK, -1, D), K.transpose(-1, -2)).view(B, HK, H // HK, T, -1)
+    i = s["cache_len"].view(B, 1, 1, 1, 1) + torch.arange(T, device="cuda")[:, None]
+    j = torch.arange(S.shape[-1], device="cuda")
+    seen = (j <= i) & (j > i - c["window"]) if c["window"] else j <= i
+    S = S.masked_fill_(~seen, -math.inf)
+    P = torch.exp_(S.sub_(S.amax(-1, keepdim=True)))
+    P = P.div_(P.sum(-1, keepdim=True))
+    o = torch.matmul(P.view(B, HK, -1, P.shape[-1]), V.transpose(-1, -2)).view(B, HK, H // HK, T, D)
+    return _heads(o, s["q"].dtype)
+
+
+def run(state):
+    s, c = state, state["c"]
+    if own:
+        from gated_delta_rule_82_amd import kda
+        if c["op"] == "rotary":
+            return kda.rotary(s["q"], s["k"], s["freqs"], s["pos"], scale=s["scale"], interleaved=c["interleaved"],
+                              inverse=c["inverse"])
+        if c["op"] == "attn_fwd":
+            return kda.attn_fwd(s["q"], s["k"], s["v"], scale=s["scale"], causal=c["causal"], window=c["window"],
+                                q_len=s["q_len"], kv_len=s["kv_len"])
+        if c["op"] == "attn_bwd":
+            return kda.attn_bwd(s["q"], s["k"], s["v"], s["o"], s["lse"], s["dout"], scale=s["scale"],
+                                causal=c["causal"], window=c["window"], q_len=s["q_len"], kv_len=s["kv_len"])
+        if c["op"] == "append":
+            kda.cache_append(s["k"], s["v"], s["kc"], s["vc"], s["ks"], s["vs"], s["table"], s["cache_len"])
+            return {"kc": s["kc"].view(F8), "ks": s["ks"], "vc": s["vc"].view(F8), "vs": s["vs"]}
+        return kda.attn_step(s["q"], s["kc"], s["vc"], s["ks"], s["vs"], s["table"], s["cache_len"], scale=s["scale"],
+                             window=c["window"])
+    return {"rotary": _plain_rotary, "attn_fwd": _plain_attn_fwd, "attn_bwd": _plain_attn_bwd, "append": _plain_append,
+            "step": _plain_step}[c["op"]](s)
+
+
+# ------------------------------------------------------------------ their work
+
+def _pairs(c):
+    """Visible (query, key) pairs of one head, over the batch."""
+    n = 0
+    for ql, kl in zip(*_attn_lengths(c)):
+        at = np.arange(ql, dtype=np.int64) + kl - ql
+        hi = np.minimum(at, kl - 1) if c["causal"] else np.full(ql, kl - 1)
+        lo = np.maximum(at - c["window"] + 1, 0) if c["window"] else np.zeros(ql, dtype=np.int64)
+        n += int(np.maximum(hi - lo + 1, 0).sum())
+    return n
+
+
+def work(case):
+    c, e = case, ESIZE[case["dtype"]]
+    if c["op"] == "rotary":
+        values = c["B"] * c["T"] * (c["H"] + c["HK"])
+        return {"bytes": 2 * values * c["D"] * e + c["B"] * c["T"] * 4, "flops": 3 * values * c["rot"]}
+    if c["op"] in ("attn_fwd", "attn_bwd"):
+        q, kv = c["B"] * c["Tq"] * c["H"] * c["D"] * e, c["B"] * c["Tk"] * c["HK"] * c["D"] * e
+        lse, pairs = c["B"] * c["H"] * c["Tq"] * 4, _pairs(c)
+        if c["op"] == "attn_fwd":
+            return {"bytes": 2 * q + 2 * kv + lse, "flops": 4 * c["D"] * c["H"] * pairs}
+        return {"bytes": 4 * q + 4 * kv + lse, "flops": 10 * c["D"] * c["H"] * pairs}
+    if c["op"] == "append":
+        values = 2 * c["B"] * c["T"] * c["HK"] * c["D"]
+        return {"bytes": values * (e + 1), "flops": 2 * values}
+    keys = sum((min(n, c["window"] + t - 1) if c["window"] else n) for n, t in ((b + t, t) for b, t in zip(*_lengths(c))))
+    return {"bytes": 2 * keys * c["HK"] * c["D"] + 2 * c["B"] * c["T"] * c["H"] * c["D"] * e,
+            "flops": 4 * c["D"] * c["H"] * c["T"] * keys}
+
+
+# ------------------------------------------------------------------ 64 bits
+
+def _exact_rotary(s):
+    """The pair (a, b) as a complex number times scale e^{i angle}."""
+    c, r = s["c"], s["c"]["rot"]
+    angle = s["pos"].double().unsqueeze(-1) * s["freqs"]
+    turn = torch.polar(torch.full_like(angle, s["scale"]), -angle if c["inverse"] else angle).unsqueeze(2)
+    out = []
+    for x in (s["q"].double(), s["k"].double()):
+        y = x.clone()
+        if c["interleaved"]:
+            y[..., :r] = torch.view_as_real(torch.view_as_complex(x[..., :r].reshape(*x.shape[:3], r // 2, 2).contiguous()) * turn).flatten(-2)
+        else:
+            z = torch.complex(x[..., :r // 2].contiguous(), x[..., r // 2:r].contiguous()) * turn
+            y[..., :r // 2], y[..., r // 2:r] = z.real, z.imag
+        out.append(y)
+    return tuple(out)
+
+
+def _exact_attn(s, backward):
+    """Sequence by sequence and head by head, only the tokens in use."""
+    c = s["c"]
+    ql, kl = _attn_lengths(c)
+    G = c["H"] // c["HK"]
+    q, k, v = s["q"].double(), s["k"].double(), s["v"].double()
+    o, dq, dk, dv = torch.zeros_like(q), torch.zeros_like(q), torch.zeros_like(k), torch.zeros_like(v)
+    lse = torch.full((c["B"], c["H"], c["Tq"]), -math.inf, dtype=torch.float64, device="cuda")
+    for b in range(c["B"]):
+        nq, nk = ql[b], kl[b]
+        at = torch.arange(nq, device="cuda").unsqueeze(1) + (nk - nq)
+        j = torch.arange(nk, device="cuda").unsqueeze(0)
+        hidden = torch.zeros(nq, nk, dtype=torch.bool, device="cuda")
+        if c["causal"]:
+            hidden |= j > at
+        if c["window"]:
+            hidden |= j <= at - c["window"]
+        alive = ~hidden.all(1)
+        for h in range(c["H"]):
+            K, V = k[b, :nk, h // G], v[b, :nk, h // G]
+            x = (q[b, :nq, h] @ K.T) * s["scale"]
+            x[hidden] = -math.inf
+            z = torch.logsumexp(x, 1)
+            lse[b, h, :nq] = z
+            p = torch.exp(x - z.masked_fill(~alive, 0.0).unsqueeze(1))
+            if not backward:
+                o[b, :nq, h] = p @ V
+                continue
+            do = s["dout"][b, :nq, h].double()
+            dv[b, :nk, h // G] += p.T @ do
+            dp = do @ V.T
+            dx = p * (dp - (p * dp).sum(1, keepdim=True)) * s["scale"]
+            dq[b, :nq, h] = dx @ K
+            dk[b, :nk, h // G] += dx.T @ q[b, :nq, h]
+    return {"dq": dq, "dk": dk, "dv": dv} if backward else (o, lse)
+
+
+def _to_e4m3(x):
+    """x in 64 bits rounded to the nearest value of 1 sign, 4 exponent and 3 mantissa bits, ties to the even one."""
+    e = torch.floor(torch.log2(x.abs().clamp(min=2.0 ** -7))).clamp(min=-6.0)
+    step = torch.exp2(e - 3.0)
+    return (torch.round(x / step) * step).clamp(-448.0, 448.0)
+
+
+def _exact_append(s):
+    c = s["c"]
+    page, table, before = c["page"], s["table"].tolist(), s["cache_len"].tolist()
+    out = {}
+    for n, codes, scales in (("k", s["kc"], s["ks"]), ("v", s["vc"].transpose(-1, -2), s["vs"])):
+        val, sc = codes.contiguous().view(F8).double(), scales.double()
+        x = s[n].double()
+        for b in range(c["B"]):
+            first, last = before[b], before[b] + c["T"]
+            for p in range(first // page, -(-last // page)):
+                lo, hi = max(first, p * page), min(last, (p + 1) * page)
+                if p >= len(table[b]) or lo >= hi:
+                    continue
+                at, new = table[b][p], x[b, lo - first:hi - first].transpose(0, 1)       # [HK,n,D]
+                top = new.abs().amax((1, 2))
+                e = torch.ceil(torch.log2(top / 448.0)).clamp(-100, 120)
+                e = torch.where(top > 448.0 * torch.exp2(e), e + 1, torch.where(top <= 448.0 * torch.exp2(e - 1), e - 1, e))
+                need = torch.exp2(e.nan_to_num(neginf=-100.0).clamp(-100, 120))
+                old = lo - p * page
+                now = torch.maximum(sc[at], need) if old else need
+                val[at, :, :old] = _to_e4m3(val[at, :, :old] * (sc[at] / now)[:, None, None])
+                val[at, :, old:hi - p * page] = _to_e4m3(new / now[:, None, None])
+                sc[at] = now
+        out[n + "c"], out[n + "s"] = val if n == "k" else val.transpose(-1, -2).contiguous(), sc
+    return out
+
+
+def _exact_step(s):
+    c = s["c"]
+    G, page = c["H"] // c["HK"], c["page"]
+    before, table = s["cache_len"].tolist(), s["table"].long()
+    o = torch.zeros(s["q"].shape, dtype=torch.float64, device="cuda")
+    for b in range(c["B"]):
+        n = before[b] + c["T"]
+        at = table[b, :-(-n // page)]
+        K = s["kc"][at].view(F8).double() * s["ks"][at].double()[:, :, None, None]
+        V = s["vc"][at].view(F8).double() * s["vs"][at].double()[:, :, None, None]
+        K = K.transpose(0, 1).reshape(c["HK"], -1, c["D"])[:, :n]
+        V = V.permute(1, 0, 3, 2).reshape(c["HK"], -1, c["D"])[:, :n]
+        x = torch.einsum("thgd,hnd->hgtn", s["q"][b].double().view(c["T"], c["HK"], G, c["D"]), K) * s["scale"]
+        i = before[b] + torch.arange(c["T"], device="cuda").unsqueeze(1)
+        j = torch.arange(n, device="cuda").unsqueeze(0)
+        x[..., (j > i) | ((j <= i - c["window"]) if c["window"] else (j < 0))] = -math.inf
+        o[b] = torch.einsum("hgtn,hnd->thgd", torch.softmax(x, -1), V).reshape(c["T"], c["H"], c["D"])
+    return o
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    if case["op"] == "rotary":
+        return _exact_rotary(s)
+    if case["op"] in ("attn_fwd", "attn_bwd"):
+        return _exact_attn(s, case["op"] == "attn_bwd")
+    return _exact_append(s) if case["op"] == "append" else _exact_step(s)
