@@ -181,7 +181,7 @@ def prepare(case, seed):
                  kv_len=_ints(kl) if c["ragged"] else None)
         if c["op"] == "attn_bwd":
             s["dout"] = _normal(g, (c["B"], c["Tq"], c["H"], c["D"]), c["dtype"])
-            s["o"], s["lse"] = _plain_attn_fwd(s)  # what the forward pass left
+            s["o"], s["lse"] = (x.contiguous() for x in _plain_attn_fwd(s))  # what the forward pass left
     elif c["op"] == "append":
         s["kc"], s["vc"], s["ks"], s["vs"], s["table"] = _cache(c, g)
         before, new = _lengths(c)
