@@ -9,6 +9,9 @@
 
 #include "../../include/kda.h"
 #include "kda_bwd.h"
+#include "kda_validate.h"
+
+using namespace kda::host;
 
 namespace {
 
@@ -17,15 +20,10 @@ constexpr double kF32Max = 3.4028234663852886e38;
 constexpr double kHeadroom = 1024.0;
 constexpr int kFactorTile = 16;  // token tile of the factored decay products
 
-bool dim_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool dtype_ok(kda_dtype dt) { return dt == KDA_F32 || dt == KDA_BF16; }
 // known bits only; the v1 gate selects the form of the in-kernel gate
 bool flags_ok(unsigned f) {
     return (f & ~15u) == 0 && (!(f & KDA_GATE_SOFTPLUS) || (f & KDA_GATE_IN_KERNEL));
 }
-int elem_bytes(kda_dtype dt) { return dt == KDA_BF16 ? 2 : 4; }
-
 bool gmin_ok(float g_min) { return isfinite(g_min) && g_min < 0.0f; }
 // the bound g_min is used by the bounded in-kernel gate only
 bool gate_ok(float g_min, unsigned f) {
@@ -41,33 +39,7 @@ bool wide_decay(float g_min, unsigned f, kda_dtype dt) {
     return kda_safe_chunk_size(g_min, dt) < kFactorTile;
 }
 
-// Checks a pointer that must be present; optional ones pass when NULL.
-kda_status need(const void* p) {
-    if (!p) return KDA_ERR_NULL;
-    return aligned16(p) ? KDA_OK : KDA_ERR_ALIGN;
-}
-kda_status maybe(const void* p) { return (!p || aligned16(p)) ? KDA_OK : KDA_ERR_ALIGN; }
-
-// Sizes the kernels index with 32-bit arithmetic: at most 2^24 (b, h) pairs,
-// 2^30 tokens and 2^46 / 128 token rows.
-bool sizes_ok(long long B, long long T, long long H) {
-    if (B < 0 || T < 0 || H < 0) return false;
-    const unsigned long long bh = (unsigned long long)B * (unsigned long long)H;
-    return bh <= (1ull << 24) && T <= (1ll << 30) && bh * (unsigned long long)T * 128ull <= (1ull << 46);
-}
 int chunks_of(int T, int chunk) { return (int)(((long long)T + chunk - 1) / chunk); }
-
-// Byte ranges [a, a + na) and [b, b + nb) share a byte (both non-empty).
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return na > 0 && nb > 0 && x < y + nb && y < x + na;
-}
-
-#define KDA_TRY(expr)                        \
-    do {                                     \
-        const kda_status st_ = (expr);       \
-        if (st_ != KDA_OK) return st_;       \
-    } while (0)
 
 }  // namespace
 
@@ -533,6 +505,7 @@ const char* kda_status_string(kda_status s) {
         case KDA_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
         case KDA_ERR_HIP: return "kernel launch failed";
         case KDA_ERR_SCRATCH: return "the sizes need more than the built-in scratch of kda_chunk_fwd_noalloc";
+        case KDA_ERR_SCALE: return "a scale is not finite or not positive";
     }
     return "unknown status";
 }

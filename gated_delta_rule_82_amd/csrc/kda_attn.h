@@ -1,0 +1,109 @@
+// kda_attn.h - argument blocks and launchers of the softmax-attention operators.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace kda {
+
+// n / d for 0 <= n < 2^31 as a multiply and a shift: with s = ceil(log2 d) and
+// m = floor(2^32 (2^s - d) / d) + 1, n / d = (mulhi(n, m) + n) >> s.
+struct FastDiv {
+    uint32_t d, m, s;
+};
+inline FastDiv fast_div(uint32_t d) {
+    FastDiv f{d, 0, 0};
+    while ((1ull << f.s) < d) ++f.s;
+    f.m = (uint32_t)(((1ull << 32) * ((1ull << f.s) - d)) / d + 1);
+    return f;
+}
+
+struct RotaryArgs {
+    const void* q; const void* k; void* q_out; void* k_out;
+    const int* positions; const double* inv_freq;
+    size_t ldq, ldk, ldqo, ldko;   // elements between tokens
+    size_t tokens;                 // B * T
+    int T, H, HK, D, rot;
+    float scale;
+    int interleaved, inverse;
+};
+hipError_t launch_rotary(int dt, const RotaryArgs& a, hipStream_t s);
+
+// The G query heads of a key/value head and their tokens are the packed rows
+// r = t * G + g of one problem, 0 <= r < G * Tq, so a tile of rows shares the
+// keys and values it streams.
+struct AttnArgs {
+    const void* q; const void* k; const void* v;
+    const int* q_len; const int* kv_len;      // nullable
+    void* o; float* lse;
+    const void* dout; void* dq; void* dk; void* dv;
+    float* rows;                // backward: (lse log2 e, dout . o) of each packed row
+    float* part_o; float* part_ml;  // split key axis: partial outputs and (maximum, sum)
+    int B, Tq, Tk, H, HK, G;
+    size_t ldq, ldk, ldv;       // elements between tokens
+    float scale, scale_log2;    // scale, scale * log2 e
+    int causal, window;         // window 0: none
+    int nsplit;
+    FastDiv divG;
+};
+// Packed rows of a wave (16-row column blocks: two in bf16, one in fp32), and
+// waves of a workgroup: as many as the rows of a key/value head fill.
+constexpr int attn_rows_per_wave(int elem_bytes) { return elem_bytes == 2 ? 32 : 16; }
+inline int attn_waves(long long rows, int per_wave) { return rows <= per_wave ? 1 : rows <= 2 * per_wave ? 2 : 4; }
+// Workgroups over the key axis (1: not split).  Two workgroups per compute unit
+// fill the card; a split takes at least 512 keys, so that its partial output
+// stays small beside the keys it reads.
+inline int attn_fwd_splits(int elem_bytes, int B, int Tq, int Tk, int HK, int G) {
+    const long long rows = (long long)Tq * G, per = attn_rows_per_wave(elem_bytes);
+    const long long bq = per * attn_waves(rows, (int)per), wgs = (long long)B * HK * ((rows + bq - 1) / bq);
+    const long long want = wgs > 0 ? 512 / wgs : 1, most = Tk / 512, n = want < most ? want : most;
+    return n < 1 ? 1 : n > 64 ? 64 : (int)n;
+}
+hipError_t launch_attn_fwd(int dt, int D, const AttnArgs& a, hipStream_t s);
+// Packed rows of one key/value head in the backward's row array.
+constexpr int kAttnRowPad = 64;
+hipError_t launch_attn_bwd(int dt, int D, const AttnArgs& a, hipStream_t s);
+
+struct AppendArgs {
+    const void* k; const void* v;
+    uint8_t* k_cache; uint8_t* v_cache; float* k_scale; float* v_scale;
+    const int* block_table; const int* cache_len; const int* new_len;
+    int n_pages, max_pages, B, T, HK, page;
+    size_t ldk, ldv;
+};
+hipError_t launch_cache_append(int dt, int D, const AppendArgs& a, hipStream_t s);
+
+struct AttnStepArgs {
+    const void* q; const uint8_t* k_cache; const uint8_t* v_cache; const float* k_scale; const float* v_scale;
+    const int* block_table; const int* cache_len; const int* new_len;
+    void* o; float* part_o; float* part_ml;
+    int n_pages, max_pages, B, Tq, H, HK, G, page, window, nsplit;
+    size_t ldq;
+    float scale_log2;
+    FastDiv divG;
+};
+// 16-row blocks of a workgroup.
+inline int attn_step_row_blocks(long long rows) { return rows <= 16 ? 1 : 2; }
+// Workgroups over a cache of max_len tokens.  Four workgroups of four waves per
+// compute unit keep enough loads in flight; a split takes at least 256 keys (one
+// block for each wave).
+inline int attn_step_splits(int B, int Tq, int HK, int G, int max_len) {
+    const long long rows = (long long)Tq * G, br = 16 * attn_step_row_blocks(rows);
+    const long long wgs = (long long)B * HK * ((rows + br - 1) / br);
+    const long long want = wgs > 0 ? 1024 / wgs : 1, most = max_len / 256, n = want < most ? want : most;
+    return n < 1 ? 1 : n > 128 ? 128 : (int)n;
+}
+hipError_t launch_attn_step(int dt, int D, const AttnStepArgs& a, hipStream_t s);
+
+// Joins the partial results of a split key axis: for packed row r of (b, hk),
+// part_o [split][B*HK][rows][D] and part_ml [split][B*HK][rows][2] hold the
+// unnormalised output, the maximum (log2 units) and the sum.
+struct JoinArgs {
+    const float* part_o; const float* part_ml; void* o; float* lse;  // lse nullable
+    int nsplit, B, Tq, H, HK, G;
+    FastDiv divG;
+};
+hipError_t launch_attn_join(int dt, int D, const JoinArgs& a, hipStream_t s);
+
+}  // namespace kda

@@ -1,0 +1,172 @@
+// kda_attn_device.h - device-side building blocks of the attention kernels.
+//
+// Tiles of token rows live in LDS as rows of D elements, cut into granules of 16
+// bytes; granule c of row r is at position c ^ (attn_swz(r) mod granules), so
+// both ways a tile is read spread over the banks:
+//   * row fragments (a lane reads 8 consecutive elements of its row): eight
+//     consecutive rows hit eight different granule positions;
+//   * column fragments (bf16: four rows by 16 columns per 16 lanes through the
+//     transposing LDS read): four consecutive rows hit four different pairs.
+// Contraction slots: row fragments hold elements 32 s + 8 (l / 16) + j of their
+// row in slot j (any map serves as long as both operands share it), column
+// fragments rows slot_index(l / 16, j), the map of frag_from_c, so that score
+// tiles go from the accumulator into the next product without moving.
+#pragma once
+
+#include "kda_attn.h"
+#include "kda_device.h"
+
+namespace kda {
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNegInf = -__builtin_inff();
+
+__device__ __forceinline__ uint32_t fdiv(uint32_t n, const FastDiv& f) { return (__umulhi(n, f.m) + n) >> f.s; }
+
+__device__ __forceinline__ int attn_swz(int row) { return ((row & 3) << 1) | ((row >> 2) & 1) | (row & 8); }
+
+// Maximum / sum over the four lane groups that share lane % 16, on the vector
+// unit (half-row swaps) rather than through LDS.
+__device__ __forceinline__ float group_max4(float x) {
+    const uint32_t u = __float_as_uint(x);
+    const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const float y = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const uint32_t w = __float_as_uint(y);
+    const auto b = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float group_add4(float x) {
+    const uint32_t u = __float_as_uint(x);
+    const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const float y = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const uint32_t w = __float_as_uint(y);
+    const auto b = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// Number of valid elements of sequence b, clamped to the tensor's range.
+__device__ __forceinline__ int seq_len(const int* len, int b, int most) {
+    if (!len) return most;
+    const int n = len[b];
+    return n < 0 ? 0 : n > most ? most : n;
+}
+
+// Where a tile of packed rows starts and which keys its rows can see.
+struct RowRange {
+    int t_first, t_last;   // tokens of the first and last row (t_last < q_len)
+    int key_lo, key_hi;    // keys seen by some row: [key_lo, key_hi)
+};
+
+__device__ __forceinline__ RowRange row_range(const AttnArgs& a, int r0, int r1, int ql, int kl) {
+    RowRange x;
+    x.t_first = (int)fdiv((uint32_t)r0, a.divG);
+    x.t_last = min((int)fdiv((uint32_t)(r1 - 1), a.divG), ql - 1);
+    const int off = kl - ql;
+    x.key_hi = a.causal ? min(kl, x.t_last + off + 1) : kl;
+    x.key_lo = a.window ? max(0, x.t_first + off - a.window + 1) : 0;
+    if (x.t_first >= ql || x.key_hi < x.key_lo) x.key_hi = x.key_lo;
+    return x;
+}
+
+template <typename T, int D> struct TileGeom {
+    static constexpr int GR = D * (int)sizeof(T) / 16;      // granules per row
+    static constexpr int NS = (D + 31) / 32;                // contraction steps over a row
+    static constexpr int ND = D / 16;                       // 16-channel blocks
+};
+
+// Copy ROWS rows of D elements into an LDS tile straight from memory (one wave
+// instruction moves 64 granules); row_ptr(r) gives the address of row r of the
+// tile, which must be readable for every r (callers clamp).
+template <typename T, int D, int ROWS, int NW, typename RowPtr>
+__device__ __forceinline__ void stage_rows(unsigned char* tile, int wave, int lane, RowPtr row_ptr) {
+    constexpr int GR = TileGeom<T, D>::GR, N = ROWS * GR / 64;
+    static_assert(ROWS * GR % 64 == 0, "whole wave instructions");
+#pragma unroll
+    for (int c = 0; c < (N + NW - 1) / NW; ++c) {
+        const int piece = c * NW + wave;
+        if (N % NW == 0 || piece < N) {
+            const int idx = piece * 64 + lane, row = idx / GR, pos = idx % GR;
+            const unsigned char* src = reinterpret_cast<const unsigned char*>(row_ptr(row)) +
+                                       (size_t)((pos ^ (attn_swz(row) & (GR - 1))) * 16);
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                             (__attribute__((address_space(3))) void*)(tile + piece * 1024), 16, 0, 0);
+        }
+    }
+}
+
+// Row fragment of rows [r0, r0 + 16) for contraction step s.
+template <int D>
+__device__ __forceinline__ Frag<bf16_t> row_frag(const unsigned char* tile, int r0, int s, int lane, bf16_t) {
+    constexpr int GR = TileGeom<bf16_t, D>::GR;
+    const int row = r0 + (lane & 15), g = lane >> 4;
+    Frag<bf16_t> f;
+    if constexpr (D >= 32) {
+        f.v = *reinterpret_cast<const bf16x8*>(tile + row * (D * 2) + (((4 * s + g) ^ (attn_swz(row) & (GR - 1))) * 16));
+    } else {
+        f.v = *reinterpret_cast<const bf16x8*>(tile + row * (D * 2) + (((g & 1) ^ (attn_swz(row) & (GR - 1))) * 16));
+        if (g >= 2) f.zero();  // 16 channels fill half a step
+    }
+    return f;
+}
+template <int D>
+__device__ __forceinline__ Frag<float> row_frag(const unsigned char* tile, int r0, int s, int lane, float) {
+    constexpr int GR = TileGeom<float, D>::GR;
+    const int row = r0 + (lane & 15), g = lane >> 4, x = attn_swz(row) & (GR - 1);
+    const int c = D >= 32 ? 8 * s + 2 * g : 2 * (g & 1);
+    const unsigned char* p = tile + row * (D * 4);
+    const float4 a = *reinterpret_cast<const float4*>(p + ((c ^ x) * 16));
+    const float4 b = *reinterpret_cast<const float4*>(p + (((c + 1) ^ x) * 16));
+    Frag<float> f;
+    f.v[0] = a.x; f.v[1] = a.y; f.v[2] = a.z; f.v[3] = a.w;
+    f.v[4] = b.x; f.v[5] = b.y; f.v[6] = b.z; f.v[7] = b.w;
+    if (D < 32 && g >= 2) f.zero();
+    return f;
+}
+
+// The same fragment straight from a row in memory (p: the row's first element).
+template <typename T, int D>
+__device__ __forceinline__ Frag<T> row_frag_global(const T* p, int s, int lane) {
+    const int g = lane >> 4;
+    Frag<T> f;
+    if constexpr (D >= 32) {
+        frag_load_row8(f, p + 32 * s + 8 * g);
+    } else {
+        frag_load_row8(f, p + 8 * (g & 1));
+        if (g >= 2) f.zero();
+    }
+    return f;
+}
+
+// Column fragment: column 16 c + l % 16 of the 32 rows from r0.
+template <int D>
+__device__ __forceinline__ Frag<bf16_t> col_frag(const unsigned char* tile, int r0, int c, int lane, bf16_t) {
+    constexpr int GR = TileGeom<bf16_t, D>::GR;
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef s16x4 __attribute__((address_space(3)))* lds4;
+    const int row = r0 + 4 * (lane >> 4) + ((lane >> 2) & 3), i = lane & 3;
+    // lane i of a 16-lane group loads 4 columns of row i / 4 and receives column i of the four rows
+    const int off = row * (D * 2) + (((2 * c + (i >> 1)) ^ (attn_swz(row) & (GR - 1))) * 16) + (i & 1) * 8;
+    const int row2 = row + 16;
+    const int off2 = row2 * (D * 2) + (((2 * c + (i >> 1)) ^ (attn_swz(row2) & (GR - 1))) * 16) + (i & 1) * 8;
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(tile + off));
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(tile + off2));
+    typedef short s16x8 __attribute__((ext_vector_type(8)));
+    Frag<bf16_t> f;
+    f.v = __builtin_bit_cast(bf16x8, s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
+    return f;
+}
+template <int D>
+__device__ __forceinline__ Frag<float> col_frag(const unsigned char* tile, int r0, int c, int lane, float) {
+    constexpr int GR = TileGeom<float, D>::GR;
+    const int col = 16 * c + (lane & 15), g = lane >> 4;
+    Frag<float> f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int row = r0 + slot_index(g, j);
+        f.v[j] = *reinterpret_cast<const float*>(tile + row * (D * 4) +
+                                                 (((col >> 2) ^ (attn_swz(row) & (GR - 1))) * 16) + (col & 3) * 4);
+    }
+    return f;
+}
+
+}  // namespace kda

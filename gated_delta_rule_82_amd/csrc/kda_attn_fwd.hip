@@ -1,0 +1,285 @@
+// kda_attn_fwd.hip - softmax attention forward on gfx950.
+//
+//   o_i = sum_j exp(c q_i.k_j - m_i) v_j / sum_j exp(c q_i.k_j - m_i)
+//
+// One pass over the keys with a running maximum and sum.  A wave owns 16 NQ
+// packed rows (see kda_attn.h) as the COLUMNS of its products: S^T = K Q^T puts
+// a row's scores into one lane column, so the maximum needs two lane swaps, the
+// rescale is one factor per lane, and the exponentials are, as they stand, the
+// right operand of O^T += V^T P^T.  Keys and values go through a two-deep LDS
+// ring filled by direct loads while the previous tile is used.
+#include "kda_attn_device.h"
+
+namespace kda {
+
+// T: element type; D: head dimension; NQ: 16-row column blocks of a wave; KB:
+// keys per tile; NW: waves.
+template <typename T, int D, int NQ, int KB, int NW>
+__global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void kda_attn_fwd_kernel(const AttnArgs a) {
+    typedef TileGeom<T, D> G_;
+    constexpr int NS = G_::NS, ND = G_::ND, NT = KB / 16, BQ = 16 * NQ * NW;
+    constexpr int kTile = KB * D * (int)sizeof(T);
+    __shared__ __attribute__((aligned(16))) unsigned char sm[2][2][kTile];
+
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4;
+    // head fastest: the tiles of one key/value head run on one XCD when the
+    // heads are a multiple of 8; late rows (the longest under a causal mask) first
+    const int nbh = a.B * a.HK, rows = a.Tq * a.G;
+    const int ntile = (rows + BQ - 1) / BQ;
+    int bid = blockIdx.x;
+    const int bh = bid % nbh;
+    bid /= nbh;
+    const int split = bid % a.nsplit;
+    const int tile = ntile - 1 - bid / a.nsplit;
+    const int b = bh / a.HK, hk = bh % a.HK;
+    const int ql = seq_len(a.q_len, b, a.Tq), kl = seq_len(a.kv_len, b, a.Tk), off = kl - ql;
+    const int r0 = tile * BQ, r1 = min(r0 + BQ, rows);
+    const RowRange blk = row_range(a, r0, r1, ql, kl);
+    int k_beg = blk.key_lo / KB, k_end = (blk.key_hi + KB - 1) / KB;  // tiles of KB keys
+    if (blk.key_hi <= blk.key_lo) k_end = k_beg;
+    if (a.nsplit > 1) {
+        const int per = (k_end - k_beg + a.nsplit - 1) / a.nsplit;
+        k_beg = min(k_end, k_beg + split * per);
+        k_end = min(k_end, k_beg + per);
+    }
+
+    // this wave's rows
+    const int w0 = r0 + wave * 16 * NQ;
+    const RowRange mine = w0 < r1 ? row_range(a, w0, min(w0 + 16 * NQ, r1), ql, kl) : RowRange{0, -1, 0, 0};
+    // every row of the wave sees the keys in [all_lo, all_hi)
+    const int all_hi = a.causal ? min(kl, mine.t_first + off + 1) : kl;
+    const int all_lo = a.window ? mine.t_last + off - a.window + 1 : 0;
+    int t[NQ], lo[NQ], hi[NQ];   // token, first and last key of this lane's rows
+    Frag<T> qf[NQ][NS];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+        const int r = min(w0 + 16 * n + (lane & 15), rows - 1);
+        t[n] = (int)fdiv((uint32_t)r, a.divG);
+        const int h = hk * a.G + (r - t[n] * a.G), p = t[n] + off;
+        hi[n] = a.causal ? min(kl - 1, p) : kl - 1;
+        lo[n] = a.window ? p - a.window + 1 : 0;
+        // rows past q_len are computed on the last valid token's values and dropped
+        const int tr = max(min(t[n], ql - 1), 0);
+        const T* qp = reinterpret_cast<const T*>(a.q) + ((size_t)b * a.Tq + tr) * a.ldq + (size_t)h * D;
+#pragma unroll
+        for (int s = 0; s < NS; ++s) qf[n][s] = row_frag_global<T, D>(qp, s, lane);
+    }
+
+    const T* kbase = reinterpret_cast<const T*>(a.k) + (size_t)b * a.Tk * a.ldk + (size_t)hk * D;
+    const T* vbase = reinterpret_cast<const T*>(a.v) + (size_t)b * a.Tk * a.ldv + (size_t)hk * D;
+    auto stage = [&](int kt, int buf) {
+        // keys past the length repeat the last one (their scores are masked)
+        stage_rows<T, D, KB, NW>(sm[buf][0], wave, lane, [&](int r) { return kbase + (size_t)min(kt * KB + r, kl - 1) * a.ldk; });
+        stage_rows<T, D, KB, NW>(sm[buf][1], wave, lane, [&](int r) { return vbase + (size_t)min(kt * KB + r, kl - 1) * a.ldv; });
+    };
+
+    const float c = a.scale_log2;
+    float m[NQ], l[NQ];
+    floatx4 o[ND][NQ];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+        m[n] = kNegInf;
+        l[n] = 0.f;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) o[d][n] = floatx4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    if (k_beg < k_end) stage(k_beg, 0);
+    for (int kt = k_beg; kt < k_end; ++kt) {
+        const int buf = (kt - k_beg) & 1, k0 = kt * KB;
+        wait_vmcnt<0>();
+        lds_barrier();  // tile kt has landed; every wave is done with the other buffer
+        if (kt + 1 < k_end) stage(kt + 1, buf ^ 1);
+        if (k0 >= mine.key_hi || k0 + KB <= mine.key_lo) continue;  // nothing for this wave's rows
+        const unsigned char* ks = sm[buf][0];
+        const unsigned char* vs = sm[buf][1];
+
+        floatx4 st[NT][NQ];
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) st[i][n] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                const Frag<T> kf = row_frag<D>(ks, 16 * i, s, lane, T());
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) st[i][n] = mma(kf, qf[n][s], st[i][n]);
+            }
+        if (k0 < all_lo || k0 + KB > all_hi) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = k0 + 16 * i + 4 * g + e;
+                        st[i][n][e] = key >= lo[n] && key <= hi[n] ? st[i][n][e] : kNegInf;
+                    }
+        }
+        bool grew = false;
+        float mu[NQ], alpha[NQ];
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+            float x = kNegInf;
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x = fmaxf(x, st[i][n][e]);
+            x = fmaxf(m[n], group_max4(x) * c);
+            mu[n] = x == kNegInf ? 0.f : x;  // a row that has seen nothing yet
+            alpha[n] = exp2_fast(m[n] - mu[n]);
+            grew |= x > m[n];
+            m[n] = x;
+        }
+        if (__any(grew)) {
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+                l[n] *= alpha[n];
+#pragma unroll
+                for (int d = 0; d < ND; ++d) o[d][n] *= alpha[n];
+            }
+        }
+        // bf16 probabilities are rounded for the product (2^-9 relative each, as
+        // the values beside them); the sum is over the unrounded ones
+        Frag<T> pf[NT / 2][NQ];
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    st[i][n][e] = exp2_fast(fmaf(st[i][n][e], c, -mu[n]));
+                    l[n] += st[i][n][e];
+                }
+#pragma unroll
+            for (int i = 0; i < NT / 2; ++i) pf[i][n] = frag_from_c<T>(st[2 * i][n], st[2 * i + 1][n]);
+        }
+#pragma unroll
+        for (int i = 0; i < NT / 2; ++i)
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+                const Frag<T> vf = col_frag<D>(vs, 32 * i, d, lane, T());
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) o[d][n] = mma(vf, pf[i][n], o[d][n]);
+            }
+    }
+
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+        const int r = w0 + 16 * n + (lane & 15);
+        const float sum = group_add4(l[n]);
+        if (r >= r1) continue;
+        if (a.nsplit > 1) {
+            const size_t row = ((size_t)split * nbh + bh) * rows + r;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) store4(a.part_o + row * D + 16 * d + 4 * g, o[d][n]);
+            // a NaN sum takes part whatever the other parts' maxima are
+            const float top = sum != sum ? -kNegInf : m[n];
+            if (g == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * row) = t[n] < ql ? make_float2(top, sum) : make_float2(kNegInf, 0.f);
+        } else {
+            const int h = hk * a.G + (r - t[n] * a.G);
+            const float inv = 1.f / sum;
+            const bool some = t[n] < ql && sum != 0.f;
+            T* op = reinterpret_cast<T*>(a.o) + (((size_t)b * a.Tq + t[n]) * a.H + h) * D;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+                const floatx4 y = o[d][n] * inv;
+                store4(op + 16 * d + 4 * g, some ? y : floatx4{0.f, 0.f, 0.f, 0.f});
+            }
+            if (a.lse && g == 0)
+                a.lse[((size_t)b * a.H + h) * a.Tq + t[n]] =
+                    some ? (m[n] + __builtin_amdgcn_logf(sum)) * kLn2 : kNegInf;
+        }
+    }
+}
+
+// A thread takes four channels of one packed row over all splits.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void kda_attn_join_kernel(const JoinArgs a) {
+    constexpr int L = D / 4;
+    const int rows = a.Tq * a.G;
+    const size_t n = (size_t)a.B * a.HK * rows, at = ((size_t)blockIdx.x * 256 + threadIdx.x) / L;
+    const int d = (threadIdx.x % L) * 4;
+    if (at >= n) return;
+    const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
+    float m = kNegInf;
+    for (int s = 0; s < a.nsplit; ++s) m = fmaxf(m, ml[s * n + at].x);
+    const float mu = m == kNegInf ? 0.f : m;
+    float sum = 0.f;
+    floatx4 o = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < a.nsplit; ++s) {
+        const float2 x = ml[s * n + at];
+        const float w = exp2_fast(x.x - mu);
+        if (w == 0.f) continue;  // a part that saw nothing (its output is not read)
+        sum = fmaf(w, x.y, sum);
+        o += w * *reinterpret_cast<const floatx4*>(a.part_o + (s * n + at) * D + d);
+    }
+    const int r = (int)(at % rows), bh = (int)(at / rows), b = bh / a.HK, hk = bh % a.HK;
+    const int t = (int)fdiv((uint32_t)r, a.divG), h = hk * a.G + (r - t * a.G);
+    const float inv = 1.f / sum;
+    store4(reinterpret_cast<T*>(a.o) + (((size_t)b * a.Tq + t) * a.H + h) * D + d, sum == 0.f ? o : o * inv);
+    if (a.lse && d == 0)
+        a.lse[((size_t)b * a.H + h) * a.Tq + t] = sum == 0.f ? kNegInf : (m + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
+template <typename T, int D>
+static hipError_t launch_join_t(const JoinArgs& a, hipStream_t s) {
+    const size_t threads = (size_t)a.B * a.HK * a.Tq * a.G * (D / 4);
+    hipLaunchKernelGGL((kda_attn_join_kernel<T, D>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+template <typename T>
+static hipError_t launch_join_d(int D, const JoinArgs& a, hipStream_t s) {
+    switch (D) {
+        case 16: return launch_join_t<T, 16>(a, s);
+        case 32: return launch_join_t<T, 32>(a, s);
+        case 64: return launch_join_t<T, 64>(a, s);
+        case 128: return launch_join_t<T, 128>(a, s);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+hipError_t launch_attn_join(int dt, int D, const JoinArgs& a, hipStream_t s) {
+    return dt == 1 ? launch_join_d<bf16_t>(D, a, s) : launch_join_d<float>(D, a, s);
+}
+
+template <typename T, int D, int NQ, int KB, int NW>
+static hipError_t launch_fwd_n(const AttnArgs& a, hipStream_t s) {
+    constexpr int BQ = 16 * NQ * NW;
+    const long long rows = (long long)a.Tq * a.G, tiles = (rows + BQ - 1) / BQ;
+    hipLaunchKernelGGL((kda_attn_fwd_kernel<T, D, NQ, KB, NW>), dim3((unsigned)(tiles * a.B * a.HK * a.nsplit)), dim3(64 * NW), 0, s, a);
+    return hipGetLastError();
+}
+
+template <typename T, int D>
+static hipError_t launch_fwd_t(const AttnArgs& a, hipStream_t s) {
+    constexpr int NQ = attn_rows_per_wave(sizeof(T)) / 16, KB = sizeof(T) == 2 ? 64 : 32;
+    const long long rows = (long long)a.Tq * a.G;
+    const int nw = attn_waves(rows, 16 * NQ);
+    hipError_t e = nw == 1 ? launch_fwd_n<T, D, NQ, KB, 1>(a, s)
+                   : nw == 2 ? launch_fwd_n<T, D, NQ, KB, 2>(a, s)
+                             : launch_fwd_n<T, D, NQ, KB, 4>(a, s);
+    if (e != hipSuccess || a.nsplit == 1) return e;
+    JoinArgs j{a.part_o, a.part_ml, a.o, a.lse, a.nsplit, a.B, a.Tq, a.H, a.HK, a.G, a.divG};
+    return launch_attn_join(sizeof(T) == 2 ? 1 : 0, D, j, s);
+}
+
+template <typename T>
+static hipError_t launch_fwd_d(int D, const AttnArgs& a, hipStream_t s) {
+    switch (D) {
+        case 16: return launch_fwd_t<T, 16>(a, s);
+        case 32: return launch_fwd_t<T, 32>(a, s);
+        case 64: return launch_fwd_t<T, 64>(a, s);
+        case 128: return launch_fwd_t<T, 128>(a, s);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+hipError_t launch_attn_fwd(int dt, int D, const AttnArgs& a, hipStream_t s) {
+    return dt == 1 ? launch_fwd_d<bf16_t>(D, a, s) : launch_fwd_d<float>(D, a, s);
+}
+
+}  // namespace kda

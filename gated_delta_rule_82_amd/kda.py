@@ -8,6 +8,7 @@ an exception is raised.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -27,6 +28,8 @@ EXPORTS = (
     "kda_layer_fwd", "kda_step", "kda_chunk_fwd_grouped", "kda_step_grouped",
     "kda_segment_compose", "kda_segment_fixup", "kda_short_conv", "kda_output_gate",
     "kda_chunk_bwd_workspace", "kda_chunk_bwd", "kda_chunk_bwd_grouped_workspace", "kda_chunk_bwd_grouped",
+    "kda_rotary_freqs", "kda_rotary", "kda_attn_fwd_workspace", "kda_attn_fwd", "kda_attn_bwd_workspace",
+    "kda_attn_bwd", "kda_cache_append", "kda_attn_step_workspace", "kda_attn_step",
     "kda_status_string",
 )
 
@@ -89,6 +92,25 @@ def load() -> ctypes.CDLL:
     L.kda_chunk_bwd_grouped_workspace.restype = S
     L.kda_chunk_bwd_grouped.argtypes = [P] * 18 + [I] * 6 + [F, U, I, P, S, P]
     L.kda_chunk_bwd_grouped.restype = I
+    D = ctypes.c_double
+    L.kda_rotary_freqs.argtypes = [P, P, I, D, I, D, I, D, D]
+    L.kda_rotary_freqs.restype = I
+    L.kda_rotary.argtypes = [P] * 6 + [I] * 10 + [F, U, I, P]
+    L.kda_rotary.restype = I
+    L.kda_attn_fwd_workspace.argtypes = [I] * 7
+    L.kda_attn_fwd_workspace.restype = S
+    L.kda_attn_fwd.argtypes = [P] * 7 + [I] * 9 + [F, I, I, I, P, S, P]
+    L.kda_attn_fwd.restype = I
+    L.kda_attn_bwd_workspace.argtypes = [I] * 7
+    L.kda_attn_bwd_workspace.restype = S
+    L.kda_attn_bwd.argtypes = [P] * 11 + [I] * 9 + [F, I, I, I, P, S, P]
+    L.kda_attn_bwd.restype = I
+    L.kda_cache_append.argtypes = [P] * 9 + [I] * 9 + [I, P]
+    L.kda_cache_append.restype = I
+    L.kda_attn_step_workspace.argtypes = [I] * 6
+    L.kda_attn_step_workspace.restype = S
+    L.kda_attn_step.argtypes = [P] * 9 + [I] * 9 + [F, I, I, P, S, P]
+    L.kda_attn_step.restype = I
     L.kda_status_string.argtypes = [I]
     L.kda_status_string.restype = ctypes.c_char_p
     _lib = L
@@ -400,3 +422,238 @@ def output_gate(o, gate, weight=None, *, y=None):
                                 _dt(o.dtype), _stream(o.device))
     _check("kda_output_gate", st)
     return y
+
+
+# ---------------------------------------------------------------- softmax attention
+
+ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+ROTARY_INTERLEAVED, ROTARY_INVERSE = 1, 2
+
+
+def _on_device(dev):
+    """The device of the tensors becomes the current one for a launch (a null
+    stream handle names the current device's stream)."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _expect(name, t, shape, dtype, dev):
+    """Checks an argument's shape, type and device; None passes."""
+    if t is None:
+        return
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError(f"{name} must be a {dtype} tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _rows(name, t):
+    """(pointer, row stride in elements) of a [B,T,H,D] tensor whose heads are
+    packed and whose tokens lie one stride apart throughout."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    B, T, H, D = t.shape
+    if t.numel() == 0:
+        return t.data_ptr(), 0
+    sb, st, sh, sd = t.stride()
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
+        raise ValueError(f"the heads of {name} must be contiguous")
+    ld = st if T > 1 else sb if B > 1 else H * D
+    if ld < H * D or (T > 1 and B > 1 and sb != T * st):
+        raise ValueError(f"the tokens of {name} must lie one stride apart")
+    return t.data_ptr(), ld
+
+
+def _attn_shapes(q, k, v, q_len, kv_len):
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q and k must be [B,T,H,D]")
+    B, Tq, H, D = q.shape
+    Tk, HK = k.shape[1], k.shape[2]
+    _expect("k", k, (B, Tk, HK, D), q.dtype, q.device)
+    _expect("v", v, (B, Tk, HK, D), q.dtype, q.device)
+    _expect("q_len", q_len, (B,), torch.int32, q.device)
+    _expect("kv_len", kv_len, (B,), torch.int32, q.device)
+    return B, Tq, Tk, H, HK, D
+
+
+def _workspace(need, given, dev):
+    if given is not None and given.numel() * given.element_size() >= need:
+        return given
+    return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+
+
+def _ws_args(ws):
+    return (None, 0) if ws is None else (_ptr(ws), ws.numel() * ws.element_size())
+
+
+def rotary_freqs(rot, *, base=10000.0, scaling="none", factor=1.0, trained=0, beta_fast=32.0, beta_slow=1.0,
+                 device="cuda"):
+    """kda_rotary_freqs: (inv_freq [rot/2] fp64 on `device`, scale) for `rotary`.
+    scaling: "none", "linear", "ntk" or "yarn" (by parts; needs `trained`)."""
+    out = torch.empty(max(int(rot), 0) // 2, dtype=torch.float64)
+    scale = ctypes.c_float()
+    _check("kda_rotary_freqs",
+           load().kda_rotary_freqs(out.data_ptr(), ctypes.addressof(scale), int(rot), base, ROTARY_SCALINGS[scaling], factor,
+                                   trained, beta_fast, beta_slow))
+    return out.to(device), scale.value
+
+
+def rotary(q, k, inv_freq, positions=None, *, scale=1.0, interleaved=False, inverse=False, q_out=None, k_out=None):
+    """kda_rotary: the rotary position encoding of q [B,T,H,D] and k [B,T,HK,D]
+    (or None) in one pass; rot = 2 * inv_freq.numel().  positions [B,T] int32 or
+    None (0 .. T-1).  inverse=True is the transposed map, which takes the
+    gradients of the outputs to those of the inputs.  q_out / k_out may be q / k
+    (in place).  q, k and the outputs may be parts of packed tensors.  Returns
+    (q_out, k_out), or q_out without k."""
+    B, T, H, D = q.shape
+    dev = q.device
+    _expect("inv_freq", inv_freq, (inv_freq.numel(),), torch.float64, dev)
+    _expect("positions", positions, (B, T), torch.int32, dev)
+    if q_out is None:
+        q_out = torch.empty((B, T, H, D), dtype=q.dtype, device=dev)
+    _expect("q_out", q_out, q.shape, q.dtype, dev)
+    qp, ldq = _rows("q", q)
+    qo, ldqo = _rows("q_out", q_out)
+    kp = ko = None
+    HK = ldk = ldko = 0
+    if k is not None:
+        HK = k.shape[2]
+        _expect("k", k, (B, T, HK, D), q.dtype, dev)
+        if k_out is None:
+            k_out = torch.empty((B, T, HK, D), dtype=q.dtype, device=dev)
+        _expect("k_out", k_out, k.shape, q.dtype, dev)
+        kp, ldk = _rows("k", k)
+        ko, ldko = _rows("k_out", k_out)
+    with _on_device(dev):
+        st = load().kda_rotary(qp, kp, qo, ko, _ptr(positions), _ptr(inv_freq), B, T, H, HK, D, 2 * inv_freq.numel(),
+                               ldq, ldk, ldqo, ldko, scale,
+                               (ROTARY_INTERLEAVED if interleaved else 0) | (ROTARY_INVERSE if inverse else 0),
+                               _dt(q.dtype), _stream(dev))
+    _check("kda_rotary", st)
+    return q_out if k is None else (q_out, k_out)
+
+
+def attn_fwd_workspace_bytes(B, Tq, Tk, H, HK, D, dtype=torch.bfloat16) -> int:
+    return load().kda_attn_fwd_workspace(B, Tq, Tk, H, HK, D, _dt(dtype))
+
+
+def attn_fwd(q, k, v, *, scale=None, causal=True, window=0, q_len=None, kv_len=None, o=None, lse=None,
+             workspace=None):
+    """kda_attn_fwd: softmax attention of q [B,Tq,H,D] over k, v [B,Tk,HK,D]
+    (H a multiple of HK; each may be part of a packed tensor).  scale None is
+    1/sqrt(D).  causal aligns the last query with the last key; window > 0
+    limits a query to that many keys; q_len, kv_len [B] int32 are the lengths of
+    padded sequences.  Returns (o [B,Tq,H,D], lse [B,H,Tq] fp32)."""
+    B, Tq, Tk, H, HK, D = _attn_shapes(q, k, v, q_len, kv_len)
+    dev, dt = q.device, q.dtype
+    if o is None:
+        o = torch.empty((B, Tq, H, D), dtype=dt, device=dev)
+    if lse is None:
+        lse = torch.empty((B, H, Tq), dtype=torch.float32, device=dev)
+    _expect("o", o, (B, Tq, H, D), dt, dev)
+    _expect("lse", lse, (B, H, Tq), torch.float32, dev)
+    (qp, ldq), (kp, ldk), (vp, ldv) = _rows("q", q), _rows("k", k), _rows("v", v)
+    ws = _workspace(attn_fwd_workspace_bytes(B, Tq, Tk, H, HK, D, dt), workspace, dev)
+    with _on_device(dev):
+        st = load().kda_attn_fwd(qp, kp, vp, _ptr(q_len), _ptr(kv_len), _ptr(o), _ptr(lse), B, Tq, Tk, H, HK, D,
+                                 ldq, ldk, ldv, D ** -0.5 if scale is None else scale, 1 if causal else 0, window,
+                                 _dt(dt), *_ws_args(ws), _stream(dev))
+    _check("kda_attn_fwd", st)
+    return o, lse
+
+
+def attn_bwd_workspace_bytes(B, Tq, Tk, H, HK, D, dtype=torch.bfloat16) -> int:
+    return load().kda_attn_bwd_workspace(B, Tq, Tk, H, HK, D, _dt(dtype))
+
+
+def attn_bwd(q, k, v, o, lse, dout, *, scale=None, causal=True, window=0, q_len=None, kv_len=None, workspace=None):
+    """kda_attn_bwd: gradients of sum(dout * o) from the inputs and results of
+    attn_fwd (same scale, masks and lengths).  Returns a dict dq [B,Tq,H,D], dk,
+    dv [B,Tk,HK,D] in the input dtype."""
+    B, Tq, Tk, H, HK, D = _attn_shapes(q, k, v, q_len, kv_len)
+    dev, dt = q.device, q.dtype
+    _expect("o", o, (B, Tq, H, D), dt, dev)
+    _expect("lse", lse, (B, H, Tq), torch.float32, dev)
+    _expect("dout", dout, (B, Tq, H, D), dt, dev)
+    g = {"dq": torch.empty((B, Tq, H, D), dtype=dt, device=dev), "dk": torch.empty((B, Tk, HK, D), dtype=dt, device=dev),
+         "dv": torch.empty((B, Tk, HK, D), dtype=dt, device=dev)}
+    (qp, ldq), (kp, ldk), (vp, ldv) = _rows("q", q), _rows("k", k), _rows("v", v)
+    ws = _workspace(attn_bwd_workspace_bytes(B, Tq, Tk, H, HK, D, dt), workspace, dev)
+    with _on_device(dev):
+        st = load().kda_attn_bwd(qp, kp, vp, _ptr(q_len), _ptr(kv_len), _ptr(o), _ptr(lse), _ptr(dout), _ptr(g["dq"]),
+                                 _ptr(g["dk"]), _ptr(g["dv"]), B, Tq, Tk, H, HK, D, ldq, ldk, ldv,
+                                 D ** -0.5 if scale is None else scale, 1 if causal else 0, window, _dt(dt),
+                                 *_ws_args(ws), _stream(dev))
+    _check("kda_attn_bwd", st)
+    return g
+
+
+def new_cache(n_pages, HK, D, page=64, device="cuda"):
+    """Buffers of an 8-bit key/value cache of n_pages pages: (k_cache
+    [n_pages,HK,page,D], v_cache [n_pages,HK,D,page], k_scale, v_scale
+    [n_pages,HK]).  Nothing needs to start at zero: what was not appended is not read."""
+    return (torch.empty((n_pages, HK, page, D), dtype=torch.uint8, device=device),
+            torch.empty((n_pages, HK, D, page), dtype=torch.uint8, device=device),
+            torch.empty((n_pages, HK), dtype=torch.float32, device=device),
+            torch.empty((n_pages, HK), dtype=torch.float32, device=device))
+
+
+def _cache_shapes(k_cache, v_cache, k_scale, v_scale, block_table, cache_len, new_len, B, D, dev):
+    n_pages, HK, page = k_cache.shape[:3]
+    _expect("k_cache", k_cache, (n_pages, HK, page, D), torch.uint8, dev)
+    _expect("v_cache", v_cache, (n_pages, HK, D, page), torch.uint8, dev)
+    _expect("k_scale", k_scale, (n_pages, HK), torch.float32, dev)
+    _expect("v_scale", v_scale, (n_pages, HK), torch.float32, dev)
+    _expect("block_table", block_table, (B, block_table.shape[-1]), torch.int32, dev)
+    _expect("cache_len", cache_len, (B,), torch.int32, dev)
+    _expect("new_len", new_len, (B,), torch.int32, dev)
+    return n_pages, HK, page, block_table.shape[1]
+
+
+def cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cache_len, new_len=None):
+    """kda_cache_append: k, v [B,T,HK,D] go, as 8-bit codes, behind the
+    cache_len[b] tokens of each sequence (new_len[b] of them, None: T), into the
+    pages block_table [B,max_pages] int32 names.  The caches and scales are
+    updated in place; cache_len is not.  Sequences of one call must not write the
+    same page."""
+    B, T, HK, D = k.shape
+    dev = k.device
+    _expect("v", v, k.shape, k.dtype, dev)
+    n_pages, hk, page, max_pages = _cache_shapes(k_cache, v_cache, k_scale, v_scale, block_table, cache_len, new_len,
+                                                 B, D, dev)
+    if hk != HK:
+        raise ValueError(f"the cache has {hk} heads, k has {HK}")
+    (kp, ldk), (vp, ldv) = _rows("k", k), _rows("v", v)
+    with _on_device(dev):
+        st = load().kda_cache_append(kp, vp, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                                     _ptr(block_table), _ptr(cache_len), _ptr(new_len), n_pages, max_pages, B, T, HK,
+                                     D, page, ldk, ldv, _dt(k.dtype), _stream(dev))
+    _check("kda_cache_append", st)
+
+
+def attn_step_workspace_bytes(B, Tq, H, HK, D, max_len) -> int:
+    return load().kda_attn_step_workspace(B, Tq, H, HK, D, max_len)
+
+
+def attn_step(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_len, new_len=None, *, scale=None, window=0,
+              o=None, workspace=None):
+    """kda_attn_step: attention of the newest tokens' q [B,Tq,H,D] over the
+    cache, after their cache_append (the same cache_len and new_len: query i of
+    sequence b stands at position cache_len[b] + i).  Returns o [B,Tq,H,D]."""
+    B, Tq, H, D = q.shape
+    dev, dt = q.device, q.dtype
+    n_pages, HK, page, max_pages = _cache_shapes(k_cache, v_cache, k_scale, v_scale, block_table, cache_len, new_len,
+                                                 B, D, dev)
+    if o is None:
+        o = torch.empty((B, Tq, H, D), dtype=dt, device=dev)
+    _expect("o", o, (B, Tq, H, D), dt, dev)
+    qp, ldq = _rows("q", q)
+    ws = _workspace(attn_step_workspace_bytes(B, Tq, H, HK, D, max_pages * page), workspace, dev)
+    with _on_device(dev):
+        st = load().kda_attn_step(qp, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
+                                  _ptr(cache_len), _ptr(new_len), _ptr(o), n_pages, max_pages, B, Tq, H, HK, D, page,
+                                  ldq, D ** -0.5 if scale is None else scale, window, _dt(dt), *_ws_args(ws),
+                                  _stream(dev))
+    _check("kda_attn_step", st)
+    return o

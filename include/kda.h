@@ -48,7 +48,8 @@ typedef enum {
     KDA_ERR_GATE = 5,      /* g_min not finite or not negative (bounded gate)  */
     KDA_ERR_WORKSPACE = 6, /* workspace NULL, misaligned or too small           */
     KDA_ERR_HIP = 7,       /* a kernel launch failed                             */
-    KDA_ERR_SCRATCH = 8    /* kda_chunk_fwd_noalloc: sizes beyond its scratch   */
+    KDA_ERR_SCRATCH = 8,   /* kda_chunk_fwd_noalloc: sizes beyond its scratch   */
+    KDA_ERR_SCALE = 9      /* a scale is not finite (or, for softmax, not > 0)  */
 } kda_status;
 
 typedef enum { KDA_F32 = 0, KDA_BF16 = 1 } kda_dtype;
@@ -361,6 +362,156 @@ kda_status kda_chunk_bwd_grouped(const void* q, const void* k, const void* v, co
                                  int B, int T, int H, int HV, int Dk, int Dv, float g_min, unsigned flags,
                                  kda_dtype dt, void* workspace, size_t workspace_bytes,
                                  hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Softmax attention: the other token mixer of a KDA stack ("KDA 模块交互式演示"
+ * §1.8: every fourth layer attends over all keys), with the position encoding
+ * in front of it and the 8-bit cache it decodes from.  Layouts as above:
+ * q [B,Tq,H,D]; k, v [B,Tk,HK,D]; query head h reads key/value head h / G with
+ * G = H / HK (H a positive multiple of HK); D in {16, 32, 64, 128}.
+ *
+ * Row strides: ld* is the distance between consecutive tokens of a tensor in
+ * elements (0 selects heads * D, a contiguous tensor; otherwise at least that
+ * and a multiple of 16 bytes); sequences are T * ld apart and heads D apart,
+ * so q, k and v may be the parts of one packed projection [B,T,H+2HK,D].
+ *
+ * Lengths: device arrays of B ints, read when the kernels run; values outside
+ * the tensor's range are clamped to it.  Nothing at or past a sequence's
+ * length is read, whatever it holds. */
+
+/* Inverse frequencies of the rotary position encoding for `rot` channels
+ * (positive, even, at most 128):
+ * inv_freq[i] = base^(-2i/rot), i < rot / 2, host memory, in radians per
+ * position, scaled for contexts `factor` times the `trained` length:
+ *   KDA_ROTARY_NONE    unscaled (factor, trained and beta_* unused);
+ *   KDA_ROTARY_LINEAR  every frequency divided by factor;
+ *   KDA_ROTARY_NTK     base * factor^(rot / (rot - 2)) in place of base (rot = 2: base);
+ *   KDA_ROTARY_YARN    by parts: frequencies that turn more than beta_fast
+ *                      times within the trained length are kept, those below
+ *                      beta_slow turns are divided by factor, those between
+ *                      are blended linearly in i; *scale = 0.1 ln(factor) + 1.
+ * *scale (nullable) receives the scale of the rotated values, 1 otherwise.
+ * KDA_ERR_NULL without inv_freq; KDA_ERR_SHAPE for rot, kind or trained < 1
+ * (by parts); KDA_ERR_SCALE unless base > 1, factor >= 1, beta_fast >
+ * beta_slow > 0, all finite.  Host only; no HIP call. */
+enum { KDA_ROTARY_NONE = 0, KDA_ROTARY_LINEAR = 1, KDA_ROTARY_NTK = 2, KDA_ROTARY_YARN = 3 };
+kda_status kda_rotary_freqs(double* inv_freq, float* scale, int rot, double base, int kind, double factor,
+                            int trained, double beta_fast, double beta_slow);
+
+/* Rotary position encoding of q and k in one pass: with a = scale cos(p w_i),
+ * b = scale sin(p w_i) for token position p,
+ *   (x_j, x_j') -> (a x_j - b x_j', b x_j + a x_j')  over the pairs of the
+ * first `rot` channels of each head; channels rot .. D-1 are copied.
+ *   mode       KDA_ROTARY_INTERLEAVED: pair i is channels (2i, 2i+1);
+ *              otherwise (i, i + rot/2).  KDA_ROTARY_INVERSE: b -> -b, the
+ *              transposed map, so the same call is the gradient.
+ *   q, q_out   [B,T,H,D] with strides ldq, ldqo; k, k_out [B,T,HK,D] with ldk,
+ *              ldko, or NULL (HK then ignored).  q_out may be q itself with the
+ *              same stride (in place), k_out likewise; outputs may not
+ *              otherwise overlap an input or each other (KDA_ERR_SHAPE).
+ *   positions  [B,T] int device, or NULL: 0 .. T-1 in every sequence.
+ *   inv_freq   [rot/2] double device (kda_rotary_freqs).  Angles are formed in
+ *              64 bits and reduced to a turn, so far positions keep their
+ *              precision.
+ *   rot        even, 2 .. D.
+ * Errors: KDA_ERR_DTYPE, KDA_ERR_SHAPE, KDA_ERR_SCALE (scale not finite),
+ * KDA_ERR_NULL, KDA_ERR_ALIGN, KDA_ERR_HIP. */
+enum { KDA_ROTARY_INTERLEAVED = 1u, KDA_ROTARY_INVERSE = 2u };
+kda_status kda_rotary(const void* q, const void* k, void* q_out, void* k_out, const int* positions,
+                      const double* inv_freq, int B, int T, int H, int HK, int D, int rot,
+                      int ldq, int ldk, int ldqo, int ldko, float scale, unsigned mode, kda_dtype dt,
+                      hipStream_t stream);
+
+/* Softmax attention forward.  Query i of sequence b stands at key position
+ * p = i + kv_len[b] - q_len[b] (the last query at the last key) and sees the
+ * keys j < kv_len[b] with j <= p if `causal`, and j > p - window if window > 0:
+ *   o_i = sum_j P_ij v_j,  P_ij = exp(scale q_i.k_j - lse_i),
+ *   lse_i = ln sum_j exp(scale q_i.k_j)   over the visible j.
+ * A query that sees no key, and queries i >= q_len[b], get o = 0 and
+ * lse = -infinity.
+ *   q_len, kv_len  [B] int device or NULL (Tq, Tk).
+ *   o    [B,Tq,H,D] contiguous, dtype dt;  lse [B,H,Tq] fp32 or NULL.
+ *   scale  finite and positive (KDA_ERR_SCALE otherwise).
+ *   workspace  kda_attn_fwd_workspace bytes, 256-byte aligned: partial results
+ *        of calls with few query rows, whose key axis is split over several
+ *        workgroups (0 bytes, and NULL accepted, for the others).
+ * Statistics and sums are fp32; bf16 probabilities are rounded to bf16 before
+ * their product with v.  A masked key inside the lengths has no effect as long
+ * as its k and v are finite; a NaN or infinity in v at such a key may reach
+ * rows of the same tile.  o may overlap no input, lse or the workspace.
+ * Errors: KDA_ERR_DTYPE, KDA_ERR_SHAPE, KDA_ERR_SCALE, KDA_ERR_NULL,
+ * KDA_ERR_ALIGN, KDA_ERR_WORKSPACE, KDA_ERR_HIP. */
+size_t kda_attn_fwd_workspace(int B, int Tq, int Tk, int H, int HK, int D, kda_dtype dt);
+kda_status kda_attn_fwd(const void* q, const void* k, const void* v, const int* q_len, const int* kv_len,
+                        void* o, float* lse, int B, int Tq, int Tk, int H, int HK, int D,
+                        int ldq, int ldk, int ldv, float scale, int causal, int window, kda_dtype dt,
+                        void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Backward of kda_attn_fwd for a loss with dL/do = dout, from the forward's
+ * inputs and its o and lse (the probabilities are recomputed):
+ *   dv_j = sum_i P_ij dout_i,   dS_ij = P_ij (dout_i.v_j - dout_i.o_i),
+ *   dq_i = scale sum_j dS_ij k_j,   dk_j = scale sum_i dS_ij q_i,
+ * dk and dv summed over the G query heads of each key/value head.  No
+ * atomics: results do not vary from run to run.
+ *   o, dout, dq [B,Tq,H,D], dk, dv [B,Tk,HK,D]: contiguous, dtype dt.  Rows
+ *   past the lengths, and rows that see or are seen by nothing, get 0; o, lse
+ *   and dout are not read past q_len.
+ *   workspace  kda_attn_bwd_workspace bytes, 256-byte aligned.
+ * Outputs may overlap neither an input, another output nor the workspace
+ * (KDA_ERR_SHAPE).  Errors otherwise as kda_attn_fwd. */
+size_t kda_attn_bwd_workspace(int B, int Tq, int Tk, int H, int HK, int D, kda_dtype dt);
+kda_status kda_attn_bwd(const void* q, const void* k, const void* v, const int* q_len, const int* kv_len,
+                        const void* o, const float* lse, const void* dout, void* dq, void* dk, void* dv,
+                        int B, int Tq, int Tk, int H, int HK, int D, int ldq, int ldk, int ldv,
+                        float scale, int causal, int window, kda_dtype dt,
+                        void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* The 8-bit key/value cache.  Pages of `page` tokens (16, 32, 64 or 128), one
+ * scale for each page and key/value head; a stored code c (e4m3: 1 sign, 4
+ * exponent, 3 mantissa bits, largest 448) stands for c * scale:
+ *   k_cache [n_pages,HK,page,D] bytes, v_cache [n_pages,HK,D,page] bytes (a
+ *   page of v is stored transposed, as the attention's products read it),
+ *   k_scale, v_scale [n_pages,HK] fp32;
+ *   block_table [B,max_pages] int: page number of each `page` tokens of a
+ *   sequence; an entry outside 0 .. n_pages-1 names no page.
+ *
+ * kda_cache_append writes new_len[b] tokens (NULL: T) of k, v [B,T,HK,D] (dtype
+ * dt, strides ldk, ldv) behind the cache_len[b] tokens sequence b already has.
+ * The scale of a page is the smallest power of two with max|x| <= 448 scale
+ * over the finite values written (at least 2^-100), never below the scale of
+ * tokens already in the page; where it grows, those tokens' codes are moved to
+ * it.  Values are divided by the scale and rounded to nearest even; infinities
+ * become +-448, NaN stays NaN.  Tokens whose page is missing (no entry, or past
+ * max_pages) are dropped; pages without new tokens, and bytes past the last
+ * token, are left as they were.  Two sequences of one call must not write the
+ * same page (shared pages are for reading).
+ * Sizes as above, n_pages * HK <= 2^30; no buffer may overlap another.
+ * Errors: KDA_ERR_DTYPE, KDA_ERR_SHAPE, KDA_ERR_NULL, KDA_ERR_ALIGN, KDA_ERR_HIP. */
+kda_status kda_cache_append(const void* k, const void* v, void* k_cache, void* v_cache,
+                            float* k_scale, float* v_scale, const int* block_table,
+                            const int* cache_len, const int* new_len, int n_pages, int max_pages,
+                            int B, int T, int HK, int D, int page, int ldk, int ldv, kda_dtype dt,
+                            hipStream_t stream);
+
+/* Attention of the new_len[b] (NULL: Tq) newest tokens over that cache, after
+ * their append (the decode step for Tq = 1; drafted tokens or a prompt's chunk
+ * for more): query i stands at position p = cache_len[b] + i and sees the cached
+ * tokens j <= p, and j > p - window if window > 0.  Tokens whose page is missing
+ * are not seen.  Queries past new_len, and those that see nothing, get o = 0.
+ *   q [B,Tq,H,D] (stride ldq), o [B,Tq,H,D] contiguous, dtype dt.
+ *   workspace  kda_attn_step_workspace(B, Tq, H, HK, D, max_pages * page)
+ *        bytes, 256-byte aligned: partial results where the cache is split
+ *        over several workgroups.
+ * fp32 queries and probabilities enter the products as three bf16 parts (24
+ * bits), bf16 ones as they are (probabilities rounded to bf16).
+ * Errors: KDA_ERR_DTYPE, KDA_ERR_SHAPE, KDA_ERR_SCALE, KDA_ERR_NULL,
+ * KDA_ERR_ALIGN, KDA_ERR_WORKSPACE, KDA_ERR_HIP. */
+size_t kda_attn_step_workspace(int B, int Tq, int H, int HK, int D, int max_len);
+kda_status kda_attn_step(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                         const float* v_scale, const int* block_table, const int* cache_len,
+                         const int* new_len, void* o, int n_pages, int max_pages, int B, int Tq,
+                         int H, int HK, int D, int page, int ldq, float scale, int window, kda_dtype dt,
+                         void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* Static description of a status code (never NULL). */
 const char* kda_status_string(kda_status s);

@@ -1,0 +1,272 @@
+"""GPU parity of softmax attention, forward and backward, with the fp64 oracle, at
+the sizes, lengths, masks and strides where tiles end; bounds in tests/attn_check.py."""
+
+import numpy as np
+import pytest
+import torch
+
+from gated_delta_rule_82_amd import kda
+from oracle import attn_oracle as ora
+from tests.attn_check import BF16, F32, bwd_bounds, check, fwd_bounds, np64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    assert torch.cuda.is_available(), "GPU tests need a ROCm device"
+    kda.load()
+    yield
+    torch.cuda.synchronize()
+
+
+def draw(B, Tq, Tk, H, HK, D, dtype, seed, packed=False):
+    g = torch.Generator().manual_seed(seed)
+    if packed and Tq == Tk:
+        x = torch.randn(B, Tq, H + 2 * HK, D, generator=g).to(dtype).cuda()
+        q, k, v = x[:, :, :H], x[:, :, H:H + HK], x[:, :, H + HK:]
+    else:
+        q, k, v = (torch.randn(B, t, h, D, generator=g).to(dtype).cuda() for t, h in ((Tq, H), (Tk, HK), (Tk, HK)))
+    return q, k, v, torch.randn(B, Tq, H, D, generator=g).to(dtype).cuda()
+
+
+def ints(x):
+    return None if x is None else torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def run_both(q, k, v, do, dtype, what="", scale=None, ql=None, kl=None, poison=False, **kw):
+    scale = q.shape[-1] ** -0.5 if scale is None else scale
+    lens = dict(q_len=ints(ql), kv_len=ints(kl))
+    ref = [np64(x) for x in (q, k, v, do)]
+    if poison:  # what lies past the lengths is never read
+        q, k, v, do = (x.clone() for x in (q, k, v, do))
+        for b in range(q.shape[0]):
+            for x, n in ((q, ql), (do, ql), (k, kl), (v, kl)):
+                if n is not None:
+                    x[b, max(n[b], 0):] = float("nan")
+    o, lse = kda.attn_fwd(q, k, v, scale=scale, **lens, **kw)
+    torch.cuda.synchronize()
+    wo, wl, bo, bl = fwd_bounds(*ref[:3], dtype, scale, q_len=ql, kv_len=kl, **kw)
+    check(o, wo, bo, f"{what} o")
+    check(lse, wl, bl, f"{what} lse")
+    if poison:
+        o, lse = o.clone(), lse.clone()
+        for b in range(q.shape[0]):
+            if ql is not None:
+                o[b, max(ql[b], 0):] = float("nan")
+                lse[b, :, max(ql[b], 0):] = float("nan")
+    g = kda.attn_bwd(q, k, v, o, lse, do, scale=scale, **lens, **kw)
+    torch.cuda.synchronize()
+    grads, bounds = bwd_bounds(*ref, dtype, scale, q_len=ql, kv_len=kl, **kw)
+    for n, w, b in zip(("dq", "dk", "dv"), grads, bounds):
+        check(g[n], w, b, f"{what} {n}")
+
+
+SIZES = [(1, 1, 1, 1, 1), (2, 1, 37, 4, 2), (1, 33, 33, 3, 3), (2, 65, 64, 2, 1), (1, 64, 129, 8, 2), (3, 20, 7, 5, 1),
+         (1, 200, 200, 2, 2)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D", [16, 32, 64, 128])
+@pytest.mark.parametrize("B,Tq,Tk,H,HK", SIZES)
+def test_attn_matches_oracle(dtype, D, B, Tq, Tk, H, HK):
+    x = draw(B, Tq, Tk, H, HK, D, dtype, 100 * D + Tq, packed=True)
+    for causal, window in ((True, 0), (False, 0), (True, 5), (False, 40)):
+        run_both(*x, dtype, f"causal {causal} window {window}", causal=causal, window=window)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 17)])
+def test_attn_lengths(dtype, causal, window):
+    B, T = 6, 150
+    x = draw(B, T, T, 4, 2, 64, dtype, 7, packed=True)
+    run_both(*x, dtype, "equal lengths", ql=[150, 1, 0, 64, 65, 127], kl=[150, 1, 0, 64, 65, 127], poison=True,
+             causal=causal, window=window)
+    # no key at all, fewer keys than queries, out of range (clamped)
+    run_both(*x, dtype, "unequal lengths", ql=[150, 10, 3, 70, 200, 128], kl=[3, 0, 150, 65, 150, -4], poison=True,
+             causal=causal, window=window)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("Tq,H,HK", [(1, 8, 2), (3, 4, 4), (16, 8, 1), (40, 6, 2)])
+def test_attn_split_key_axis(dtype, Tq, H, HK):
+    """Few rows over a long key axis: several workgroups and a join."""
+    B, Tk = 2, 2600
+    assert kda.attn_fwd_workspace_bytes(B, Tq, Tk, H, HK, 64, dtype) > 0
+    q, k, v, _ = draw(B, Tq, Tk, H, HK, 64, dtype, Tq)
+    for kw, ql, kl in ((dict(causal=True, window=0), None, None), (dict(causal=False, window=0), [Tq, Tq], [2600, 9]),
+                       (dict(causal=True, window=700), [Tq, Tq // 2], [2600, 1300])):
+        o, lse = kda.attn_fwd(q, k, v, q_len=ints(ql), kv_len=ints(kl), **kw)
+        torch.cuda.synchronize()
+        wo, wl, bo, bl = fwd_bounds(np64(q), np64(k), np64(v), dtype, 64 ** -0.5, q_len=ql, kv_len=kl, **kw)
+        check(o, wo, bo, f"o {kw}")
+        check(lse, wl, bl, f"lse {kw}")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("scale", [1e-3, 1.0, 30.0])
+def test_attn_scales(dtype, scale):
+    """From nearly uniform rows to one key per row; large scores on both sides of zero."""
+    q, k, v, do = draw(1, 70, 70, 2, 2, 32, dtype, 11)
+    run_both(q, k, v, do, dtype, f"scale {scale}", scale=scale, causal=True, window=0)
+
+
+def test_attn_equal_rows_and_large_magnitudes():
+    q, k, v, do = draw(1, 40, 40, 2, 1, 64, BF16, 12)
+    k.zero_()
+    run_both(q, k, v, do, BF16, "zero keys", causal=True, window=0)
+    q, k, v, do = draw(1, 40, 40, 2, 1, 64, F32, 13)
+    run_both(q * 1e-20, k, v * 1e15, do, F32, "tiny queries", causal=False, window=0)
+
+
+def test_attn_nan_and_infinity_reach_only_the_rows_that_see_them():
+    q, k, v, _ = draw(1, 300, 300, 1, 1, 64, F32, 14)
+    k[0, 200, 0, 3] = float("nan")
+    o, lse = kda.attn_fwd(q, k, v, causal=True)
+    torch.cuda.synchronize()
+    bad = torch.isnan(o[0, :, 0]).any(-1)
+    assert bool(bad[200:].all()) and not bool(bad[:200].any())
+    assert bool(torch.isnan(lse[0, 0, 200:]).all()) and bool(torch.isfinite(lse[0, 0, :200]).all())
+    # the same through the split key axis
+    o, lse = kda.attn_fwd(q[:, -1:], torch.cat([k] * 6, 1), torch.cat([v] * 6, 1), causal=True)
+    assert bool(torch.isnan(o).all()) and bool(torch.isnan(lse).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_attn_writes_its_outputs_only(dtype):
+    B, Tq, Tk, H, HK, D = 2, 37, 50, 4, 2, 64
+    q, k, v, do = draw(B, Tq, Tk, H, HK, D, dtype, 15)
+    big = torch.full((B * Tq * H * D + 512,), 7.0, dtype=dtype, device="cuda")
+    o = big[256:-256].view(B, Tq, H, D)
+    lbig = torch.full((B * H * Tq + 64,), 7.0, device="cuda")
+    lse = lbig[32:-32].view(B, H, Tq)
+    kda.attn_fwd(q, k, v, o=o, lse=lse)
+    torch.cuda.synchronize()
+    assert bool((big[:256] == 7).all()) and bool((big[-256:] == 7).all())
+    assert bool((lbig[:32] == 7).all()) and bool((lbig[-32:] == 7).all())
+
+
+def test_attn_bwd_repeats_bit_for_bit():
+    q, k, v, do = draw(2, 260, 260, 8, 2, 128, BF16, 16)
+    o, lse = kda.attn_fwd(q, k, v)
+    a = kda.attn_bwd(q, k, v, o, lse, do)
+    for _ in range(3):
+        b = kda.attn_bwd(q, k, v, o, lse, do)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a[n], b[n]) for n in a)
+
+
+def test_attn_gradient_against_differences():
+    """The derivative along a direction, from differences of the fp64 forward, against
+    the operator's gradients: the gradients' own bounds plus the difference's h^2 term
+    (third derivatives of these sums are below 1e3 at this size)."""
+    q, k, v, do = draw(1, 24, 30, 4, 2, 16, F32, 17)
+    kw = dict(causal=True, window=9, q_len=[20], kv_len=[27])
+    o, lse = kda.attn_fwd(q, k, v, causal=True, window=9, q_len=ints([20]), kv_len=ints([27]))
+    g = kda.attn_bwd(q, k, v, o, lse, do, causal=True, window=9, q_len=ints([20]), kv_len=ints([27]))
+    ref = [np64(x) for x in (q, k, v, do)]
+    _, bounds = bwd_bounds(*ref, F32, 0.25, **kw)
+    rng, h = np.random.default_rng(0), 1e-4
+    for i, n in enumerate(("dq", "dk", "dv")):
+        d = rng.standard_normal(ref[i].shape)
+        at = lambda s: (ora.attn_forward(*[x + s * d if j == i else x for j, x in enumerate(ref[:3])], 0.25, **kw)[0] * ref[3]).sum()  # noqa: E731
+        diff = (at(h) - at(-h)) / (2 * h)
+        assert abs(diff - (np64(g[n]) * d).sum()) <= (bounds[i] * np.abs(d)).sum() + 1e3 * h * h, n
+
+
+def test_attn_streams_and_two_calls_at_once():
+    xs = [draw(1, 128, 1500, 8, 2, 64, BF16, s) for s in (21, 22)]
+    want = [kda.attn_fwd(*x[:3]) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = []
+    for s, x in zip(streams, xs):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            got.append([kda.attn_fwd(*x[:3]) for _ in range(4)])
+    torch.cuda.synchronize()
+    for w, many in zip(want, got):
+        for o, lse in many:
+            assert torch.equal(o, w[0]) and torch.equal(lse, w[1])
+
+
+def test_attn_captured_and_replayed():
+    q, k, v, do = draw(2, 100, 100, 4, 2, 64, BF16, 23)
+    qs, ks, vs, _ = draw(1, 4, 2048, 8, 2, 64, BF16, 24)   # the split form
+    step = lambda: (kda.attn_fwd(q, k, v), kda.attn_fwd(qs, ks, vs))  # noqa: E731
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        (o, lse), _ = step()
+        kda.attn_bwd(q, k, v, o, lse, do)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        (o, lse), (o2, lse2) = step()
+        g = kda.attn_bwd(q, k, v, o, lse, do)
+    for i in range(3):
+        for x in (q, k, v, do, qs, ks, vs):
+            x.copy_(torch.randn(x.shape, generator=torch.Generator().manual_seed(30 + i)).to(BF16))
+        graph.replay()
+        torch.cuda.synchronize()
+        (wo, wl), (wo2, wl2) = step()
+        wg = kda.attn_bwd(q, k, v, wo, wl, do)
+        torch.cuda.synchronize()
+        assert torch.equal(o, wo) and torch.equal(lse, wl) and torch.equal(o2, wo2) and torch.equal(lse2, wl2)
+        assert all(torch.equal(g[n], wg[n]) for n in g)
+
+
+def test_attn_empty():
+    for B, Tq, Tk in ((0, 3, 3), (2, 0, 3), (2, 3, 0)):
+        q, k, v, do = draw(B, Tq, Tk, 2, 1, 32, F32, 1)
+        o, lse = kda.attn_fwd(q, k, v)
+        g = kda.attn_bwd(q, k, v, o, lse, do)
+        torch.cuda.synchronize()
+        assert bool((o == 0).all()) and bool((lse == float("-inf")).all())
+        assert all(bool((x == 0).all()) for x in g.values())
+
+
+def test_attn_rows_past_32_bit_offsets():
+    """Keys whose byte offset in the tensor passes 2^32: the last sequence of a long cache."""
+    B, Tk, HK, D = 5, 524288, 8, 128
+    k = torch.zeros(B, Tk, HK, D, dtype=BF16, device="cuda")
+    v = torch.zeros(B, Tk, HK, D, dtype=BF16, device="cuda")
+    q = torch.randn(B, 1, HK, D, generator=torch.Generator().manual_seed(2)).to(BF16).cuda()
+    n = [64, 64, 64, 64, Tk]
+    k[4, -8:] = torch.randn(8, HK, D, generator=torch.Generator().manual_seed(3)).to(BF16).cuda()
+    v[4, -8:] = torch.randn(8, HK, D, generator=torch.Generator().manual_seed(4)).to(BF16).cuda()
+    o, lse = kda.attn_fwd(q, k, v, kv_len=ints(n), window=8)
+    torch.cuda.synchronize()
+    wo, wl, bo, bl = fwd_bounds(np64(q[4:]), np64(k[4:, -8:]), np64(v[4:, -8:]), BF16, D ** -0.5)
+    check(o[4:], wo, bo, "o")
+    check(lse[4:], wl, bl, "lse")
+
+
+def test_attn_refusals():
+    q, k, v, do = draw(2, 8, 8, 4, 2, 32, BF16, 1)
+    o, lse = kda.attn_fwd(q, k, v)
+    with pytest.raises(TypeError):
+        kda.attn_fwd(q.half(), k.half(), v.half())
+    with pytest.raises(TypeError):
+        kda.attn_fwd(q, k.float(), v)
+    with pytest.raises(ValueError):
+        kda.attn_fwd(q, k, v[:, :4])
+    with pytest.raises(ValueError):
+        kda.attn_fwd(q.transpose(1, 2), k.transpose(1, 2), v.transpose(1, 2))
+    with pytest.raises(ValueError):
+        kda.attn_fwd(q, k, v, kv_len=ints([1, 2, 3]))
+    with pytest.raises(TypeError):
+        kda.attn_fwd(q, k, v, kv_len=torch.ones(2, dtype=torch.int64, device="cuda"))
+    with pytest.raises(kda.KDAError):
+        kda.attn_fwd(q[:, :, :3], k, v)            # three query heads over two
+    for s in (0.0, -1.0, float("inf"), float("nan")):
+        with pytest.raises(kda.KDAError):
+            kda.attn_fwd(q, k, v, scale=s)
+    with pytest.raises(kda.KDAError):
+        kda.attn_fwd(q, k, v, window=-1)
+    with pytest.raises(kda.KDAError):
+        kda.attn_fwd(q, k, v, o=q)                 # the output over an input
+    with pytest.raises(ValueError):
+        kda.attn_bwd(q, k, v, o, lse, do[:, :4])
+    with pytest.raises(kda.KDAError):
+        kda.attn_fwd(*(x[..., :24].contiguous() for x in (q, k, v)))
