@@ -51,14 +51,16 @@ struct AttnArgs {
 // waves of a workgroup: as many as the rows of a key/value head fill.
 constexpr int attn_rows_per_wave(int elem_bytes) { return elem_bytes == 2 ? 32 : 16; }
 inline int attn_waves(long long rows, int per_wave) { return rows <= per_wave ? 1 : rows <= 2 * per_wave ? 2 : 4; }
+// Most parts a key axis is split into (the join reads their statistics at once).
+constexpr int kMaxSplits = 128;
 // Workgroups over the key axis (1: not split).  Two workgroups per compute unit
-// fill the card; a split takes at least 512 keys, so that its partial output
+// fill the card; a split takes at least 256 keys, so that its partial output
 // stays small beside the keys it reads.
 inline int attn_fwd_splits(int elem_bytes, int B, int Tq, int Tk, int HK, int G) {
     const long long rows = (long long)Tq * G, per = attn_rows_per_wave(elem_bytes);
     const long long bq = per * attn_waves(rows, (int)per), wgs = (long long)B * HK * ((rows + bq - 1) / bq);
-    const long long want = wgs > 0 ? 512 / wgs : 1, most = Tk / 512, n = want < most ? want : most;
-    return n < 1 ? 1 : n > 64 ? 64 : (int)n;
+    const long long want = wgs > 0 ? 512 / wgs : 1, most = Tk / 256, n = want < most ? want : most;
+    return n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : (int)n;
 }
 hipError_t launch_attn_fwd(int dt, int D, const AttnArgs& a, hipStream_t s);
 // Packed rows of one key/value head in the backward's row array.
@@ -92,7 +94,7 @@ inline int attn_step_splits(int B, int Tq, int HK, int G, int max_len) {
     const long long rows = (long long)Tq * G, br = 16 * attn_step_row_blocks(rows);
     const long long wgs = (long long)B * HK * ((rows + br - 1) / br);
     const long long want = wgs > 0 ? 1024 / wgs : 1, most = max_len / 256, n = want < most ? want : most;
-    return n < 1 ? 1 : n > 128 ? 128 : (int)n;
+    return n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : (int)n;
 }
 hipError_t launch_attn_step(int dt, int D, const AttnStepArgs& a, hipStream_t s);
 

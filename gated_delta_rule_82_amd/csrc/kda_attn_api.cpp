@@ -27,7 +27,8 @@ bool attn_sizes_ok(int B, int Tq, int Tk, int H, int HK) {
 // Row stride in elements: 0 selects contiguous tokens.
 kda_status stride(int ld, int heads, int D, kda_dtype dt, size_t* out) {
     const long long least = (long long)heads * D;
-    if (ld < 0 || (ld > 0 && ld < least)) return KDA_ERR_SHAPE;
+    // 64 rows of 4-byte elements stay below 2^31 bytes (tiles are addressed with 32-bit offsets)
+    if (ld < 0 || (ld > 0 && ld < least) || ld > (1 << 23) || least > (1 << 23)) return KDA_ERR_SHAPE;
     *out = ld ? (size_t)ld : (size_t)least;
     return (*out * elem_bytes(dt)) % 16 == 0 ? KDA_OK : KDA_ERR_ALIGN;
 }

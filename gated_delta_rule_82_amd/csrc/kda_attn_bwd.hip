@@ -54,7 +54,8 @@ __global__ __launch_bounds__(64 * NW, 1) void kda_attn_dkv_kernel(const AttnArgs
     constexpr int NS = G_::NS, ND = G_::ND, BK = 16 * NK * NW;
     constexpr int kTile = RB * D * (int)sizeof(T);
     __shared__ __attribute__((aligned(16))) unsigned char sm[2][2][kTile];
-    __shared__ __attribute__((aligned(16))) float srow[2][RB * 2];
+    __shared__ __attribute__((aligned(16))) float srow[2][256];  // RB pairs, and room for a whole wave's copy
+    static_assert(RB <= 128, "row values fit");
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4;
     const int nbh = a.B * a.HK;
@@ -102,23 +103,33 @@ __global__ __launch_bounds__(64 * NW, 1) void kda_attn_dkv_kernel(const AttnArgs
     const bool active = __any(some);
 
     const T* qbase = reinterpret_cast<const T*>(a.q) + (size_t)b * a.Tq * a.ldq + (size_t)hk * a.G * D;
-    const T* dobase = reinterpret_cast<const T*>(a.dout) + ((size_t)b * a.Tq * a.H + (size_t)hk * a.G) * D;
+    const size_t ldo = (size_t)a.H * D;
+    const T* dobase = reinterpret_cast<const T*>(a.dout) + (size_t)b * a.Tq * ldo + (size_t)hk * a.G * D;
     const float* rbase = a.rows + 2 * (size_t)bh * padded;
+    Stage<T, D, RB, NW> qst, dst;
+    const uint32_t lds0 = lds_address(&sm[0][0][0]), lds_rows = lds_address(&srow[0][0]);
+    auto place = [&](int skip) {  // row x of a tile is packed row skip + x of the window's tokens
+        qst.init(wave, lane, [&](int x) {
+            const int t = (int)fdiv((uint32_t)(skip + x), a.divG);
+            return (uint32_t)((t * a.ldq + (size_t)(skip + x - t * a.G) * D) * sizeof(T));
+        });
+        dst.init(wave, lane, [&](int x) {
+            const int t = (int)fdiv((uint32_t)(skip + x), a.divG);
+            return (uint32_t)((t * ldo + (size_t)(skip + x - t * a.G) * D) * sizeof(T));
+        });
+    };
+    place(0);
+    const bool whole_tokens = RB % a.G == 0;  // every tile starts with a token's first head
     auto stage = [&](int rt, int buf) {
-        const int last = ql * a.G - 1;  // rows past the last valid one repeat it
-        stage_rows<T, D, RB, NW>(sm[buf][0], wave, lane, [&](int x) {
-            const int r = min(rt * RB + x, last), t = (int)fdiv((uint32_t)r, a.divG);
-            return qbase + (size_t)t * a.ldq + (size_t)(r - t * a.G) * D;
-        });
-        stage_rows<T, D, RB, NW>(sm[buf][1], wave, lane, [&](int x) {
-            const int r = min(rt * RB + x, last), t = (int)fdiv((uint32_t)r, a.divG);
-            return dobase + ((size_t)t * a.H + (r - t * a.G)) * D;
-        });
-        // the row array is padded to whole tiles
-        if (wave == 0 && lane < RB / 2)
-            __builtin_amdgcn_global_load_lds(
-                (const __attribute__((address_space(1))) void*)(rbase + 2 * (size_t)rt * RB + lane * 4),
-                (__attribute__((address_space(3))) void*)(&srow[buf][0]), 16, 0, 0);
+        const int t0 = (int)fdiv((uint32_t)(rt * RB), a.divG);
+        if (!whole_tokens) place(rt * RB - t0 * a.G);
+        const long long left = ql - 1 - t0;  // rows past the last token's are past the windows and read as zeros
+        qst.issue(buffer_window(qbase + t0 * a.ldq, (left * (long long)a.ldq + (long long)a.G * D) * (long long)sizeof(T)),
+                  lds0 + buf * 2 * kTile, wave);
+        dst.issue(buffer_window(dobase + t0 * ldo, (left * (long long)ldo + (long long)a.G * D) * (long long)sizeof(T)),
+                  lds0 + (buf * 2 + 1) * kTile, wave);
+        // the row array is padded to whole tiles; lanes past a tile's rows read zeros past the window, into the spare half
+        if (wave == 0) copy_to_lds(buffer_window(rbase + 2 * (size_t)rt * RB, RB * 8), lane * 16, lds_rows + buf * 1024);
     };
 
     const float c = a.scale_log2;
@@ -258,9 +269,14 @@ __global__ __launch_bounds__(64 * NW, 1) void kda_attn_dq_kernel(const AttnArgs 
 
     const T* kbase = reinterpret_cast<const T*>(a.k) + (size_t)b * a.Tk * a.ldk + (size_t)hk * D;
     const T* vbase = reinterpret_cast<const T*>(a.v) + (size_t)b * a.Tk * a.ldv + (size_t)hk * D;
+    Stage<T, D, KB, NW> kst, vst;
+    kst.init(wave, lane, [&](int r) { return (uint32_t)(r * a.ldk * sizeof(T)); });
+    vst.init(wave, lane, [&](int r) { return (uint32_t)(r * a.ldv * sizeof(T)); });
+    const uint32_t lds0 = lds_address(&sm[0][0][0]);
     auto stage = [&](int kt, int buf) {
-        stage_rows<T, D, KB, NW>(sm[buf][0], wave, lane, [&](int r) { return kbase + (size_t)min(kt * KB + r, kl - 1) * a.ldk; });
-        stage_rows<T, D, KB, NW>(sm[buf][1], wave, lane, [&](int r) { return vbase + (size_t)min(kt * KB + r, kl - 1) * a.ldv; });
+        const long long k0 = (long long)kt * KB, left = kl - 1 - k0;
+        kst.issue(buffer_window(kbase + k0 * a.ldk, (left * (long long)a.ldk + D) * (long long)sizeof(T)), lds0 + buf * 2 * kTile, wave);
+        vst.issue(buffer_window(vbase + k0 * a.ldv, (left * (long long)a.ldv + D) * (long long)sizeof(T)), lds0 + (buf * 2 + 1) * kTile, wave);
     };
     const float c = a.scale_log2;
     if (k_beg < k_end) stage(k_beg, 0);

@@ -74,25 +74,49 @@ template <typename T, int D> struct TileGeom {
     static constexpr int ND = D / 16;                       // 16-channel blocks
 };
 
-// Copy ROWS rows of D elements into an LDS tile straight from memory (one wave
-// instruction moves 64 granules); row_ptr(r) gives the address of row r of the
-// tile, which must be readable for every r (callers clamp).
-template <typename T, int D, int ROWS, int NW, typename RowPtr>
-__device__ __forceinline__ void stage_rows(unsigned char* tile, int wave, int lane, RowPtr row_ptr) {
-    constexpr int GR = TileGeom<T, D>::GR, N = ROWS * GR / 64;
-    static_assert(ROWS * GR % 64 == 0, "whole wave instructions");
-#pragma unroll
-    for (int c = 0; c < (N + NW - 1) / NW; ++c) {
-        const int piece = c * NW + wave;
-        if (N % NW == 0 || piece < N) {
-            const int idx = piece * 64 + lane, row = idx / GR, pos = idx % GR;
-            const unsigned char* src = reinterpret_cast<const unsigned char*>(row_ptr(row)) +
-                                       (size_t)((pos ^ (attn_swz(row) & (GR - 1))) * 16);
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                             (__attribute__((address_space(3))) void*)(tile + piece * 1024), 16, 0, 0);
-        }
-    }
+// A window of memory for buffer loads: reads at or past `bytes` give zero.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ u32x4 buffer_window(const void* p, long long bytes) {
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    const uint32_t n = bytes <= 0 ? 0u : bytes > 0xffffffffll ? 0xffffffffu : (uint32_t)bytes;
+    return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)a), (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(a >> 32)) & 0xffffu,
+                 (uint32_t)__builtin_amdgcn_readfirstlane(n), 0x00020000u};
 }
+
+// 16 bytes a lane from window + off into LDS at lds + 16 * lane.  Written as
+// assembly because the compiler, seeing the copy, would wait for all copies in
+// flight (the next tile's) before the transposing reads of the current one.  It has
+// no output registers; the kernels wait with wait_vmcnt and a barrier.  m0, which
+// holds the LDS address, is set at every use and used by nothing else here.
+__device__ __forceinline__ void copy_to_lds(const u32x4& window, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(window) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return (uint32_t)reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)p);
+}
+
+// Copies of ROWS-row tiles into LDS by NW waves: one wave instruction moves 64
+// granules.  row_off(r) is the byte offset of the tile's row r in the window.
+template <typename T, int D, int ROWS, int NW> struct Stage {
+    static constexpr int GR = TileGeom<T, D>::GR, N = ROWS * GR / 64, PER = (N + NW - 1) / NW;
+    static_assert(ROWS * GR % 64 == 0, "whole wave instructions");
+    uint32_t off[PER];
+    static __device__ __forceinline__ int row(int c, int wave, int lane) { return ((c * NW + wave) * 64 + lane) / GR; }
+    // byte offset within its row of the granule that lands at this lane's place
+    static __device__ __forceinline__ uint32_t col(int c, int wave, int lane) {
+        return (uint32_t)(((lane % GR) ^ (attn_swz(row(c, wave, lane)) & (GR - 1))) * 16);
+    }
+    template <typename RowOff> __device__ __forceinline__ void init(int wave, int lane, RowOff row_off) {
+#pragma unroll
+        for (int c = 0; c < PER; ++c) off[c] = row_off(row(c, wave, lane)) + col(c, wave, lane);
+    }
+    __device__ __forceinline__ void issue(const u32x4& window, uint32_t tile, int wave) const {
+#pragma unroll
+        for (int c = 0; c < PER; ++c)
+            if (N % NW == 0 || c * NW + wave < N) copy_to_lds(window, off[c], tile + (c * NW + wave) * 1024);
+    }
+};
 
 // Row fragment of rows [r0, r0 + 16) for contraction step s.
 template <int D>

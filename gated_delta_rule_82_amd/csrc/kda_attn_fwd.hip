@@ -67,10 +67,15 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void kda_attn_fwd_kernel(
 
     const T* kbase = reinterpret_cast<const T*>(a.k) + (size_t)b * a.Tk * a.ldk + (size_t)hk * D;
     const T* vbase = reinterpret_cast<const T*>(a.v) + (size_t)b * a.Tk * a.ldv + (size_t)hk * D;
+    // keys past the length are past the windows and read as zeros
+    Stage<T, D, KB, NW> kst, vst;
+    kst.init(wave, lane, [&](int r) { return (uint32_t)(r * a.ldk * sizeof(T)); });
+    vst.init(wave, lane, [&](int r) { return (uint32_t)(r * a.ldv * sizeof(T)); });
+    const uint32_t lds0 = lds_address(&sm[0][0][0]);
     auto stage = [&](int kt, int buf) {
-        // keys past the length repeat the last one (their scores are masked)
-        stage_rows<T, D, KB, NW>(sm[buf][0], wave, lane, [&](int r) { return kbase + (size_t)min(kt * KB + r, kl - 1) * a.ldk; });
-        stage_rows<T, D, KB, NW>(sm[buf][1], wave, lane, [&](int r) { return vbase + (size_t)min(kt * KB + r, kl - 1) * a.ldv; });
+        const long long k0 = (long long)kt * KB, left = kl - 1 - k0;
+        kst.issue(buffer_window(kbase + k0 * a.ldk, (left * (long long)a.ldk + D) * (long long)sizeof(T)), lds0 + buf * 2 * kTile, wave);
+        vst.issue(buffer_window(vbase + k0 * a.ldv, (left * (long long)a.ldv + D) * (long long)sizeof(T)), lds0 + (buf * 2 + 1) * kTile, wave);
     };
 
     const float c = a.scale_log2;
@@ -195,39 +200,56 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void kda_attn_fwd_kernel(
     }
 }
 
-// A thread takes four channels of one packed row over all splits.
+// One workgroup per packed row.  The splits' maxima and sums are read at once, one
+// a thread; then 256 / (D / 4) groups of threads take every so-manieth split's
+// output, four channels each, and are summed in LDS in a fixed order.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void kda_attn_join_kernel(const JoinArgs a) {
-    constexpr int L = D / 4;
-    const int rows = a.Tq * a.G;
-    const size_t n = (size_t)a.B * a.HK * rows, at = ((size_t)blockIdx.x * 256 + threadIdx.x) / L;
-    const int d = (threadIdx.x % L) * 4;
-    if (at >= n) return;
-    const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
-    float m = kNegInf;
-    for (int s = 0; s < a.nsplit; ++s) m = fmaxf(m, ml[s * n + at].x);
-    const float mu = m == kNegInf ? 0.f : m;
-    float sum = 0.f;
+    constexpr int L = D / 4, NG = 256 / L;
+    __shared__ float weight[kMaxSplits];
+    __shared__ float red[2][4];
+    __shared__ floatx4 part[NG][L];
+    const int rows = a.Tq * a.G, tid = threadIdx.x;
+    const size_t n = (size_t)a.B * a.HK * rows, at = blockIdx.x;
+    const float2 x = tid < a.nsplit ? reinterpret_cast<const float2*>(a.part_ml)[tid * n + at] : make_float2(kNegInf, 0.f);
+    float m = x.x;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+    if ((tid & 63) == 0) red[0][tid >> 6] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+    const float w = exp2_fast(x.x - (m == kNegInf ? 0.f : m));
+    float sum = w == 0.f ? 0.f : w * x.y;  // a part that saw nothing takes no part
+    if (tid < a.nsplit) weight[tid] = w;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+    if ((tid & 63) == 0) red[1][tid >> 6] = sum;
+    __syncthreads();
+    sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+    const int grp = tid / L, d = (tid % L) * 4;
     floatx4 o = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < a.nsplit; ++s) {
-        const float2 x = ml[s * n + at];
-        const float w = exp2_fast(x.x - mu);
-        if (w == 0.f) continue;  // a part that saw nothing (its output is not read)
-        sum = fmaf(w, x.y, sum);
-        o += w * *reinterpret_cast<const floatx4*>(a.part_o + (s * n + at) * D + d);
+#pragma unroll 4
+    for (int s = grp; s < a.nsplit; s += NG) {
+        const float f = weight[s];
+        const floatx4 y = *reinterpret_cast<const floatx4*>(a.part_o + (s * n + at) * D + d);
+        o += f == 0.f ? floatx4{0.f, 0.f, 0.f, 0.f} : f * y;
     }
+    part[grp][tid % L] = o;
+    __syncthreads();
+    if (grp != 0) return;
+    for (int i = 1; i < NG; ++i) o += part[i][tid];
     const int r = (int)(at % rows), bh = (int)(at / rows), b = bh / a.HK, hk = bh % a.HK;
     const int t = (int)fdiv((uint32_t)r, a.divG), h = hk * a.G + (r - t * a.G);
     const float inv = 1.f / sum;
-    store4(reinterpret_cast<T*>(a.o) + (((size_t)b * a.Tq + t) * a.H + h) * D + d, sum == 0.f ? o : o * inv);
-    if (a.lse && d == 0)
+    store4(reinterpret_cast<T*>(a.o) + (((size_t)b * a.Tq + t) * a.H + h) * D + d, sum == 0.f ? floatx4{0.f, 0.f, 0.f, 0.f} : o * inv);
+    if (a.lse && tid == 0)
         a.lse[((size_t)b * a.H + h) * a.Tq + t] = sum == 0.f ? kNegInf : (m + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
 template <typename T, int D>
 static hipError_t launch_join_t(const JoinArgs& a, hipStream_t s) {
-    const size_t threads = (size_t)a.B * a.HK * a.Tq * a.G * (D / 4);
-    hipLaunchKernelGGL((kda_attn_join_kernel<T, D>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, a);
+    const size_t rows = (size_t)a.B * a.HK * a.Tq * a.G;
+    hipLaunchKernelGGL((kda_attn_join_kernel<T, D>), dim3((unsigned)rows), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
