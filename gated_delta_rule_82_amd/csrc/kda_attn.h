@@ -38,7 +38,7 @@ struct AttnArgs {
     const int* q_len; const int* kv_len;      // nullable
     void* o; float* lse;
     const void* dout; void* dq; void* dk; void* dv;
-    float* rows;                // backward: (lse log2 e, dout . o) of each packed row
+    float* rows;                // backward: (-lse / scale, -dout . o) of each query
     float* part_o; float* part_ml;  // split key axis: partial outputs and (maximum, sum)
     int B, Tq, Tk, H, HK, G;
     size_t ldq, ldk, ldv;       // elements between tokens
@@ -63,7 +63,7 @@ inline int attn_fwd_splits(int elem_bytes, int B, int Tq, int Tk, int HK, int G)
     return n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : (int)n;
 }
 hipError_t launch_attn_fwd(int dt, int D, const AttnArgs& a, hipStream_t s);
-// Packed rows of one key/value head in the backward's row array.
+// The backward's row array holds a multiple of this many queries per head.
 constexpr int kAttnRowPad = 64;
 hipError_t launch_attn_bwd(int dt, int D, const AttnArgs& a, hipStream_t s);
 

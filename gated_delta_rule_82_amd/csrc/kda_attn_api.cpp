@@ -21,7 +21,7 @@ bool attn_sizes_ok(int B, int Tq, int Tk, int H, int HK) {
     // packed rows of one key/value head, and 2^24 workgroups of 64 rows or keys
     // (a grid holds less than 2^32 threads)
     const unsigned long long rows = (unsigned long long)(H / HK) * Tq, bh = (unsigned long long)B * HK;
-    return rows <= (1ull << 30) && bh * (rows / 64 + 1) < (1ull << 24) && bh * ((unsigned long long)Tk / 64 + 1) < (1ull << 24);
+    return rows <= (1ull << 29) && Tk <= (1 << 29) && bh * (rows / 64 + 1) < (1ull << 24) && bh * ((unsigned long long)Tk / 64 + 1) < (1ull << 24);
 }
 
 // Row stride in elements: 0 selects contiguous tokens.
@@ -60,15 +60,13 @@ size_t split_bytes(int n, size_t rows, int D) {
     return n <= 1 ? 0 : round256((size_t)n * rows * D * 4) + round256((size_t)n * rows * 8);
 }
 
-// Packed rows of the backward's row array, padded to whole tiles per head.
-size_t padded_rows(int Tq, int G) {
-    return ((size_t)Tq * G + kda::kAttnRowPad - 1) / kda::kAttnRowPad * kda::kAttnRowPad;
-}
+// Queries per head in the backward's row array.
+size_t padded_rows(int Tq) { return ((size_t)Tq + kda::kAttnRowPad - 1) / kda::kAttnRowPad * kda::kAttnRowPad; }
 
 bool scale_ok(float s) { return s > 0.f && isfinite((float)(s * kLog2eD)); }  // the kernels use it times log2 e
 
-// A window no shorter than every position's distance to the first key hides nothing.
-int clamp_window(int w) { return w >= (1 << 30) ? 0 : w; }
+// A window as long as the key axis hides nothing.
+int clamp_window(int w, int keys) { return w >= keys ? 0 : w; }
 
 }  // namespace
 
@@ -173,7 +171,7 @@ kda_status kda_attn_fwd(const void* q, const void* k, const void* v, const int* 
     a.q = q; a.k = k; a.v = v; a.q_len = q_len; a.kv_len = kv_len; a.o = o; a.lse = lse;
     a.B = B; a.Tq = Tq; a.Tk = Tk; a.H = H; a.HK = HK; a.G = H / HK;
     a.scale = scale; a.scale_log2 = (float)(scale * kLog2eD);
-    a.causal = causal ? 1 : 0; a.window = clamp_window(window);
+    a.causal = causal ? 1 : 0; a.window = clamp_window(window, Tk);
     a.divG = kda::fast_div((uint32_t)a.G);
     a.nsplit = kda::attn_fwd_splits(elem_bytes(dt), B, Tq, Tk, HK, a.G);
     if (a.nsplit > 1) {
@@ -185,7 +183,7 @@ kda_status kda_attn_fwd(const void* q, const void* k, const void* v, const int* 
 
 size_t kda_attn_bwd_workspace(int B, int Tq, int Tk, int H, int HK, int D, kda_dtype dt) {
     if (!dtype_ok(dt) || !dim_ok(D) || !attn_sizes_ok(B, Tq, Tk, H, HK) || B == 0 || H == 0 || Tq == 0) return 0;
-    return round256((size_t)B * HK * padded_rows(Tq, H / HK) * 8);
+    return round256((size_t)B * H * padded_rows(Tq) * 8);
 }
 
 kda_status kda_attn_bwd(const void* q, const void* k, const void* v, const int* q_len, const int* kv_len,
@@ -217,7 +215,7 @@ kda_status kda_attn_bwd(const void* q, const void* k, const void* v, const int* 
     a.dout = dout; a.dq = dq; a.dk = dk; a.dv = dv; a.rows = reinterpret_cast<float*>(workspace);
     a.B = B; a.Tq = Tq; a.Tk = Tk; a.H = H; a.HK = HK; a.G = H / HK;
     a.scale = scale; a.scale_log2 = (float)(scale * kLog2eD);
-    a.causal = causal ? 1 : 0; a.window = clamp_window(window);
+    a.causal = causal ? 1 : 0; a.window = clamp_window(window, Tk);
     a.divG = kda::fast_div((uint32_t)a.G);
     a.nsplit = 1;
     return kda::launch_attn_bwd(dt == KDA_BF16 ? 1 : 0, D, a, stream) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
@@ -293,7 +291,7 @@ kda_status kda_attn_step(const void* q, const void* k_cache, const void* v_cache
     a.q = q; a.k_cache = (const uint8_t*)k_cache; a.v_cache = (const uint8_t*)v_cache; a.k_scale = k_scale; a.v_scale = v_scale;
     a.block_table = block_table; a.cache_len = cache_len; a.new_len = new_len; a.o = o;
     a.n_pages = n_pages; a.max_pages = n_pages > 0 ? max_pages : 0; a.B = B; a.Tq = Tq; a.H = H; a.HK = HK; a.G = H / HK;
-    a.page = page; a.window = clamp_window(window);
+    a.page = page; a.window = clamp_window(window, max_len);
     a.scale_log2 = (float)(scale * kLog2eD);
     a.divG = kda::fast_div((uint32_t)a.G);
     a.nsplit = kda::attn_step_splits(B, Tq, HK, a.G, max_len);

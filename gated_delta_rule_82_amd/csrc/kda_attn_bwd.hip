@@ -14,17 +14,18 @@
 
 namespace kda {
 
-// Row values of every packed row, padded per head to whole tiles with rows that
-// contribute nothing (lse = +inf makes P zero): rows[bh][r] = (lse log2 e, delta).
+// Row values of every query, padded per head to whole tiles with rows that
+// contribute nothing: -lse / c and -delta, the initial accumulators of the products
+// that give S - lse / c and dP - delta (-inf makes P zero).  Four queries' values of
+// each kind lie together: rows[b][h][t / 4][kind][t % 4].
 template <typename T, int D>
 __global__ __launch_bounds__(256) void kda_attn_rows_kernel(const AttnArgs a, int padded) {
     constexpr int N = Gran16<T>::N, L = D / N;   // elements and lanes per row
-    const size_t at = ((size_t)blockIdx.x * 256 + threadIdx.x) / L;
+    const size_t at = ((size_t)blockIdx.x * 256 + threadIdx.x) / L;   // heads fastest, as the tensors lie
     const int part = threadIdx.x % L;
-    const size_t n = (size_t)a.B * a.HK * padded;
+    const size_t n = (size_t)a.B * a.H * padded;
     const bool inside = at < n;
-    const int r = (int)(at % padded), bh = (int)(at / padded), b = bh / a.HK, hk = bh % a.HK;
-    const int t = (int)fdiv((uint32_t)r, a.divG), h = hk * a.G + (r - t * a.G);
+    const int h = (int)(at % a.H), t = (int)(at / a.H % padded), b = (int)(at / a.H / padded);
     const bool live = inside && t < seq_len(a.q_len, inside ? b : 0, a.Tq);
     float sum = 0.f, lse = kNegInf;
     if (live) {
@@ -39,60 +40,73 @@ __global__ __launch_bounds__(256) void kda_attn_rows_kernel(const AttnArgs a, in
     for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
     if (inside && part == 0) {
         const bool none = !live || lse == kNegInf;
-        *reinterpret_cast<float2*>(a.rows + 2 * at) = none ? make_float2(-kNegInf, 0.f) : make_float2(lse * kLog2e, sum);
+        float* to = a.rows + ((size_t)b * a.H + h) * padded * 2 + (t >> 2) * 8 + (t & 3);
+        to[0] = none ? kNegInf : -lse / a.scale;
+        to[4] = none ? 0.f : -sum;
     }
 }
 
-// dk and dv of a tile of 16 NK NW keys.  Keys are the columns of S = Q K^T and
+// dk and dv of a tile of 16 NK NG keys.  Keys are the columns of S = Q K^T and
 // dP = dO V^T, so the probabilities are right operands of dV^T += dO^T P and
-// dK^T += Q^T dS as they stand; a wave keeps its keys' fragments of K and V and
-// both accumulators in registers while 32 RB / 32 packed rows at a time pass through
-// a two-deep LDS ring.
-template <typename T, int D, int NK, int RB, int NW>
-__global__ __launch_bounds__(64 * NW, 1) void kda_attn_dkv_kernel(const AttnArgs a, int padded) {
+// dK^T += Q^T dS as they stand.  The 4 waves are NG groups of keys times 4 / NG turns:
+// a wave keeps its keys' fragments of K and V and both accumulators in registers
+// and takes every (4 / NG)-th step of 32 queries from a two-deep LDS ring, head after
+// head of those that share the keys; the turns are summed in LDS at the end, in order.
+template <typename T, int D, int NK, int NG, int RB>
+__global__ __launch_bounds__(256, 2) void kda_attn_dkv_kernel(const AttnArgs a, int padded) {
     typedef TileGeom<T, D> G_;
-    constexpr int NS = G_::NS, ND = G_::ND, BK = 16 * NK * NW;
+    constexpr int NW = 4, NT = NW / NG, NS = G_::NS, ND = G_::ND, BK = 16 * NK * NG;
+    // contraction steps whose K and V fragments stay in registers; at D = 128 half of
+    // them live in LDS (a wave's own, 1 KiB a fragment), or two waves would not fit a SIMD
+    constexpr int VR = sizeof(T) == 2 && D == 128 ? 3 : NS, VL = NS - VR;
     constexpr int kTile = RB * D * (int)sizeof(T);
-    __shared__ __attribute__((aligned(16))) unsigned char sm[2][2][kTile];
+    static_assert(RB == 32 * NT && RB <= 128, "one step a wave and tile");
+    constexpr int kSum = NT > 1 ? (NT - 1) * NG * 16 * NK * D * 4 : 0;   // the other turns' sums
+    constexpr int kRing = 4 * kTile;
+    __shared__ __attribute__((aligned(16))) unsigned char sm[kRing > kSum ? kRing : kSum];
     __shared__ __attribute__((aligned(16))) float srow[2][256];  // RB pairs, and room for a whole wave's copy
-    static_assert(RB <= 128, "row values fit");
+    __shared__ __attribute__((aligned(16))) T sv[VL > 0 ? NW * 2 * NK * VL * 512 : 1];
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4;
-    const int nbh = a.B * a.HK;
-    const int bh = blockIdx.x % nbh, tile = blockIdx.x / nbh;  // early keys (seen by most rows) first
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
+    const int kgrp = wave % NG, turn = wave / NG;
+    // Under a causal mask early keys are seen by most rows.  Workgroups that share a
+    // compute unit come half a grid apart, so the second half runs backwards: a long
+    // tile's neighbour is a short one.
+    const int nbh = a.B * a.HK, ntile = (a.Tk + BK - 1) / BK, half = (ntile + 1) / 2, at_tile = blockIdx.x / nbh;
+    const int bh = blockIdx.x % nbh, tile = at_tile < half ? at_tile : ntile - 1 - (at_tile - half);
     const int b = bh / a.HK, hk = bh % a.HK;
     const int ql = seq_len(a.q_len, b, a.Tq), kl = seq_len(a.kv_len, b, a.Tk), off = kl - ql;
     const int k0 = tile * BK, k1 = min(k0 + BK, kl);  // keys of the tile inside the length
     // tokens that see some key of [k0, k1): t >= k0 - off if causal, t < k1 - 1 + window - off
     int t_lo = 0, t_hi = k0 < k1 ? ql : 0;
     if (a.causal) t_lo = max(0, k0 - off);
-    if (a.window) t_hi = min((long long)t_hi, max(0ll, (long long)k1 - 1 + a.window - off));
-    const int r_lo = t_lo < t_hi ? t_lo * a.G : 0, r_hi = t_lo < t_hi ? t_hi * a.G : 0;
-    const int beg = r_lo / RB, end = (r_hi + RB - 1) / RB;
+    if (a.window) t_hi = min(t_hi, max(0, k1 - 1 + a.window - off));
+    const int beg = t_lo / RB, per = t_lo < t_hi ? (t_hi + RB - 1) / RB - beg : 0;  // tiles of a head
+    const int steps = per * a.G;
 
-    // this lane's keys and the packed rows [rlo, rhi) that see them
-    int rlo[NK], rhi[NK];
-    Frag<T> kf[NK][NS], vf[NK][NS];
+    // the tokens [seen_from(key), seen_to(key)) that see a key (lengths and the
+    // window are below 2^29: no sum overflows)
+    auto seen_from = [&](int key) { return a.causal ? min(max(key - off, 0), ql) : 0; };
+    auto seen_to = [&](int key) { return key >= kl ? 0 : a.window ? min(max(key - off + a.window, 0), ql) : ql; };
+    Frag<T> kf[NK][VR], vf[NK][VR];
+    T* mine = sv + wave * 2 * NK * VL * 512;
     floatx4 dk[ND][NK], dv[ND][NK];
-    const int w0 = k0 + wave * 16 * NK;
-    bool some = false;
+    const int w0 = k0 + kgrp * 16 * NK, w1 = min(w0 + 16 * NK, kl);
 #pragma unroll
     for (int n = 0; n < NK; ++n) {
-        const int key = w0 + 16 * n + (lane & 15);
-        long long tl = a.causal ? (long long)key - off : 0, th = a.window ? (long long)key + a.window - off : ql;
-        tl = tl < 0 ? 0 : tl > ql ? ql : tl;
-        th = th < 0 ? 0 : th > ql ? ql : th;
-        if (key >= kl) th = 0;
-        rlo[n] = (int)tl * a.G;
-        rhi[n] = (int)th * a.G;
-        some |= rlo[n] < rhi[n];
-        const int kr = max(min(key, kl - 1), 0);
+        const int kr = max(min(w0 + 16 * n + (lane & 15), kl - 1), 0);
         const T* kp = reinterpret_cast<const T*>(a.k) + ((size_t)b * a.Tk + kr) * a.ldk + (size_t)hk * D;
         const T* vp = reinterpret_cast<const T*>(a.v) + ((size_t)b * a.Tk + kr) * a.ldv + (size_t)hk * D;
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
-            kf[n][s] = row_frag_global<T, D>(kp, s, lane);
-            vf[n][s] = row_frag_global<T, D>(vp, s, lane);
+            const Frag<T> x = row_frag_global<T, D>(kp, s, lane), y = row_frag_global<T, D>(vp, s, lane);
+            if (s < VR) {
+                kf[n][s < VR ? s : 0] = x;
+                vf[n][s < VR ? s : 0] = y;
+            } else {
+                frag_store(x, mine + ((s - VR) * 2 * NK + 2 * n) * 512, lane);
+                frag_store(y, mine + ((s - VR) * 2 * NK + 2 * n + 1) * 512, lane);
+            }
         }
 #pragma unroll
         for (int d = 0; d < ND; ++d) {
@@ -100,120 +114,144 @@ __global__ __launch_bounds__(64 * NW, 1) void kda_attn_dkv_kernel(const AttnArgs
             dv[d][n] = floatx4{0.f, 0.f, 0.f, 0.f};
         }
     }
-    const bool active = __any(some);
+    // queries that see some key of the wave, and those that see all 16 NK of them
+    const int any_lo = w0 < w1 ? seen_from(w0) : 0, any_hi = w0 < w1 ? seen_to(w1 - 1) : 0;
+    const int all_lo = seen_from(w0 + 16 * NK - 1), all_hi = w1 - w0 == 16 * NK ? seen_to(w0) : 0;
 
     const T* qbase = reinterpret_cast<const T*>(a.q) + (size_t)b * a.Tq * a.ldq + (size_t)hk * a.G * D;
     const size_t ldo = (size_t)a.H * D;
     const T* dobase = reinterpret_cast<const T*>(a.dout) + (size_t)b * a.Tq * ldo + (size_t)hk * a.G * D;
-    const float* rbase = a.rows + 2 * (size_t)bh * padded;
+    const float* rbase = a.rows + ((size_t)b * a.H + (size_t)hk * a.G) * padded * 2;
     Stage<T, D, RB, NW> qst, dst;
-    const uint32_t lds0 = lds_address(&sm[0][0][0]), lds_rows = lds_address(&srow[0][0]);
-    auto place = [&](int skip) {  // row x of a tile is packed row skip + x of the window's tokens
-        qst.init(wave, lane, [&](int x) {
-            const int t = (int)fdiv((uint32_t)(skip + x), a.divG);
-            return (uint32_t)((t * a.ldq + (size_t)(skip + x - t * a.G) * D) * sizeof(T));
-        });
-        dst.init(wave, lane, [&](int x) {
-            const int t = (int)fdiv((uint32_t)(skip + x), a.divG);
-            return (uint32_t)((t * ldo + (size_t)(skip + x - t * a.G) * D) * sizeof(T));
-        });
-    };
-    place(0);
-    const bool whole_tokens = RB % a.G == 0;  // every tile starts with a token's first head
-    auto stage = [&](int rt, int buf) {
-        const int t0 = (int)fdiv((uint32_t)(rt * RB), a.divG);
-        if (!whole_tokens) place(rt * RB - t0 * a.G);
-        const long long left = ql - 1 - t0;  // rows past the last token's are past the windows and read as zeros
-        qst.issue(buffer_window(qbase + t0 * a.ldq, (left * (long long)a.ldq + (long long)a.G * D) * (long long)sizeof(T)),
+    const uint32_t lds0 = lds_address(&sm[0]), lds_rows = lds_address(&srow[0][0]);
+    qst.init(wave, lane, [&](int x) { return (uint32_t)(x * a.ldq * sizeof(T)); });
+    dst.init(wave, lane, [&](int x) { return (uint32_t)(x * ldo * sizeof(T)); });
+    auto stage = [&](int h, int tt, int buf) {
+        const int t0 = tt * RB;
+        const long long left = ql - 1 - t0;  // queries past the last one are past the windows and read as zeros
+        qst.issue(buffer_window(qbase + t0 * a.ldq + (size_t)h * D, (left * (long long)a.ldq + D) * (long long)sizeof(T)),
                   lds0 + buf * 2 * kTile, wave);
-        dst.issue(buffer_window(dobase + t0 * ldo, (left * (long long)ldo + (long long)a.G * D) * (long long)sizeof(T)),
+        dst.issue(buffer_window(dobase + t0 * ldo + (size_t)h * D, (left * (long long)ldo + D) * (long long)sizeof(T)),
                   lds0 + (buf * 2 + 1) * kTile, wave);
-        // the row array is padded to whole tiles; lanes past a tile's rows read zeros past the window, into the spare half
-        if (wave == 0) copy_to_lds(buffer_window(rbase + 2 * (size_t)rt * RB, RB * 8), lane * 16, lds_rows + buf * 1024);
+        // the row array is padded to whole tiles; lanes past a tile's rows read zeros past the window, into the spare room
+        if (wave == 0) copy_to_lds(buffer_window(rbase + 2 * ((size_t)h * padded + t0), RB * 8), lane * 16, lds_rows + buf * 1024);
     };
 
+    const TileLane<T, D> at(lane);
     const float c = a.scale_log2;
-    if (beg < end) stage(beg, 0);
-    for (int rt = beg; rt < end; ++rt) {
-        const int buf = (rt - beg) & 1;
-        wait_vmcnt<0>();
-        lds_barrier();
-        if (rt + 1 < end) stage(rt + 1, buf ^ 1);
-        if (!active) continue;
-        const unsigned char* qs = sm[buf][0];
-        const unsigned char* ds = sm[buf][1];
+    auto step = [&](int rb, uint32_t qs, uint32_t ds, const float* rows, bool masked) {
+        // bf16: P and dS are rounded for their products, 2^-9 relative each
+        Frag<T> pf[NK], sf[NK];
 #pragma unroll
-        for (int u = 0; u < RB / 32; ++u) {
-            const int rb = rt * RB + 32 * u;
-            floatx4 st[2][NK], dp[2][NK];
+        for (int i = 0; i < 2; ++i) {
+            if (VL > 0) asm volatile("" ::: "memory");  // the second half reads its fragments again instead of keeping them
+            const floatx4* rp = reinterpret_cast<const floatx4*>(rows + 2 * (16 * i + 4 * g));
+            const floatx4 de = rp[1];
+            floatx4 st[NK], dp[NK];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int n = 0; n < NK; ++n) st[n] = rp[0];
+            if (masked) {  // -inf where the key is not seen: P and dS come out zero
 #pragma unroll
                 for (int n = 0; n < NK; ++n) {
-                    st[i][n] = floatx4{0.f, 0.f, 0.f, 0.f};
-                    dp[i][n] = floatx4{0.f, 0.f, 0.f, 0.f};
-                }
+                    const int key = w0 + 16 * n + (lane & 15), lo = seen_from(key);
+                    const uint32_t span = max(seen_to(key) - lo, 0), first = rb + 16 * i + 4 * g - lo;
 #pragma unroll
-                for (int s = 0; s < NS; ++s) {
-                    const Frag<T> qf = row_frag<D>(qs, 32 * u + 16 * i, s, lane, T());
-                    const Frag<T> df = row_frag<D>(ds, 32 * u + 16 * i, s, lane, T());
-#pragma unroll
-                    for (int n = 0; n < NK; ++n) {
-                        st[i][n] = mma(qf, kf[n][s], st[i][n]);
-                        dp[i][n] = mma(df, vf[n][s], dp[i][n]);
-                    }
+                    for (int e = 0; e < 4; ++e) st[n][e] = first + e < span ? st[n][e] : kNegInf;
                 }
             }
-            bool whole = true;  // every key of the wave is seen by every row of the step
 #pragma unroll
-            for (int n = 0; n < NK; ++n) whole &= rlo[n] <= rb && rb + 32 <= rhi[n];
-            const bool masked = !__all(whole);
+            for (int s = 0; s < NS; ++s) {
+                const Frag<T> qf = row_frag<D>(sm, qs, 16 * i, s, at, lane);
+                const Frag<T> df = row_frag<D>(sm, ds, 16 * i, s, at, lane);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float4* rp = reinterpret_cast<const float4*>(&srow[buf][2 * (32 * u + 16 * i + 4 * g)]);
-                const float4 x = rp[0], y = rp[1];
-                const float ls[4] = {x.x, x.z, y.x, y.z}, de[4] = {x.y, x.w, y.y, y.w};
-#pragma unroll
-                for (int n = 0; n < NK; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float p = exp2_fast(fmaf(st[i][n][e], c, -ls[e]));
-                        if (masked) {
-                            const int r = rb + 16 * i + 4 * g + e;
-                            p = r >= rlo[n] && r < rhi[n] ? p : 0.f;
-                        }
-                        st[i][n][e] = p;
-                        dp[i][n][e] = p == 0.f ? 0.f : p * (dp[i][n][e] - de[e]);
+                for (int n = 0; n < NK; ++n) {
+                    Frag<T> x, y;
+                    if (s < VR) {
+                        x = kf[n][s < VR ? s : 0];
+                        y = vf[n][s < VR ? s : 0];
+                    } else {
+                        frag_load(x, mine + ((s - VR) * 2 * NK + 2 * n) * 512, lane);
+                        frag_load(y, mine + ((s - VR) * 2 * NK + 2 * n + 1) * 512, lane);
                     }
+                    st[n] = mma(qf, x, st[n]);
+                    dp[n] = mma(df, y, s == 0 ? de : dp[n]);
+                }
             }
-            // bf16: P and dS are rounded for their products, 2^-9 relative each
-            Frag<T> pf[NK], sf[NK];
+#pragma unroll
+            for (int n = 0; n < NK; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    st[n][e] = exp2_fast(st[n][e] * c);
+                    dp[n][e] *= st[n][e];
+                }
+#pragma unroll
+            for (int n = 0; n < NK; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    pf[n].set(4 * i + e, st[n][e]);
+                    sf[n].set(4 * i + e, dp[n][e]);
+                }
+        }
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+            const Frag<T> dt = col_frag<D>(sm, ds, 0, d, at, lane);
+            const Frag<T> qt = col_frag<D>(sm, qs, 0, d, at, lane);
 #pragma unroll
             for (int n = 0; n < NK; ++n) {
-                pf[n] = frag_from_c<T>(st[0][n], st[1][n]);
-                sf[n] = frag_from_c<T>(dp[0][n], dp[1][n]);
-            }
-#pragma unroll
-            for (int d = 0; d < ND; ++d) {
-                const Frag<T> dt = col_frag<D>(ds, 32 * u, d, lane, T());
-                const Frag<T> qt = col_frag<D>(qs, 32 * u, d, lane, T());
-#pragma unroll
-                for (int n = 0; n < NK; ++n) {
-                    dv[d][n] = mma(dt, pf[n], dv[d][n]);
-                    dk[d][n] = mma(qt, sf[n], dk[d][n]);
-                }
+                dv[d][n] = mma(dt, pf[n], dv[d][n]);
+                dk[d][n] = mma(qt, sf[n], dk[d][n]);
             }
         }
+    };
+    int h = 0, tt = beg;
+    if (steps > 0) stage(0, beg, 0);
+    for (int it = 0; it < steps; ++it) {
+        const int buf = it & 1, t0 = tt * RB + 32 * turn;
+        if (++tt == beg + per) tt = beg, ++h;  // the next tile
+        wait_vmcnt<0>();
+        lds_barrier();
+        if (it + 1 < steps) stage(h, tt, buf ^ 1);
+        if (t0 >= any_hi || t0 + 32 <= any_lo) continue;
+        const uint32_t qs = buf * 2 * kTile + 32 * turn * D * (int)sizeof(T), ds = qs + kTile;
+        step(t0, qs, ds, &srow[buf][2 * 32 * turn], t0 < all_lo || t0 + 32 > all_hi);
+    }
+
+    if constexpr (NT > 1) {  // the other turns' sums, one of dk and dv at a time
+        float* part = reinterpret_cast<float*>(sm) + (size_t)(((turn - 1) * NG + kgrp) * 64 + lane) * 4;
+        constexpr int kStride = (NT - 1) * NG * 64 * 4;   // floats between the fragments of one lane
+        auto join = [&](floatx4 (&x)[ND][NK]) {
+            lds_barrier();
+            if (turn > 0) {
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int n = 0; n < NK; ++n) *reinterpret_cast<floatx4*>(part + (d * NK + n) * kStride) = x[d][n];
+            }
+            lds_barrier();
+            if (turn == 0) {
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int n = 0; n < NK; ++n)
+#pragma unroll
+                        for (int t = 0; t < NT - 1; ++t)
+                            x[d][n] += *reinterpret_cast<const floatx4*>(reinterpret_cast<const float*>(sm) + (d * NK + n) * kStride +
+                                                                         ((t * NG + kgrp) * 64 + lane) * 4);
+            }
+        };
+        join(dk);
+        join(dv);
+        if (turn > 0) return;
     }
 #pragma unroll
     for (int n = 0; n < NK; ++n) {
         const int key = w0 + 16 * n + (lane & 15);
         if (key >= a.Tk) continue;
-        const size_t at = (((size_t)b * a.Tk + key) * a.HK + hk) * D + 4 * g;
+        const size_t to = (((size_t)b * a.Tk + key) * a.HK + hk) * D + 4 * g;
 #pragma unroll
         for (int d = 0; d < ND; ++d) {
-            store4(reinterpret_cast<T*>(a.dk) + at + 16 * d, dk[d][n] * a.scale);
-            store4(reinterpret_cast<T*>(a.dv) + at + 16 * d, dv[d][n]);
+            store4(reinterpret_cast<T*>(a.dk) + to + 16 * d, dk[d][n] * a.scale);
+            store4(reinterpret_cast<T*>(a.dv) + to + 16 * d, dv[d][n]);
         }
     }
 }
@@ -225,9 +263,9 @@ __global__ __launch_bounds__(64 * NW, 1) void kda_attn_dq_kernel(const AttnArgs 
     typedef TileGeom<T, D> G_;
     constexpr int NS = G_::NS, ND = G_::ND, BQ = 16 * NQ * NW;
     constexpr int kTile = KB * D * (int)sizeof(T);
-    __shared__ __attribute__((aligned(16))) unsigned char sm[2][2][kTile];
+    __shared__ __attribute__((aligned(16))) unsigned char sm[4 * kTile];
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
     const int nbh = a.B * a.HK, rows = a.Tq * a.G;
     const int ntile = (rows + BQ - 1) / BQ;
     const int bh = blockIdx.x % nbh, tile = ntile - 1 - blockIdx.x / nbh;
@@ -260,9 +298,9 @@ __global__ __launch_bounds__(64 * NW, 1) void kda_attn_dq_kernel(const AttnArgs 
             qf[n][s] = row_frag_global<T, D>(qp, s, lane);
             df[n][s] = row_frag_global<T, D>(dp, s, lane);
         }
-        const float2 x = *reinterpret_cast<const float2*>(a.rows + 2 * ((size_t)bh * padded + r));
-        ls[n] = x.x;
-        de[n] = x.y;
+        const float* x = a.rows + ((size_t)b * a.H + h) * padded * 2 + (t[n] >> 2) * 8 + (t[n] & 3);
+        ls[n] = x[0] * a.scale_log2;
+        de[n] = x[4];
 #pragma unroll
         for (int d = 0; d < ND; ++d) dq[d][n] = floatx4{0.f, 0.f, 0.f, 0.f};
     }
@@ -272,12 +310,13 @@ __global__ __launch_bounds__(64 * NW, 1) void kda_attn_dq_kernel(const AttnArgs 
     Stage<T, D, KB, NW> kst, vst;
     kst.init(wave, lane, [&](int r) { return (uint32_t)(r * a.ldk * sizeof(T)); });
     vst.init(wave, lane, [&](int r) { return (uint32_t)(r * a.ldv * sizeof(T)); });
-    const uint32_t lds0 = lds_address(&sm[0][0][0]);
+    const uint32_t lds0 = lds_address(&sm[0]);
     auto stage = [&](int kt, int buf) {
         const long long k0 = (long long)kt * KB, left = kl - 1 - k0;
         kst.issue(buffer_window(kbase + k0 * a.ldk, (left * (long long)a.ldk + D) * (long long)sizeof(T)), lds0 + buf * 2 * kTile, wave);
         vst.issue(buffer_window(vbase + k0 * a.ldv, (left * (long long)a.ldv + D) * (long long)sizeof(T)), lds0 + (buf * 2 + 1) * kTile, wave);
     };
+    const TileLane<T, D> at(lane);
     const float c = a.scale_log2;
     if (k_beg < k_end) stage(k_beg, 0);
     for (int kt = k_beg; kt < k_end; ++kt) {
@@ -286,8 +325,7 @@ __global__ __launch_bounds__(64 * NW, 1) void kda_attn_dq_kernel(const AttnArgs 
         lds_barrier();
         if (kt + 1 < k_end) stage(kt + 1, buf ^ 1);
         if (k0 >= mine.key_hi || k0 + KB <= mine.key_lo) continue;
-        const unsigned char* ks = sm[buf][0];
-        const unsigned char* vs = sm[buf][1];
+        const uint32_t ks = buf * 2 * kTile, vs = ks + kTile;
         const bool masked = k0 < all_lo || k0 + KB > all_hi;
 #pragma unroll
         for (int u = 0; u < KB / 32; ++u) {
@@ -301,8 +339,8 @@ __global__ __launch_bounds__(64 * NW, 1) void kda_attn_dq_kernel(const AttnArgs 
                 }
 #pragma unroll
                 for (int s = 0; s < NS; ++s) {
-                    const Frag<T> kf = row_frag<D>(ks, 32 * u + 16 * i, s, lane, T());
-                    const Frag<T> vf = row_frag<D>(vs, 32 * u + 16 * i, s, lane, T());
+                    const Frag<T> kf = row_frag<D>(sm, ks, 32 * u + 16 * i, s, at, lane);
+                    const Frag<T> vf = row_frag<D>(sm, vs, 32 * u + 16 * i, s, at, lane);
 #pragma unroll
                     for (int n = 0; n < NQ; ++n) {
                         st[i][n] = mma(kf, qf[n][s], st[i][n]);
@@ -317,18 +355,18 @@ __global__ __launch_bounds__(64 * NW, 1) void kda_attn_dq_kernel(const AttnArgs 
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float p = exp2_fast(fmaf(st[i][n][e], c, -ls[n]));
+                        float p = exp2_fast(fmaf(st[i][n][e], c, ls[n]));
                         if (masked) {
                             const int key = k0 + 32 * u + 16 * i + 4 * g + e;
                             p = key >= lo[n] && key <= hi[n] ? p : 0.f;
                         }
-                        dp[i][n][e] = p == 0.f ? 0.f : p * (dp[i][n][e] - de[n]);
+                        dp[i][n][e] = p == 0.f ? 0.f : p * (dp[i][n][e] + de[n]);
                     }
                 sf[n] = frag_from_c<T>(dp[0][n], dp[1][n]);
             }
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
-                const Frag<T> kt_ = col_frag<D>(ks, 32 * u, d, lane, T());
+                const Frag<T> kt_ = col_frag<D>(sm, ks, 32 * u, d, at, lane);
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) dq[d][n] = mma(kt_, sf[n], dq[d][n]);
             }
@@ -349,18 +387,18 @@ __global__ __launch_bounds__(64 * NW, 1) void kda_attn_dq_kernel(const AttnArgs 
 template <typename T, int D>
 static hipError_t launch_bwd_t(const AttnArgs& a, hipStream_t s) {
     constexpr bool kWide = sizeof(T) == 2;
-    constexpr int NK = kWide ? 2 : 1, RB = kWide ? 64 : 32, NQ = kWide ? 2 : 1, KB = kWide ? 64 : 32;
+    constexpr int NK = kWide ? 2 : 1, NG = kWide ? 4 : 4, NQ = kWide ? 2 : 1, KB = kWide ? 64 : 32;
     const long long rows = (long long)a.Tq * a.G, nbh = (long long)a.B * a.HK;
-    const int padded = (int)((rows + kAttnRowPad - 1) / kAttnRowPad * kAttnRowPad);
+    const int padded = (a.Tq + kAttnRowPad - 1) / kAttnRowPad * kAttnRowPad;
     if (rows > 0) {
-        const size_t threads = (size_t)nbh * padded * (D * sizeof(T) / 16);
+        const size_t threads = (size_t)a.B * a.H * padded * (D * sizeof(T) / 16);
         hipLaunchKernelGGL((kda_attn_rows_kernel<T, D>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, a, padded);
         if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
     }
     if (a.Tk > 0) {
-        constexpr int BK = 16 * NK * 4;
+        constexpr int BK = 16 * NK * NG;
         const long long tiles = ((long long)a.Tk + BK - 1) / BK;
-        hipLaunchKernelGGL((kda_attn_dkv_kernel<T, D, NK, RB, 4>), dim3((unsigned)(tiles * nbh)), dim3(256), 0, s, a, padded);
+        hipLaunchKernelGGL((kda_attn_dkv_kernel<T, D, NK, NG, 128 / NG>), dim3((unsigned)(tiles * nbh)), dim3(256), 0, s, a, padded);
         if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
     }
     if (rows > 0) {

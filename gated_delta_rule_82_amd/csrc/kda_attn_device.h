@@ -118,32 +118,43 @@ template <typename T, int D, int ROWS, int NW> struct Stage {
     }
 };
 
-// Row fragment of rows [r0, r0 + 16) for contraction step s.
-template <int D>
-__device__ __forceinline__ Frag<bf16_t> row_frag(const unsigned char* tile, int r0, int s, int lane, bf16_t) {
-    constexpr int GR = TileGeom<bf16_t, D>::GR;
-    const int row = r0 + (lane & 15), g = lane >> 4;
-    Frag<bf16_t> f;
-    if constexpr (D >= 32) {
-        f.v = *reinterpret_cast<const bf16x8*>(tile + row * (D * 2) + (((4 * s + g) ^ (attn_swz(row) & (GR - 1))) * 16));
-    } else {
-        f.v = *reinterpret_cast<const bf16x8*>(tile + row * (D * 2) + (((g & 1) ^ (attn_swz(row) & (GR - 1))) * 16));
-        if (g >= 2) f.zero();  // 16 channels fill half a step
+// A lane's place in a tile: byte offset of its granule of row l % 16 at
+// contraction step 0 and, for column fragments of bf16, of the four columns it
+// loads of row 4 (l / 16) + (l / 4) % 4 at column block 0.  Steps and blocks differ
+// by an exclusive or within the row (`tile` and r0 move whole rows), so that only
+// these two values are kept and the others cost one instruction at their use.
+template <typename T, int D> struct TileLane {
+    static constexpr int RB = D * (int)sizeof(T);   // bytes per row
+    uint32_t row, col;
+    __device__ __forceinline__ explicit TileLane(int lane) {
+        constexpr int GR = TileGeom<T, D>::GR;
+        const int r = lane & 15, g = lane >> 4, i = lane & 3;
+        const int c = sizeof(T) == 2 ? (D >= 32 ? g : g & 1) : (D >= 32 ? 2 * g : 2 * (g & 1));
+        row = r * RB + ((c ^ (attn_swz(r) & (GR - 1))) * 16);
+        const int q = 4 * g + ((lane >> 2) & 3);
+        col = q * RB + (((i >> 1) ^ (attn_swz(q) & (GR - 1))) * 16) + (i & 1) * 8;
     }
+};
+
+// Row fragment of rows [r0, r0 + 16) of the tile at byte `tile` of `sm`, contraction step s.
+template <int D>
+__device__ __forceinline__ Frag<bf16_t> row_frag(const unsigned char* sm, uint32_t tile, int r0, int s, const TileLane<bf16_t, D>& l,
+                                                 int lane) {
+    Frag<bf16_t> f;
+    f.v = *reinterpret_cast<const bf16x8*>(sm + ((l.row + tile) ^ (64 * s)) + r0 * (D * 2));
+    if (D < 32 && (lane >> 4) >= 2) f.zero();  // 16 channels fill half a step
     return f;
 }
 template <int D>
-__device__ __forceinline__ Frag<float> row_frag(const unsigned char* tile, int r0, int s, int lane, float) {
-    constexpr int GR = TileGeom<float, D>::GR;
-    const int row = r0 + (lane & 15), g = lane >> 4, x = attn_swz(row) & (GR - 1);
-    const int c = D >= 32 ? 8 * s + 2 * g : 2 * (g & 1);
-    const unsigned char* p = tile + row * (D * 4);
-    const float4 a = *reinterpret_cast<const float4*>(p + ((c ^ x) * 16));
-    const float4 b = *reinterpret_cast<const float4*>(p + (((c + 1) ^ x) * 16));
+__device__ __forceinline__ Frag<float> row_frag(const unsigned char* sm, uint32_t tile, int r0, int s, const TileLane<float, D>& l,
+                                                int lane) {
+    const uint32_t o = (l.row + tile) ^ (128 * s);
+    const float4 a = *reinterpret_cast<const float4*>(sm + o + r0 * (D * 4));
+    const float4 b = *reinterpret_cast<const float4*>(sm + (o ^ 16) + r0 * (D * 4));
     Frag<float> f;
     f.v[0] = a.x; f.v[1] = a.y; f.v[2] = a.z; f.v[3] = a.w;
     f.v[4] = b.x; f.v[5] = b.y; f.v[6] = b.z; f.v[7] = b.w;
-    if (D < 32 && g >= 2) f.zero();
+    if (D < 32 && (lane >> 4) >= 2) f.zero();
     return f;
 }
 
@@ -161,33 +172,31 @@ __device__ __forceinline__ Frag<T> row_frag_global(const T* p, int s, int lane) 
     return f;
 }
 
-// Column fragment: column 16 c + l % 16 of the 32 rows from r0.
+// Column fragment: column 16 c + l % 16 of the 32 rows from r0 of the tile.
 template <int D>
-__device__ __forceinline__ Frag<bf16_t> col_frag(const unsigned char* tile, int r0, int c, int lane, bf16_t) {
-    constexpr int GR = TileGeom<bf16_t, D>::GR;
+__device__ __forceinline__ Frag<bf16_t> col_frag(const unsigned char* sm, uint32_t tile, int r0, int c, const TileLane<bf16_t, D>& l,
+                                                 int) {
     typedef short s16x4 __attribute__((ext_vector_type(4)));
-    typedef s16x4 __attribute__((address_space(3)))* lds4;
-    const int row = r0 + 4 * (lane >> 4) + ((lane >> 2) & 3), i = lane & 3;
-    // lane i of a 16-lane group loads 4 columns of row i / 4 and receives column i of the four rows
-    const int off = row * (D * 2) + (((2 * c + (i >> 1)) ^ (attn_swz(row) & (GR - 1))) * 16) + (i & 1) * 8;
-    const int row2 = row + 16;
-    const int off2 = row2 * (D * 2) + (((2 * c + (i >> 1)) ^ (attn_swz(row2) & (GR - 1))) * 16) + (i & 1) * 8;
-    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(tile + off));
-    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(tile + off2));
     typedef short s16x8 __attribute__((ext_vector_type(8)));
+    typedef s16x4 __attribute__((address_space(3)))* lds4;
+    // lane i of a 16-lane group loads 4 columns of row i / 4 and receives column i of the four rows
+    const unsigned char* p = sm + ((l.col + tile) ^ (32 * c)) + r0 * (D * 2);
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p));
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + 16 * (D * 2)));
     Frag<bf16_t> f;
     f.v = __builtin_bit_cast(bf16x8, s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
     return f;
 }
 template <int D>
-__device__ __forceinline__ Frag<float> col_frag(const unsigned char* tile, int r0, int c, int lane, float) {
+__device__ __forceinline__ Frag<float> col_frag(const unsigned char* sm, uint32_t tile, int r0, int c, const TileLane<float, D>&,
+                                                int lane) {
     constexpr int GR = TileGeom<float, D>::GR;
     const int col = 16 * c + (lane & 15), g = lane >> 4;
     Frag<float> f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const int row = r0 + slot_index(g, j);
-        f.v[j] = *reinterpret_cast<const float*>(tile + row * (D * 4) +
+        f.v[j] = *reinterpret_cast<const float*>(sm + tile + row * (D * 4) +
                                                  (((col >> 2) ^ (attn_swz(row) & (GR - 1))) * 16) + (col & 3) * 4);
     }
     return f;

@@ -19,9 +19,9 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void kda_attn_fwd_kernel(
     typedef TileGeom<T, D> G_;
     constexpr int NS = G_::NS, ND = G_::ND, NT = KB / 16, BQ = 16 * NQ * NW;
     constexpr int kTile = KB * D * (int)sizeof(T);
-    __shared__ __attribute__((aligned(16))) unsigned char sm[2][2][kTile];
+    __shared__ __attribute__((aligned(16))) unsigned char sm[4 * kTile];
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
     // head fastest: the tiles of one key/value head run on one XCD when the
     // heads are a multiple of 8; late rows (the longest under a causal mask) first
     const int nbh = a.B * a.HK, rows = a.Tq * a.G;
@@ -71,13 +71,14 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void kda_attn_fwd_kernel(
     Stage<T, D, KB, NW> kst, vst;
     kst.init(wave, lane, [&](int r) { return (uint32_t)(r * a.ldk * sizeof(T)); });
     vst.init(wave, lane, [&](int r) { return (uint32_t)(r * a.ldv * sizeof(T)); });
-    const uint32_t lds0 = lds_address(&sm[0][0][0]);
+    const uint32_t lds0 = lds_address(&sm[0]);
     auto stage = [&](int kt, int buf) {
         const long long k0 = (long long)kt * KB, left = kl - 1 - k0;
         kst.issue(buffer_window(kbase + k0 * a.ldk, (left * (long long)a.ldk + D) * (long long)sizeof(T)), lds0 + buf * 2 * kTile, wave);
         vst.issue(buffer_window(vbase + k0 * a.ldv, (left * (long long)a.ldv + D) * (long long)sizeof(T)), lds0 + (buf * 2 + 1) * kTile, wave);
     };
 
+    const TileLane<T, D> place(lane);
     const float c = a.scale_log2;
     float m[NQ], l[NQ];
     floatx4 o[ND][NQ];
@@ -96,8 +97,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void kda_attn_fwd_kernel(
         lds_barrier();  // tile kt has landed; every wave is done with the other buffer
         if (kt + 1 < k_end) stage(kt + 1, buf ^ 1);
         if (k0 >= mine.key_hi || k0 + KB <= mine.key_lo) continue;  // nothing for this wave's rows
-        const unsigned char* ks = sm[buf][0];
-        const unsigned char* vs = sm[buf][1];
+        const uint32_t ks = buf * 2 * kTile, vs = ks + kTile;
 
         floatx4 st[NT][NQ];
 #pragma unroll
@@ -108,7 +108,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void kda_attn_fwd_kernel(
         for (int s = 0; s < NS; ++s)
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                const Frag<T> kf = row_frag<D>(ks, 16 * i, s, lane, T());
+                const Frag<T> kf = row_frag<D>(sm, ks, 16 * i, s, place, lane);
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) st[i][n] = mma(kf, qf[n][s], st[i][n]);
             }
@@ -165,7 +165,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void kda_attn_fwd_kernel(
         for (int i = 0; i < NT / 2; ++i)
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
-                const Frag<T> vf = col_frag<D>(vs, 32 * i, d, lane, T());
+                const Frag<T> vf = col_frag<D>(sm, vs, 32 * i, d, place, lane);
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) o[d][n] = mma(vf, pf[i][n], o[d][n]);
             }

@@ -174,7 +174,7 @@ __global__ __launch_bounds__(64 * kStepWaves) void kda_attn_step_kernel(const At
     __shared__ __attribute__((aligned(16))) float so[NW][16][D + 4];
     __shared__ float sml[NW][16][2];
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, lr = lane & 15;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, lr = lane & 15;
     const int nbh = a.B * a.HK, rows = a.Tq * a.G;
     int bid = blockIdx.x;
     const int bh = bid % nbh;

@@ -26,7 +26,7 @@ hipError_t launch_rotary(int, const RotaryArgs& a, hipStream_t) {
 }
 static void attn_sizes(const AttnArgs& a) {
     expect(a.G >= 1 && a.H == a.G * a.HK && a.nsplit >= 1, "attention sizes");
-    expect((unsigned long long)a.Tq * a.G <= (1ull << 30) && a.window >= 0 && a.window < (1 << 30), "attention rows");
+    expect((unsigned long long)a.Tq * a.G <= (1ull << 29) && a.Tk <= (1 << 29) && a.window >= 0 && (a.window == 0 || a.window < a.Tk), "attention rows");
     expect(a.nsplit == 1 || (a.part_o && a.part_ml), "attention partials");
 }
 hipError_t launch_attn_fwd(int, int, const AttnArgs& a, hipStream_t) { ++g_launches; attn_sizes(a); return hipSuccess; }
@@ -38,7 +38,7 @@ hipError_t launch_cache_append(int, int, const AppendArgs& a, hipStream_t) {
 }
 hipError_t launch_attn_step(int, int, const AttnStepArgs& a, hipStream_t) {
     ++g_launches;
-    expect((long long)a.max_pages * a.page <= (1 << 30) && a.nsplit >= 1, "step sizes");
+    expect((long long)a.max_pages * a.page <= (1 << 29) && a.nsplit >= 1, "step sizes");
     return hipSuccess;
 }
 }  // namespace kda

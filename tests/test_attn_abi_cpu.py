@@ -189,5 +189,5 @@ def test_workspace_sizes(lib):
     assert lib.kda_attn_fwd_workspace(4, 4096, 4096, 16, 4, 128, 1) == 0          # enough rows to fill the card
     assert lib.kda_attn_step_workspace(256, 1, 32, 8, 128, 65536) == 0
     assert lib.kda_attn_step_workspace(1, 1, 8, 3, 128, 65536) == 0
-    # two floats for each packed row, the rows of a key/value head padded to 64
-    assert lib.kda_attn_bwd_workspace(2, 33, 50, 4, 2, 64, 1) == 2 * 2 * 128 * 8
+    # two floats for each query, a head's padded to 64
+    assert lib.kda_attn_bwd_workspace(2, 33, 50, 4, 2, 64, 1) == 2 * 4 * 64 * 8
