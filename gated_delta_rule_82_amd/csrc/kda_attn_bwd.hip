@@ -46,6 +46,34 @@ __global__ __launch_bounds__(256) void kda_attn_rows_kernel(const AttnArgs a, in
     }
 }
 
+// Adds the accumulators of the waves that took the other turns, through LDS, in
+// the order of the turns; turn 0 is left with the sums.
+template <int NG, int NT, int ND, int N>
+__device__ __forceinline__ void join_turns(float* lds, floatx4 (&x)[ND][N], int group, int turn, int lane) {
+    constexpr int kStride = (NT - 1) * NG * 64 * 4;   // floats between the fragments of one lane
+    lds_barrier();  // the previous use of the LDS is over
+    if (turn > 0) {
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+                *reinterpret_cast<floatx4*>(lds + (d * N + n) * kStride + (((turn - 1) * NG + group) * 64 + lane) * 4) = x[d][n];
+    }
+    lds_barrier();
+    if (turn == 0) {
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int t = 0; t < NT - 1; ++t)
+                    x[d][n] += *reinterpret_cast<const floatx4*>(lds + (d * N + n) * kStride + ((t * NG + group) * 64 + lane) * 4);
+    }
+}
+
+// Grids of fewer workgroups than this leave compute units idle.
+constexpr int kSmallGrid = 256;
+
 // dk and dv of a tile of 16 NK NG keys.  Keys are the columns of S = Q K^T and
 // dP = dO V^T, so the probabilities are right operands of dV^T += dO^T P and
 // dK^T += Q^T dS as they stand.  The 4 waves are NG groups of keys times 4 / NG turns:
@@ -216,31 +244,9 @@ __global__ __launch_bounds__(256, 2) void kda_attn_dkv_kernel(const AttnArgs a, 
         step(t0, qs, ds, &srow[buf][2 * 32 * turn], t0 < all_lo || t0 + 32 > all_hi);
     }
 
-    if constexpr (NT > 1) {  // the other turns' sums, one of dk and dv at a time
-        float* part = reinterpret_cast<float*>(sm) + (size_t)(((turn - 1) * NG + kgrp) * 64 + lane) * 4;
-        constexpr int kStride = (NT - 1) * NG * 64 * 4;   // floats between the fragments of one lane
-        auto join = [&](floatx4 (&x)[ND][NK]) {
-            lds_barrier();
-            if (turn > 0) {
-#pragma unroll
-                for (int d = 0; d < ND; ++d)
-#pragma unroll
-                    for (int n = 0; n < NK; ++n) *reinterpret_cast<floatx4*>(part + (d * NK + n) * kStride) = x[d][n];
-            }
-            lds_barrier();
-            if (turn == 0) {
-#pragma unroll
-                for (int d = 0; d < ND; ++d)
-#pragma unroll
-                    for (int n = 0; n < NK; ++n)
-#pragma unroll
-                        for (int t = 0; t < NT - 1; ++t)
-                            x[d][n] += *reinterpret_cast<const floatx4*>(reinterpret_cast<const float*>(sm) + (d * NK + n) * kStride +
-                                                                         ((t * NG + kgrp) * 64 + lane) * 4);
-            }
-        };
-        join(dk);
-        join(dv);
+    if constexpr (NT > 1) {
+        join_turns<NG, NT>(reinterpret_cast<float*>(sm), dk, kgrp, turn, lane);
+        join_turns<NG, NT>(reinterpret_cast<float*>(sm), dv, kgrp, turn, lane);
         if (turn > 0) return;
     }
 #pragma unroll
@@ -257,13 +263,17 @@ __global__ __launch_bounds__(256, 2) void kda_attn_dkv_kernel(const AttnArgs a, 
 }
 
 // dq of a tile of packed rows: the forward's loop with the rows' lse in hand,
-// S^T = K Q^T and dP^T = V dO^T, then dQ^T += K^T dS^T.
-template <typename T, int D, int NQ, int KB, int NW>
-__global__ __launch_bounds__(64 * NW, 1) void kda_attn_dq_kernel(const AttnArgs a, int padded) {
+// S^T = K Q^T and dP^T = V dO^T, then dQ^T += K^T dS^T.  The 4 waves are NG groups of
+// rows times 4 / NG turns over the steps of 32 keys, summed in LDS at the end.
+template <typename T, int D, int NQ, int NG>
+__global__ __launch_bounds__(256, 1) void kda_attn_dq_kernel(const AttnArgs a, int padded) {
     typedef TileGeom<T, D> G_;
-    constexpr int NS = G_::NS, ND = G_::ND, BQ = 16 * NQ * NW;
+    constexpr int NW = 4, NT = NW / NG, NS = G_::NS, ND = G_::ND, BQ = 16 * NQ * NG;
+    constexpr int KB = sizeof(T) == 2 && NT == 1 ? 64 : 32 * NT;
     constexpr int kTile = KB * D * (int)sizeof(T);
-    __shared__ __attribute__((aligned(16))) unsigned char sm[4 * kTile];
+    constexpr int kStep = 32 * D * (int)sizeof(T);
+    constexpr int kSum = (NT - 1) * NG * 16 * NQ * D * 4;   // the other turns' sums
+    __shared__ __attribute__((aligned(16))) unsigned char sm[4 * kTile > kSum ? 4 * kTile : kSum];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
     const int nbh = a.B * a.HK, rows = a.Tq * a.G;
@@ -275,7 +285,8 @@ __global__ __launch_bounds__(64 * NW, 1) void kda_attn_dq_kernel(const AttnArgs 
     const RowRange blk = row_range(a, r0, r1, ql, kl);
     const int k_beg = blk.key_lo / KB, k_end = blk.key_hi > blk.key_lo ? (blk.key_hi + KB - 1) / KB : k_beg;
 
-    const int w0 = r0 + wave * 16 * NQ;
+    const int rgrp = wave % NG, turn = wave / NG;
+    const int w0 = r0 + rgrp * 16 * NQ;
     const RowRange mine = w0 < r1 ? row_range(a, w0, min(w0 + 16 * NQ, r1), ql, kl) : RowRange{0, -1, 0, 0};
     const int all_hi = a.causal ? min(kl, mine.t_first + off + 1) : kl;
     const int all_lo = a.window ? mine.t_last + off - a.window + 1 : 0;
@@ -328,7 +339,8 @@ __global__ __launch_bounds__(64 * NW, 1) void kda_attn_dq_kernel(const AttnArgs 
         const uint32_t ks = buf * 2 * kTile, vs = ks + kTile;
         const bool masked = k0 < all_lo || k0 + KB > all_hi;
 #pragma unroll
-        for (int u = 0; u < KB / 32; ++u) {
+        for (int v = 0; v < KB / 32 / NT; ++v) {
+            const int u = v * NT + turn;
             floatx4 st[2][NQ], dp[2][NQ];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -339,8 +351,8 @@ __global__ __launch_bounds__(64 * NW, 1) void kda_attn_dq_kernel(const AttnArgs 
                 }
 #pragma unroll
                 for (int s = 0; s < NS; ++s) {
-                    const Frag<T> kf = row_frag<D>(sm, ks, 32 * u + 16 * i, s, at, lane);
-                    const Frag<T> vf = row_frag<D>(sm, vs, 32 * u + 16 * i, s, at, lane);
+                    const Frag<T> kf = row_frag<D>(sm, ks + turn * kStep, 32 * v * NT + 16 * i, s, at, lane);
+                    const Frag<T> vf = row_frag<D>(sm, vs + turn * kStep, 32 * v * NT + 16 * i, s, at, lane);
 #pragma unroll
                     for (int n = 0; n < NQ; ++n) {
                         st[i][n] = mma(kf, qf[n][s], st[i][n]);
@@ -366,11 +378,15 @@ __global__ __launch_bounds__(64 * NW, 1) void kda_attn_dq_kernel(const AttnArgs 
             }
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
-                const Frag<T> kt_ = col_frag<D>(sm, ks, 32 * u, d, at, lane);
+                const Frag<T> kt_ = col_frag<D>(sm, ks + turn * kStep, 32 * v * NT, d, at, lane);
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) dq[d][n] = mma(kt_, sf[n], dq[d][n]);
             }
         }
+    }
+    if constexpr (NT > 1) {
+        join_turns<NG, NT>(reinterpret_cast<float*>(sm), dq, rgrp, turn, lane);
+        if (turn > 0) return;
     }
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
@@ -384,29 +400,47 @@ __global__ __launch_bounds__(64 * NW, 1) void kda_attn_dq_kernel(const AttnArgs 
     }
 }
 
+// Key or row groups of a workgroup for a grid too small to fill the card: the waves
+// then share fewer keys or rows and take turns, as far as the LDS ring reaches (its
+// tiles hold 32 rows for each turn).
+template <typename T, int D> constexpr int small_groups() { return D * (int)sizeof(T) >= 512 ? 2 : 1; }
+
+template <typename T, int D, int NG>
+static hipError_t launch_dkv(const AttnArgs& a, int padded, hipStream_t s) {
+    constexpr int NK = sizeof(T) == 2 ? 2 : 1, BK = 16 * NK * NG;
+    const long long tiles = ((long long)a.Tk + BK - 1) / BK;
+    hipLaunchKernelGGL((kda_attn_dkv_kernel<T, D, NK, NG, 128 / NG>), dim3((unsigned)(tiles * a.B * a.HK)), dim3(256), 0, s, a, padded);
+    return hipGetLastError();
+}
+template <typename T, int D, int NG>
+static hipError_t launch_dq(const AttnArgs& a, int padded, hipStream_t s) {
+    constexpr int NQ = sizeof(T) == 2 ? 2 : 1, BQ = 16 * NQ * NG;
+    const long long rows = (long long)a.Tq * a.G, tiles = (rows + BQ - 1) / BQ;
+    hipLaunchKernelGGL((kda_attn_dq_kernel<T, D, NQ, NG>), dim3((unsigned)(tiles * a.B * a.HK)), dim3(256), 0, s, a, padded);
+    return hipGetLastError();
+}
+
 template <typename T, int D>
 static hipError_t launch_bwd_t(const AttnArgs& a, hipStream_t s) {
-    constexpr bool kWide = sizeof(T) == 2;
-    constexpr int NK = kWide ? 2 : 1, NG = kWide ? 4 : 4, NQ = kWide ? 2 : 1, KB = kWide ? 64 : 32;
+    constexpr int kWide = sizeof(T) == 2 ? 128 : 64, kSmall = small_groups<T, D>();  // keys or rows of a workgroup
     const long long rows = (long long)a.Tq * a.G, nbh = (long long)a.B * a.HK;
     const int padded = (a.Tq + kAttnRowPad - 1) / kAttnRowPad * kAttnRowPad;
+    hipError_t e = hipSuccess;
     if (rows > 0) {
         const size_t threads = (size_t)a.B * a.H * padded * (D * sizeof(T) / 16);
         hipLaunchKernelGGL((kda_attn_rows_kernel<T, D>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, a, padded);
-        if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
+        if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (a.Tk > 0) {
-        constexpr int BK = 16 * NK * NG;
-        const long long tiles = ((long long)a.Tk + BK - 1) / BK;
-        hipLaunchKernelGGL((kda_attn_dkv_kernel<T, D, NK, NG, 128 / NG>), dim3((unsigned)(tiles * nbh)), dim3(256), 0, s, a, padded);
-        if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
+        const bool small = nbh * ((a.Tk + kWide - 1) / kWide) < kSmallGrid;
+        e = small ? launch_dkv<T, D, kSmall>(a, padded, s) : launch_dkv<T, D, 4>(a, padded, s);
+        if (e != hipSuccess) return e;
     }
     if (rows > 0) {
-        constexpr int BQ = 16 * NQ * 4;
-        const long long tiles = (rows + BQ - 1) / BQ;
-        hipLaunchKernelGGL((kda_attn_dq_kernel<T, D, NQ, KB, 4>), dim3((unsigned)(tiles * nbh)), dim3(256), 0, s, a, padded);
+        const bool small = nbh * ((rows + kWide - 1) / kWide) < kSmallGrid;
+        e = small ? launch_dq<T, D, kSmall>(a, padded, s) : launch_dq<T, D, 4>(a, padded, s);
     }
-    return hipGetLastError();
+    return e;
 }
 
 template <typename T>

@@ -29,76 +29,244 @@ __device__ __forceinline__ float finite_abs(float x) {
     return y < __builtin_inff() ? y : 0.f;  // infinities and NaN set no scale
 }
 
-// Code of x * inv, nearest even; infinities saturate, NaN stays NaN.
-__device__ __forceinline__ uint32_t encode(float x, float inv) {
-    float y = x * inv;
-    if (!(y != y)) y = fminf(fmaxf(y, -kE4m3Max), kE4m3Max);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y, 0.f, 0, false) & 0xffu;
+// x * inv within the codes' range: infinities saturate, NaN stays NaN.
+__device__ __forceinline__ float to_range(float x, float inv) {
+    const float y = x * inv;
+    return y != y ? y : __builtin_amdgcn_fmed3f(y, -kE4m3Max, kE4m3Max);
+}
+// Codes of four values in range, nearest even, the first in the lowest byte.
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, lo, true);
+}
+__device__ __forceinline__ uint8_t encode(float x, float inv) {
+    return (uint8_t)(__builtin_amdgcn_cvt_pk_fp8_f32(to_range(x, inv), 0.f, 0, false) & 0xff);
 }
 __device__ __forceinline__ float decode(uint32_t code) { return __builtin_amdgcn_cvt_f32_fp8((int)code, 0); }
 
-__device__ __forceinline__ float block_max(float x, float* red) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor(x, o, 64));
-    __syncthreads();  // the previous use of red is over
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
-    __syncthreads();
-    return fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-}
+// Eight consecutive elements as loaded.
+template <typename T> struct Raw8;
+template <> struct Raw8<bf16_t> {
+    uint4 v;
+    __device__ __forceinline__ void load(const bf16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ float get(int i) const { return Gran16<bf16_t>::get(v, i); }
+};
+template <> struct Raw8<float> {
+    uint4 v[2];
+    __device__ __forceinline__ void load(const float* p) {
+        v[0] = reinterpret_cast<const uint4*>(p)[0];
+        v[1] = reinterpret_cast<const uint4*>(p)[1];
+    }
+    __device__ __forceinline__ void zero() { v[0] = v[1] = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ float get(int i) const { return Gran16<float>::get(v[i >> 2], i & 3); }
+};
+
+// Threads of the append's workgroup: one for each four tokens by eight channels of
+// a page, at most 256.
+constexpr int append_items(int D, int page) { return (D / 8) * (page / 4); }
+constexpr int append_threads(int D, int page) { return append_items(D, page) >= 256 ? 256 : append_items(D, page) >= 128 ? 128 : 64; }
 
 }  // namespace
 
-// One workgroup per (sequence, key/value head, page touched).
-template <typename T, int D>
-__global__ __launch_bounds__(256) void kda_cache_append_kernel(const AppendArgs a, int touched) {
-    __shared__ float red[4];
+// One workgroup per (sequence, key/value head, page touched).  A thread holds four
+// tokens by eight channels of K and of V, so every input is read once: the maxima
+// of both are reduced together, K's codes leave as they are (8 bytes a token), V's
+// are turned into words of four tokens and leave through LDS as whole 16-byte
+// pieces of the page's rows (single bytes where tokens before or after them stay).
+template <typename T, int D, int PAGE>
+__global__ __launch_bounds__(append_threads(D, PAGE)) void kda_cache_append_kernel(const AppendArgs a, int touched) {
+    constexpr int NTH = append_threads(D, PAGE), G8 = D / 8, ITEMS = append_items(D, PAGE), U = (ITEMS + NTH - 1) / NTH;
+    constexpr int ROW = PAGE / 4 + 1;                       // words of an LDS row (odd: rows spread over the banks)
+    __shared__ float red[2][NTH / 64];
+    __shared__ uint32_t turned[D * ROW];
+    const int tid = threadIdx.x;
     const int bh = blockIdx.x / touched, j = blockIdx.x % touched;
     const int b = bh / a.HK, hk = bh % a.HK;
     const long long before = max(a.cache_len[b], 0), fresh = seq_len(a.new_len, b, a.T);
-    const long long pn = before / a.page + j, p0 = pn * a.page;   // page of the sequence and its first token
-    const long long lo = max(before, p0), hi = min(before + fresh, p0 + a.page);
+    const long long pn = before / PAGE + j, p0 = pn * PAGE;  // page of the sequence and its first token
+    const long long lo = max(before, p0), hi = min(before + fresh, p0 + PAGE);
     if (lo >= hi || pn >= a.max_pages) return;
     const int pg = a.block_table[(size_t)b * a.max_pages + pn];
-    if (pg < 0 || pg >= a.n_pages) return;
-    const size_t slot = (size_t)pg * a.HK + hk;
-    const int older = (int)(lo - p0), n = (int)(hi - lo);          // tokens there, tokens to write
-    const size_t tok = (size_t)b * a.T + (size_t)(lo - before);
+    const int older = (int)(lo - p0), end = (int)(hi - p0);  // slots [older, end) of the page are written
+    const size_t tok0 = (size_t)b * a.T + (size_t)(lo - before);
+
+    Raw8<T> xk[U][4], xv[U][4];
+    float top_k = 0.f, top_v = 0.f;
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-        const size_t ld = kv ? a.ldv : a.ldk;
-        const T* x = reinterpret_cast<const T*>(kv ? a.v : a.k) + tok * ld + (size_t)hk * D;
-        uint8_t* codes = (kv ? a.v_cache : a.k_cache) + slot * (size_t)a.page * D;
-        float* scale = (kv ? a.v_scale : a.k_scale) + slot;
-        float top = 0.f;
-        for (int i = threadIdx.x; i < n * D; i += 256) top = fmaxf(top, finite_abs(to_f<T>(x[(size_t)(i / D) * ld + i % D])));
-        float s = scale_for(block_max(top, red));
-        if (older > 0) {
-            const float was = *scale;
-            __syncthreads();  // read by every thread before one writes it
-            s = fmaxf(s, was);
-            if (s > was) {  // the tokens there move to the larger scale
-                const float r = was / s;
-                for (int i = threadIdx.x; i < older * D; i += 256) {
-                    uint8_t* p = kv ? codes + (size_t)(i % D) * a.page + i / D : codes + i;
-                    *p = (uint8_t)encode(decode(*p), r);
-                }
+    for (int u = 0; u < U; ++u) {
+        const int item = u * NTH + tid, dg = item % G8, s4 = item / G8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int slot = 4 * s4 + i;
+            if (slot >= older && slot < end) {
+                const size_t tok = tok0 + (slot - older);
+                xk[u][i].load(reinterpret_cast<const T*>(a.k) + tok * a.ldk + (size_t)hk * D + dg * 8);
+                xv[u][i].load(reinterpret_cast<const T*>(a.v) + tok * a.ldv + (size_t)hk * D + dg * 8);
+            } else {
+                xk[u][i].zero();
+                xv[u][i].zero();
             }
         }
-        const float inv = 1.f / s;
-        for (int i = threadIdx.x; i < n * D; i += 256) {
-            const int t = i / D, d = i % D;
-            uint8_t* p = kv ? codes + (size_t)d * a.page + older + t : codes + (size_t)(older + t) * D + d;
-            *p = (uint8_t)encode(to_f<T>(x[(size_t)t * ld + d]), inv);
+    }
+    if (pg < 0 || pg >= a.n_pages) return;  // no page: the tokens are dropped
+    const size_t slot0 = (size_t)pg * a.HK + hk;
+    uint8_t* kc = a.k_cache + slot0 * (PAGE * D);
+    uint8_t* vc = a.v_cache + slot0 * (PAGE * D);
+    const float was_k = older > 0 ? a.k_scale[slot0] : 0.f, was_v = older > 0 ? a.v_scale[slot0] : 0.f;
+    // this thread's four tokens hold none that is written
+    auto idle = [&](int u) {
+        const int s = 4 * ((u * NTH + tid) / G8);
+        return s + 4 <= older || s >= end;
+    };
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (idle(u)) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                top_k = fmaxf(top_k, finite_abs(xk[u][i].get(e)));
+                top_v = fmaxf(top_v, finite_abs(xv[u][i].get(e)));
+            }
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+        top_k = fmaxf(top_k, __shfl_xor(top_k, o, 64));
+        top_v = fmaxf(top_v, __shfl_xor(top_v, o, 64));
+    }
+    if ((tid & 63) == 0) {
+        red[0][tid >> 6] = top_k;
+        red[1][tid >> 6] = top_v;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NTH / 64; ++w) {
+        top_k = fmaxf(top_k, red[0][w]);
+        top_v = fmaxf(top_v, red[1][w]);
+    }
+    // never below the scale of the tokens there (one that is not a number counts as none)
+    const float sk = fmaxf(scale_for(top_k), was_k), sv = fmaxf(scale_for(top_v), was_v);
+    if (older > 0 && (sk > was_k || sv > was_v)) {  // those tokens move to the larger scale
+        const float rk = was_k / sk, rv = was_v / sv;
+        for (int i = tid; i < older * D; i += NTH) {
+            if (sk > was_k) kc[i] = encode(decode(kc[i]), rk);
+            if (sv > was_v) {
+                uint8_t* p = vc + (size_t)(i % D) * PAGE + i / D;
+                *p = encode(decode(*p), rv);
+            }
         }
-        if (threadIdx.x == 0) *scale = s;
+    }
+    const float ik = 1.f / sk, iv = 1.f / sv;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int item = u * NTH + tid, dg = item % G8, s4 = item / G8;
+        if (idle(u)) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int slot = 4 * s4 + i;
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = to_range(xk[u][i].get(e), ik);
+            if (slot >= older && slot < end)
+                *reinterpret_cast<uint2*>(kc + slot * D + dg * 8) = make_uint2(encode4(y[0], y[1], y[2], y[3]), encode4(y[4], y[5], y[6], y[7]));
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            turned[(dg * 8 + e) * ROW + s4] = encode4(to_range(xv[u][0].get(e), iv), to_range(xv[u][1].get(e), iv),
+                                                     to_range(xv[u][2].get(e), iv), to_range(xv[u][3].get(e), iv));
+    }
+    __syncthreads();
+    constexpr int C = PAGE / 16;   // 16-byte pieces of a row
+    for (int i = tid; i < D * C; i += NTH) {
+        const int d = i / C, s0 = (i % C) * 16;
+        if (s0 + 16 <= older || s0 >= end) continue;
+        const uint32_t* w = turned + d * ROW + s0 / 4;
+        uint8_t* p = vc + d * PAGE + s0;
+        if (s0 >= older && s0 + 16 <= end) {
+            *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+            for (int s = max(older - s0, 0); s < min(end - s0, 16); ++s) p[s] = (uint8_t)(w[s >> 2] >> (8 * (s & 3)));
+        }
+    }
+    if (tid == 0) {
+        a.k_scale[slot0] = sk;
+        a.v_scale[slot0] = sv;
     }
 }
 
+// One token a sequence (decode): a lane holds eight channels of K or of V, D / 8 lanes
+// each, a wave one (sequence, key/value head); no LDS and no barrier.  B = 256, 8 heads,
+// D = 128: 5 us, against 14 us with the workgroup above, whose registers for a whole
+// page let only five of them share a compute unit.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void kda_cache_append_one_kernel(const AppendArgs a) {
+    constexpr int G8 = D / 8;
+    const int lane = threadIdx.x & 63, bh = blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (bh >= a.B * a.HK) return;
+    const int b = bh / a.HK, hk = bh % a.HK;
+    const bool kv = lane >= G8, mine = lane < 2 * G8;     // V's lanes follow K's
+    const int dg = lane % G8;
+    Raw8<T> x;
+    x.zero();
+    if (mine) x.load(reinterpret_cast<const T*>(kv ? a.v : a.k) + (size_t)b * (kv ? a.ldv : a.ldk) + (size_t)hk * D + dg * 8);
+    const int before = max(a.cache_len[b], 0), pn = before / a.page, older = before % a.page;
+    if (seq_len(a.new_len, b, 1) == 0 || pn >= a.max_pages) return;
+    const int pg = a.block_table[(size_t)b * a.max_pages + pn];
+    if (pg < 0 || pg >= a.n_pages) return;
+    const size_t slot0 = (size_t)pg * a.HK + hk;
+    uint8_t* codes = (kv ? a.v_cache : a.k_cache) + slot0 * a.page * D;
+    float* scale = (kv ? a.v_scale : a.k_scale) + slot0;
+    const float was = older > 0 ? *scale : 0.f;
+    float top = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = fmaxf(top, finite_abs(x.get(e)));
+#pragma unroll
+    for (int o = G8 / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+    if (!mine) return;
+    const float s = fmaxf(scale_for(top), was), inv = 1.f / s;
+    if (older > 0 && s > was) {  // the tokens there move to the larger scale: each lane those of its channels
+        const float r = was / s;
+        for (int t = 0; t < older; ++t)
+            for (int e = 0; e < 8; ++e) {
+                const int d = dg * 8 + e;
+                uint8_t* p = codes + (kv ? (size_t)d * a.page + t : (size_t)t * D + d);
+                *p = encode(decode(*p), r);
+            }
+    }
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = to_range(x.get(e), inv);
+    const uint32_t w0 = encode4(y[0], y[1], y[2], y[3]), w1 = encode4(y[4], y[5], y[6], y[7]);
+    if (!kv) {
+        *reinterpret_cast<uint2*>(codes + (size_t)older * D + dg * 8) = make_uint2(w0, w1);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) codes[(size_t)(dg * 8 + e) * a.page + older] = (uint8_t)((e < 4 ? w0 : w1) >> (8 * (e & 3)));
+    }
+    if (dg == 0) *scale = s;
+}
+
+template <typename T, int D, int PAGE>
+static hipError_t launch_append_p(const AppendArgs& a, hipStream_t s) {
+    const int touched = (a.T + PAGE - 2) / PAGE + 1;
+    hipLaunchKernelGGL((kda_cache_append_kernel<T, D, PAGE>), dim3((unsigned)((size_t)a.B * a.HK * touched)),
+                       dim3(append_threads(D, PAGE)), 0, s, a, touched);
+    return hipGetLastError();
+}
 template <typename T, int D>
 static hipError_t launch_append_t(const AppendArgs& a, hipStream_t s) {
-    const int touched = (a.T + a.page - 2) / a.page + 1;
-    hipLaunchKernelGGL((kda_cache_append_kernel<T, D>), dim3((unsigned)((size_t)a.B * a.HK * touched)), dim3(256), 0, s, a, touched);
-    return hipGetLastError();
+    if (a.T == 1) {
+        hipLaunchKernelGGL((kda_cache_append_one_kernel<T, D>), dim3((unsigned)(((size_t)a.B * a.HK + 3) / 4)), dim3(256), 0, s, a);
+        return hipGetLastError();
+    }
+    switch (a.page) {
+        case 16: return launch_append_p<T, D, 16>(a, s);
+        case 32: return launch_append_p<T, D, 32>(a, s);
+        case 64: return launch_append_p<T, D, 64>(a, s);
+        case 128: return launch_append_p<T, D, 128>(a, s);
+        default: return hipErrorInvalidValue;
+    }
 }
 template <typename T>
 static hipError_t launch_append_d(int D, const AppendArgs& a, hipStream_t s) {

@@ -8,7 +8,6 @@ an exception is raised.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -430,32 +429,38 @@ ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 ROTARY_INTERLEAVED, ROTARY_INVERSE = 1, 2
 
 
-def _on_device(dev):
-    """The device of the tensors becomes the current one for a launch (a null
-    stream handle names the current device's stream)."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+def _launch(name, dev, *args):
+    """Calls an entry point on the current stream of `dev`, which becomes the current
+    device for the call (a null stream handle names the current device's stream)."""
+    fn = getattr(_lib or load(), name)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if st:
+        _check(name, st)
 
 
 def _expect(name, t, shape, dtype, dev):
     """Checks an argument's shape, type and device; None passes."""
-    if t is None:
+    if t is None or (t.dtype is dtype and t.shape == shape and t.device == dev):
         return
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
-        raise TypeError(f"{name} must be a {dtype} tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be a {dtype} tensor, not {t.dtype}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
 def _rows(name, t):
-    """(pointer, row stride in elements) of a [B,T,H,D] tensor whose heads are
-    packed and whose tokens lie one stride apart throughout."""
+    """(pointer, row stride in elements, 0: contiguous) of a [B,T,H,D] device tensor
+    whose heads are packed and whose tokens lie one stride apart throughout."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    B, T, H, D = t.shape
-    if t.numel() == 0:
+    if t.is_contiguous():
         return t.data_ptr(), 0
+    B, T, H, D = t.shape
     sb, st, sh, sd = t.stride()
     if (D > 1 and sd != 1) or (H > 1 and sh != D):
         raise ValueError(f"the heads of {name} must be contiguous")
@@ -507,30 +512,29 @@ def rotary(q, k, inv_freq, positions=None, *, scale=1.0, interleaved=False, inve
     (in place).  q, k and the outputs may be parts of packed tensors.  Returns
     (q_out, k_out), or q_out without k."""
     B, T, H, D = q.shape
-    dev = q.device
-    _expect("inv_freq", inv_freq, (inv_freq.numel(),), torch.float64, dev)
+    dev, dt = q.device, q.dtype
+    pairs = inv_freq.numel()
+    _expect("inv_freq", inv_freq, (pairs,), torch.float64, dev)
     _expect("positions", positions, (B, T), torch.int32, dev)
     if q_out is None:
-        q_out = torch.empty((B, T, H, D), dtype=q.dtype, device=dev)
-    _expect("q_out", q_out, q.shape, q.dtype, dev)
+        q_out = torch.empty((B, T, H, D), dtype=dt, device=dev)
+    else:
+        _expect("q_out", q_out, q.shape, dt, dev)
     qp, ldq = _rows("q", q)
     qo, ldqo = _rows("q_out", q_out)
     kp = ko = None
     HK = ldk = ldko = 0
     if k is not None:
         HK = k.shape[2]
-        _expect("k", k, (B, T, HK, D), q.dtype, dev)
+        _expect("k", k, (B, T, HK, D), dt, dev)
         if k_out is None:
-            k_out = torch.empty((B, T, HK, D), dtype=q.dtype, device=dev)
-        _expect("k_out", k_out, k.shape, q.dtype, dev)
+            k_out = torch.empty((B, T, HK, D), dtype=dt, device=dev)
+        else:
+            _expect("k_out", k_out, k.shape, dt, dev)
         kp, ldk = _rows("k", k)
         ko, ldko = _rows("k_out", k_out)
-    with _on_device(dev):
-        st = load().kda_rotary(qp, kp, qo, ko, _ptr(positions), _ptr(inv_freq), B, T, H, HK, D, 2 * inv_freq.numel(),
-                               ldq, ldk, ldqo, ldko, scale,
-                               (ROTARY_INTERLEAVED if interleaved else 0) | (ROTARY_INVERSE if inverse else 0),
-                               _dt(q.dtype), _stream(dev))
-    _check("kda_rotary", st)
+    _launch("kda_rotary", dev, qp, kp, qo, ko, _ptr(positions), _ptr(inv_freq), B, T, H, HK, D, 2 * pairs, ldq, ldk,
+            ldqo, ldko, scale, (ROTARY_INTERLEAVED if interleaved else 0) | (ROTARY_INVERSE if inverse else 0), _dt(dt))
     return q_out if k is None else (q_out, k_out)
 
 
@@ -549,17 +553,16 @@ def attn_fwd(q, k, v, *, scale=None, causal=True, window=0, q_len=None, kv_len=N
     dev, dt = q.device, q.dtype
     if o is None:
         o = torch.empty((B, Tq, H, D), dtype=dt, device=dev)
+    else:
+        _expect("o", o, (B, Tq, H, D), dt, dev)
     if lse is None:
         lse = torch.empty((B, H, Tq), dtype=torch.float32, device=dev)
-    _expect("o", o, (B, Tq, H, D), dt, dev)
-    _expect("lse", lse, (B, H, Tq), torch.float32, dev)
+    else:
+        _expect("lse", lse, (B, H, Tq), torch.float32, dev)
     (qp, ldq), (kp, ldk), (vp, ldv) = _rows("q", q), _rows("k", k), _rows("v", v)
     ws = _workspace(attn_fwd_workspace_bytes(B, Tq, Tk, H, HK, D, dt), workspace, dev)
-    with _on_device(dev):
-        st = load().kda_attn_fwd(qp, kp, vp, _ptr(q_len), _ptr(kv_len), _ptr(o), _ptr(lse), B, Tq, Tk, H, HK, D,
-                                 ldq, ldk, ldv, D ** -0.5 if scale is None else scale, 1 if causal else 0, window,
-                                 _dt(dt), *_ws_args(ws), _stream(dev))
-    _check("kda_attn_fwd", st)
+    _launch("kda_attn_fwd", dev, qp, kp, vp, _ptr(q_len), _ptr(kv_len), _ptr(o), _ptr(lse), B, Tq, Tk, H, HK, D, ldq,
+            ldk, ldv, D ** -0.5 if scale is None else scale, 1 if causal else 0, window, _dt(dt), *_ws_args(ws))
     return o, lse
 
 
@@ -580,12 +583,9 @@ def attn_bwd(q, k, v, o, lse, dout, *, scale=None, causal=True, window=0, q_len=
          "dv": torch.empty((B, Tk, HK, D), dtype=dt, device=dev)}
     (qp, ldq), (kp, ldk), (vp, ldv) = _rows("q", q), _rows("k", k), _rows("v", v)
     ws = _workspace(attn_bwd_workspace_bytes(B, Tq, Tk, H, HK, D, dt), workspace, dev)
-    with _on_device(dev):
-        st = load().kda_attn_bwd(qp, kp, vp, _ptr(q_len), _ptr(kv_len), _ptr(o), _ptr(lse), _ptr(dout), _ptr(g["dq"]),
-                                 _ptr(g["dk"]), _ptr(g["dv"]), B, Tq, Tk, H, HK, D, ldq, ldk, ldv,
-                                 D ** -0.5 if scale is None else scale, 1 if causal else 0, window, _dt(dt),
-                                 *_ws_args(ws), _stream(dev))
-    _check("kda_attn_bwd", st)
+    _launch("kda_attn_bwd", dev, qp, kp, vp, _ptr(q_len), _ptr(kv_len), _ptr(o), _ptr(lse), _ptr(dout), _ptr(g["dq"]),
+            _ptr(g["dk"]), _ptr(g["dv"]), B, Tq, Tk, H, HK, D, ldq, ldk, ldv, D ** -0.5 if scale is None else scale, 1
+            if causal else 0, window, _dt(dt), *_ws_args(ws))
     return g
 
 
@@ -625,11 +625,9 @@ def cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cache_le
     if hk != HK:
         raise ValueError(f"the cache has {hk} heads, k has {HK}")
     (kp, ldk), (vp, ldv) = _rows("k", k), _rows("v", v)
-    with _on_device(dev):
-        st = load().kda_cache_append(kp, vp, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-                                     _ptr(block_table), _ptr(cache_len), _ptr(new_len), n_pages, max_pages, B, T, HK,
-                                     D, page, ldk, ldv, _dt(k.dtype), _stream(dev))
-    _check("kda_cache_append", st)
+    _launch("kda_cache_append", dev, kp, vp, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+            _ptr(block_table), _ptr(cache_len), _ptr(new_len), n_pages, max_pages, B, T, HK, D, page, ldk, ldv,
+            _dt(k.dtype))
 
 
 def attn_step_workspace_bytes(B, Tq, H, HK, D, max_len) -> int:
@@ -647,13 +645,11 @@ def attn_step(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_len, new
                                                  B, D, dev)
     if o is None:
         o = torch.empty((B, Tq, H, D), dtype=dt, device=dev)
-    _expect("o", o, (B, Tq, H, D), dt, dev)
+    else:
+        _expect("o", o, (B, Tq, H, D), dt, dev)
     qp, ldq = _rows("q", q)
     ws = _workspace(attn_step_workspace_bytes(B, Tq, H, HK, D, max_pages * page), workspace, dev)
-    with _on_device(dev):
-        st = load().kda_attn_step(qp, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
-                                  _ptr(cache_len), _ptr(new_len), _ptr(o), n_pages, max_pages, B, Tq, H, HK, D, page,
-                                  ldq, D ** -0.5 if scale is None else scale, window, _dt(dt), *_ws_args(ws),
-                                  _stream(dev))
-    _check("kda_attn_step", st)
+    _launch("kda_attn_step", dev, qp, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
+            _ptr(cache_len), _ptr(new_len), _ptr(o), n_pages, max_pages, B, Tq, H, HK, D, page, ldq, D ** -0.5 if
+            scale is None else scale, window, _dt(dt), *_ws_args(ws))
     return o

@@ -104,6 +104,16 @@ def test_attn_split_key_axis(dtype, Tq, H, HK):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D,H,HK,T", [(128, 16, 16, 150), (64, 32, 16, 97), (16, 48, 16, 130)])
+def test_attn_enough_heads_to_fill_the_card(dtype, D, H, HK, T):
+    """Grids of at least 256 workgroups: the forms with whole tiles of keys and rows."""
+    x = draw(16, T, T, H, HK, D, dtype, D, packed=True)
+    n = [T - 9 * b for b in range(16)]
+    for kw, lens in ((dict(causal=True, window=0), {}), (dict(causal=True, window=40), dict(ql=n, kl=n))):
+        run_both(*x, dtype, f"D {D} {kw}", **lens, **kw)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("scale", [1e-3, 1.0, 30.0])
 def test_attn_scales(dtype, scale):
     """From nearly uniform rows to one key per row; large scores on both sides of zero."""
