@@ -1,12 +1,16 @@
 // kda_attn_device.h - device-side building blocks of the attention kernels.
 //
 // Tiles of token rows live in LDS as rows of D elements, cut into granules of 16
-// bytes; granule c of row r is at position c ^ (attn_swz(r) mod granules), so
-// both ways a tile is read spread over the banks:
-//   * row fragments (a lane reads 8 consecutive elements of its row): eight
-//     consecutive rows hit eight different granule positions;
-//   * column fragments (bf16: four rows by 16 columns per 16 lanes through the
-//     transposing LDS read): four consecutive rows hit four different pairs.
+// bytes; granule c of row r is at position c ^ tile_swizzle(r), so that both ways a
+// tile is read fill the 256 bytes a cycle of the 64 banks:
+//   * row fragments (a lane reads 8 consecutive elements of its row): a 16-byte read
+//     is served in phases of 16 lanes, {0-3, 12-15, 20-27} and {4-11, 16-19, 28-31} of
+//     each half wave (measured): rows 0-3 and 12-15 at granule c, rows 4-11 at c ^ 1;
+//   * column fragments of bf16 (four rows by 16 columns per 16 lanes through the
+//     transposing LDS read): phases of 32 lanes, eight rows by two granules.
+// Even swizzles 2 (r mod 8) (for 256-byte rows; one step per 256 bytes in general)
+// meet both.  With a swizzle that serves only one of them every read of the other
+// kind took twice as long.
 // Contraction slots: row fragments hold elements 32 s + 8 (l / 16) + j of their
 // row in slot j (any map serves as long as both operands share it), column
 // fragments rows slot_index(l / 16, j), the map of frag_from_c, so that score
@@ -22,8 +26,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_inff();
 
 __device__ __forceinline__ uint32_t fdiv(uint32_t n, const FastDiv& f) { return (__umulhi(n, f.m) + n) >> f.s; }
-
-__device__ __forceinline__ int attn_swz(int row) { return ((row & 3) << 1) | ((row >> 2) & 1) | (row & 8); }
 
 // Maximum / sum over the four lane groups that share lane % 16, on the vector
 // unit (half-row swaps) rather than through LDS.
@@ -74,6 +76,21 @@ template <typename T, int D> struct TileGeom {
     static constexpr int ND = D / 16;                       // 16-channel blocks
 };
 
+// Swizzle of a tile row (see the top of this file).  fp32 columns are read a word a
+// lane, four rows at once: there the row number itself spreads them.
+template <typename T, int D> __device__ __forceinline__ int tile_swizzle(int row) {
+    constexpr int GR = TileGeom<T, D>::GR, RPL = GR < 16 ? 16 / GR : 1;   // rows per 256 bytes
+    return sizeof(T) == 2 ? 2 * ((row / RPL) & (GR / 2 - 1) & 7) : (row / RPL) & (GR - 1) & 15;
+}
+
+// Swizzle of a tile that is read by 32x32x16 products (Wide fragments below): row
+// fragments put rows {0-3, 12-15, 20-27} or {4-11, 16-19, 28-31} of one granule into a
+// phase, column fragments four rows by four granules.
+template <int D> __device__ __forceinline__ int wide_swizzle(int row) {
+    constexpr int GR = TileGeom<bf16_t, D>::GR, RPL = GR < 16 ? 16 / GR : 1;
+    return ((4 * (row / RPL)) & (GR - 1) & 12) | ((row >> 3) & 3);
+}
+
 // A window of memory for buffer loads: reads at or past `bytes` give zero.
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ u32x4 buffer_window(const void* p, long long bytes) {
@@ -98,23 +115,26 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 
 // Copies of ROWS-row tiles into LDS by NW waves: one wave instruction moves 64
 // granules.  row_off(r) is the byte offset of the tile's row r in the window.
-template <typename T, int D, int ROWS, int NW> struct Stage {
+template <typename T, int D, int ROWS, int NW, bool Wide = false> struct Stage {
     static constexpr int GR = TileGeom<T, D>::GR, N = ROWS * GR / 64, PER = (N + NW - 1) / NW;
     static_assert(ROWS * GR % 64 == 0, "whole wave instructions");
     uint32_t off[PER];
+    static __device__ __forceinline__ int swizzle(int r) { return Wide ? wide_swizzle<D>(r) : tile_swizzle<T, D>(r); }
     static __device__ __forceinline__ int row(int c, int wave, int lane) { return ((c * NW + wave) * 64 + lane) / GR; }
     // byte offset within its row of the granule that lands at this lane's place
     static __device__ __forceinline__ uint32_t col(int c, int wave, int lane) {
-        return (uint32_t)(((lane % GR) ^ (attn_swz(row(c, wave, lane)) & (GR - 1))) * 16);
+        return (uint32_t)(((lane % GR) ^ swizzle(row(c, wave, lane))) * 16);
     }
     template <typename RowOff> __device__ __forceinline__ void init(int wave, int lane, RowOff row_off) {
 #pragma unroll
         for (int c = 0; c < PER; ++c) off[c] = row_off(row(c, wave, lane)) + col(c, wave, lane);
     }
+    __device__ __forceinline__ void issue_one(const u32x4& window, uint32_t tile, int wave, int c) const {
+        if (N % NW == 0 || c * NW + wave < N) copy_to_lds(window, off[c], tile + (c * NW + wave) * 1024);
+    }
     __device__ __forceinline__ void issue(const u32x4& window, uint32_t tile, int wave) const {
 #pragma unroll
-        for (int c = 0; c < PER; ++c)
-            if (N % NW == 0 || c * NW + wave < N) copy_to_lds(window, off[c], tile + (c * NW + wave) * 1024);
+        for (int c = 0; c < PER; ++c) issue_one(window, tile, wave, c);
     }
 };
 
@@ -127,12 +147,11 @@ template <typename T, int D> struct TileLane {
     static constexpr int RB = D * (int)sizeof(T);   // bytes per row
     uint32_t row, col;
     __device__ __forceinline__ explicit TileLane(int lane) {
-        constexpr int GR = TileGeom<T, D>::GR;
         const int r = lane & 15, g = lane >> 4, i = lane & 3;
         const int c = sizeof(T) == 2 ? (D >= 32 ? g : g & 1) : (D >= 32 ? 2 * g : 2 * (g & 1));
-        row = r * RB + ((c ^ (attn_swz(r) & (GR - 1))) * 16);
+        row = r * RB + ((c ^ tile_swizzle<T, D>(r)) * 16);
         const int q = 4 * g + ((lane >> 2) & 3);
-        col = q * RB + (((i >> 1) ^ (attn_swz(q) & (GR - 1))) * 16) + (i & 1) * 8;
+        col = q * RB + (((i >> 1) ^ tile_swizzle<T, D>(q)) * 16) + (i & 1) * 8;
     }
 };
 
@@ -190,15 +209,87 @@ __device__ __forceinline__ Frag<bf16_t> col_frag(const unsigned char* sm, uint32
 template <int D>
 __device__ __forceinline__ Frag<float> col_frag(const unsigned char* sm, uint32_t tile, int r0, int c, const TileLane<float, D>&,
                                                 int lane) {
-    constexpr int GR = TileGeom<float, D>::GR;
     const int col = 16 * c + (lane & 15), g = lane >> 4;
     Frag<float> f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const int row = r0 + slot_index(g, j);
         f.v[j] = *reinterpret_cast<const float*>(sm + tile + row * (D * 4) +
-                                                 (((col >> 2) ^ (attn_swz(row) & (GR - 1))) * 16) + (col & 3) * 4);
+                                                 (((col >> 2) ^ tile_swizzle<float, D>(row)) * 16) + (col & 3) * 4);
     }
+    return f;
+}
+
+// ---------------------------------------------------------------- 32x32x16
+// The same products on 32x32 tiles (bf16, D >= 32).  Per flop they hold the vector
+// unit's issue for half as long: beside back-to-back 16x16x32 products another wave
+// of the SIMD issues a vector instruction every 9.3 cycles, beside 32x32x16 ones
+// every 6.0 (4.8 alone; exponentials 18.9, 11.2 and 8.5).
+//   * accumulator: lane l, element i is row 8 (i / 4) + 4 (l / 32) + i % 4, column l % 32;
+//   * operand fragment of a 16-long step: lane l supplies row (column) l % 32 at 8 slots.
+//     Row fragments hold elements 16 s + 8 (l / 32) + j; column fragments of 32 rows
+//     hold, at step u, rows 16 u + 8 (j / 4) + 4 (l / 32) + j % 4: elements 8 u .. 8 u + 7
+//     of an accumulator, rounded, are the matching operand.
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ floatx16 mma32(const Frag<bf16_t>& a, const Frag<bf16_t>& b, const floatx16& c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.v, b.v, c, 0, 0, 0);
+}
+__device__ __forceinline__ floatx16 splat16(float x) {
+    floatx16 v;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = x;
+    return v;
+}
+// Operand of step u from an accumulator.
+__device__ __forceinline__ Frag<bf16_t> frag_of(const floatx16& x, int u) {
+    Frag<bf16_t> f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f.v[j] = (bf16_t)x[8 * u + j];
+    return f;
+}
+
+// Maximum / sum over the two lanes that share a column.
+__device__ __forceinline__ float pair_max(float x) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+__device__ __forceinline__ float pair_add(float x) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+
+// A lane's place in a tile, as TileLane.
+template <int D> struct WideLane {
+    static constexpr int RB = D * 2;
+    uint32_t row, col;
+    __device__ __forceinline__ explicit WideLane(int lane) {
+        const int r = lane & 31, h = lane >> 5, i = lane & 3;
+        row = r * RB + ((h ^ wide_swizzle<D>(r)) * 16);
+        // lanes 16 .. 31 of a half take the upper 16 of 32 columns
+        const int q = 4 * h + ((lane >> 2) & 3);
+        col = q * RB + (((2 * ((lane >> 4) & 1) + (i >> 1)) ^ wide_swizzle<D>(q)) * 16) + (i & 1) * 8;
+    }
+};
+// Row fragment of rows [r0, r0 + 32) (r0 a multiple of 32), step s.
+template <int D>
+__device__ __forceinline__ Frag<bf16_t> wide_row(const unsigned char* sm, uint32_t tile, int r0, int s, const WideLane<D>& l) {
+    Frag<bf16_t> f;
+    f.v = *reinterpret_cast<const bf16x8*>(sm + ((l.row + tile) ^ (32 * s)) + r0 * (D * 2));
+    return f;
+}
+// Column fragment: columns 32 c + l % 32 at step u of the 32 rows from r0.
+template <int D>
+__device__ __forceinline__ Frag<bf16_t> wide_col(const unsigned char* sm, uint32_t tile, int r0, int u, int c, const WideLane<D>& l) {
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef short s16x8 __attribute__((ext_vector_type(8)));
+    typedef s16x4 __attribute__((address_space(3)))* lds4;
+    // rows 16 u + 8 k + 4 h + .. differ from 4 h + .. in bits 3 and 4, the swizzle's low bits
+    const unsigned char* base = sm + (r0 + 16 * u) * (D * 2);
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(base + ((l.col + tile) ^ (64 * c) ^ (16 * (2 * u)))));
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(base + 8 * (D * 2) + ((l.col + tile) ^ (64 * c) ^ (16 * (2 * u + 1)))));
+    Frag<bf16_t> f;
+    f.v = __builtin_bit_cast(bf16x8, s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
     return f;
 }
 

@@ -12,6 +12,15 @@
 
 namespace kda {
 
+// The maximum that a row's exponentials are taken against is kept until a score
+// exceeds it by a factor 2^8: sums and outputs stay far inside fp32 either way, and
+// the rescaling of every accumulator becomes rare (with 32 rows to a wave some row's
+// maximum grows in most tiles).
+constexpr float kSlack = 8.f;
+
+// Workgroups of 256 rows that fill the card's 256 compute units.
+constexpr int kTurnsGrid = 256;
+
 // Parts that one thread joins by itself.  8 184 rows of 3 parts (D = 64, fp32): 4 us,
 // against 13 us with a workgroup per row; 512 rows of 64 parts the other way: 6 us
 // against 46.
@@ -119,17 +128,16 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void kda_attn_fwd_kernel(
             }
         if (k0 < all_lo || k0 + KB > all_hi) {
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
+            for (int n = 0; n < NQ; ++n) {
+                const uint32_t span = max(hi[n] - lo[n] + 1, 0), first = k0 + 4 * g - lo[n];
 #pragma unroll
-                for (int n = 0; n < NQ; ++n)
+                for (int i = 0; i < NT; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = k0 + 16 * i + 4 * g + e;
-                        st[i][n][e] = key >= lo[n] && key <= hi[n] ? st[i][n][e] : kNegInf;
-                    }
+                    for (int e = 0; e < 4; ++e) st[i][n][e] = first + 16 * i + e < span ? st[i][n][e] : kNegInf;
+            }
         }
         bool grew = false;
-        float mu[NQ], alpha[NQ];
+        float mu[NQ], top[NQ];
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
             float x = kNegInf;
@@ -137,20 +145,21 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void kda_attn_fwd_kernel(
             for (int i = 0; i < NT; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x = fmaxf(x, st[i][n][e]);
-            x = fmaxf(m[n], group_max4(x) * c);
-            mu[n] = x == kNegInf ? 0.f : x;  // a row that has seen nothing yet
-            alpha[n] = exp2_fast(m[n] - mu[n]);
-            grew |= x > m[n];
-            m[n] = x;
+            top[n] = group_max4(x) * c;
+            grew |= top[n] > m[n] + kSlack;
         }
         if (__any(grew)) {
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
-                l[n] *= alpha[n];
+                const float x = fmaxf(m[n], top[n]), alpha = exp2_fast(m[n] - (x == kNegInf ? 0.f : x));
+                m[n] = x;
+                l[n] *= alpha;
 #pragma unroll
-                for (int d = 0; d < ND; ++d) o[d][n] *= alpha[n];
+                for (int d = 0; d < ND; ++d) o[d][n] *= alpha;
             }
         }
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) mu[n] = m[n] == kNegInf ? 0.f : m[n];  // a row that has seen nothing yet
         // bf16 probabilities are rounded for the product (2^-9 relative each, as
         // the values beside them); the sum is over the unrounded ones
         Frag<T> pf[NT / 2][NQ];
@@ -202,6 +211,261 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void kda_attn_fwd_kernel(
                 a.lse[((size_t)b * a.H + h) * a.Tq + t[n]] =
                     some ? (m[n] + __builtin_amdgcn_logf(sum)) * kLn2 : kNegInf;
         }
+    }
+}
+
+// The forward for grids that fill the card: eight waves share the tiles, two on each
+// SIMD, and take turns.  Between two barriers one half forms products (O += V P of
+// a tile and S = K Q of the next) while the other half, on the vector unit, turns its
+// scores into probabilities; then they change over.  Left to themselves the two
+// waves of a SIMD want the same unit at the same time.  Three tiles of keys and three
+// of values: the copies for two tiles ahead are issued in the vector turn, so that the
+// matrix turn holds nothing but fragment reads and products, and have a whole
+// matrix turn to land.
+template <int D>
+__global__ __launch_bounds__(512, 2) void kda_attn_fwd_turns_kernel(const AttnArgs a) {
+    typedef bf16_t T;
+    constexpr int KB = 64, NW = 8, NS = D / 16, ND = D / 32, NT = KB / 32, BQ = 32 * NW;
+    constexpr int kTile = KB * D * (int)sizeof(T);
+    __shared__ __attribute__((aligned(16))) unsigned char sm[6 * kTile];   // three of K, three of V
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5;
+    const bool late = wave >= 4;   // the half that starts a turn later
+    const int nbh = a.B * a.HK, rows = a.Tq * a.G;
+    const int ntile = (rows + BQ - 1) / BQ;
+    const int bh = blockIdx.x % nbh, tile = ntile - 1 - blockIdx.x / nbh;
+    const int b = bh / a.HK, hk = bh % a.HK;
+    const int ql = seq_len(a.q_len, b, a.Tq), kl = seq_len(a.kv_len, b, a.Tk), off = kl - ql;
+    const int r0 = tile * BQ, r1 = min(r0 + BQ, rows);
+    const RowRange blk = row_range(a, r0, r1, ql, kl);
+    const int k_beg = blk.key_lo / KB, k_end = blk.key_hi > blk.key_lo ? (blk.key_hi + KB - 1) / KB : k_beg;
+
+    const int w0 = r0 + wave * 32;
+    const RowRange mine = w0 < r1 ? row_range(a, w0, min(w0 + 32, r1), ql, kl) : RowRange{0, -1, 0, 0};
+    const int all_hi = a.causal ? min(kl, mine.t_first + off + 1) : kl;
+    const int all_lo = a.window ? mine.t_last + off - a.window + 1 : 0;
+    const int r = w0 + (lane & 31), t = (int)fdiv((uint32_t)min(r, rows - 1), a.divG);
+    const int head = hk * a.G + (min(r, rows - 1) - t * a.G);
+    Frag<T> qf[NS];
+    {
+        const int tr = max(min(t, ql - 1), 0);   // rows past q_len are dropped at the end
+        const T* qp = reinterpret_cast<const T*>(a.q) + ((size_t)b * a.Tq + tr) * a.ldq + (size_t)head * D + 8 * half;
+#pragma unroll
+        for (int s = 0; s < NS; ++s) frag_load_row8(qf[s], qp + 16 * s);
+    }
+
+    const T* kbase = reinterpret_cast<const T*>(a.k) + (size_t)b * a.Tk * a.ldk + (size_t)hk * D;
+    const T* vbase = reinterpret_cast<const T*>(a.v) + (size_t)b * a.Tk * a.ldv + (size_t)hk * D;
+    Stage<T, D, KB, NW, true> kst, vst;
+    kst.init(wave, lane, [&](int r) { return (uint32_t)(r * a.ldk * sizeof(T)); });
+    vst.init(wave, lane, [&](int r) { return (uint32_t)(r * a.ldv * sizeof(T)); });
+    const uint32_t lds0 = lds_address(&sm[0]);
+    // windows of the next tiles to copy, and the ring places they go to
+    const long long kstep = (long long)KB * a.ldk, vstep = (long long)KB * a.ldv;
+    const T* knext = kbase + k_beg * kstep;
+    const T* vnext = vbase + k_beg * vstep;
+    long long kleft = ((kl - 1 - (long long)k_beg * KB) * (long long)a.ldk + D) * (long long)sizeof(T);
+    long long vleft = ((kl - 1 - (long long)k_beg * KB) * (long long)a.ldv + D) * (long long)sizeof(T);
+    int knum = k_beg, vnum = k_beg, kplace = 0, vplace = 0;
+    auto load_k = [&]() {
+        if (knum < k_end) kst.issue(buffer_window(knext, kleft), lds0 + kplace * kTile, wave);
+        knext += kstep;
+        kleft -= kstep * (long long)sizeof(T);
+        kplace = kplace == 2 ? 0 : kplace + 1;
+        ++knum;
+    };
+    auto load_v = [&]() {
+        if (vnum < k_end) vst.issue(buffer_window(vnext, vleft), lds0 + (3 + vplace) * kTile, wave);
+        vnext += vstep;
+        vleft -= vstep * (long long)sizeof(T);
+        vplace = vplace == 2 ? 0 : vplace + 1;
+        ++vnum;
+    };
+
+    const WideLane<D> place(lane);
+    const float c = a.scale_log2;
+    float m = kNegInf, l = 0.f;
+    floatx16 o[ND], st[NT];
+    Frag<T> pf[NT][2];
+#pragma unroll
+    for (int d = 0; d < ND; ++d) o[d] = splat16(0.f);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        st[i] = splat16(0.f);
+        pf[i][0].zero();
+        pf[i][1].zero();
+    }
+    auto scores = [&](uint32_t ks) {
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+            for (int i = 0; i < NT; ++i) st[i] = mma32(wide_row<D>(sm, ks, 32 * i, s, place), qf[s], s == 0 ? splat16(0.f) : st[i]);
+    };
+    auto values = [&](uint32_t vs) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int d = 0; d < ND; ++d) o[d] = mma32(wide_col<D>(sm, vs, 32 * i, u, d, place), pf[i][u], o[d]);
+    };
+    // both, in one stream of fragments read kAhead fragments before their products:
+    // nobody else covers this wave's LDS latency in its matrix turn
+    auto values_and_scores = [&](uint32_t vs, uint32_t ks) {
+        constexpr int NV = NT * 2 * ND, NF = NV + NS * NT, kAhead = 6;
+        Frag<T> ring[kAhead];
+        auto fetch = [&](int f) {
+            return f < NV ? wide_col<D>(sm, vs, 32 * (f / (2 * ND)), f / ND % 2, f % ND, place)
+                          : wide_row<D>(sm, ks, 32 * ((f - NV) % NT), (f - NV) / NT, place);
+        };
+#pragma unroll
+        for (int f = 0; f < kAhead; ++f) ring[f] = fetch(f);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+            const Frag<T> x = ring[f % kAhead];
+            if (f + kAhead < NF) ring[f % kAhead] = fetch(f + kAhead);
+            if (f < NV) {
+                o[f % ND] = mma32(x, pf[f / (2 * ND)][f / ND % 2], o[f % ND]);
+            } else {
+                const int i = (f - NV) % NT, s = (f - NV) / NT;
+                st[i] = mma32(x, qf[s], s == 0 ? splat16(0.f) : st[i]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    auto probabilities = [&](int kt) {
+        const int k0 = kt * KB;
+        if (k0 < all_lo || k0 + KB > all_hi) {
+            const int p = t + off, hi = a.causal ? min(kl - 1, p) : kl - 1, lo = a.window ? p - a.window + 1 : 0;
+            const uint32_t span = max(hi - lo + 1, 0), first = k0 + 4 * half - lo;
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) st[i][e] = first + 32 * i + 8 * (e / 4) + e % 4 < span ? st[i][e] : kNegInf;
+        }
+        float x = kNegInf;
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x = fmaxf(x, st[i][e]);
+        x = pair_max(x) * c;
+        if (__any(x > m + kSlack)) {
+            const float top = fmaxf(m, x), alpha = exp2_fast(m - (top == kNegInf ? 0.f : top));
+            m = top;
+            l *= alpha;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) o[d] *= alpha;
+        }
+        const float mu = m == kNegInf ? 0.f : m;  // a row that has seen nothing yet
+        // probabilities are rounded to bf16 for the product (2^-9 relative each, as the
+        // values beside them); the sum is over the unrounded ones
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                st[i][e] = exp2_fast(fmaf(st[i][e], c, -mu));
+                part[e % 4] += st[i][e];
+            }
+            pf[i][0] = frag_of(st[i], 0);
+            pf[i][1] = frag_of(st[i], 1);
+        }
+        l += (part[0] + part[1]) + (part[2] + part[3]);
+    };
+
+    if (k_beg < k_end) {
+        load_k();
+        load_k();
+        load_v();
+        load_k();
+        load_v();
+        wait_vmcnt<0>();
+        lds_barrier();
+        // the tiles [first, last) that this wave's rows see
+        const bool any = mine.key_hi > mine.key_lo;
+        const int first = any ? mine.key_lo / KB : k_end + 1, last = any ? (mine.key_hi + KB - 1) / KB : k_end + 1;
+        if (first == k_beg) {
+            scores(0);
+            probabilities(k_beg);
+        }
+        // Before tile kt's products: keys up to kt + 2 and values up to kt + 1 are in LDS
+        // or in flight.  Both halves wait for their copies at the end of a matrix turn;
+        // the next ones go to the places of keys kt and values kt - 1, last read before it.
+        uint32_t vs = 3 * kTile, ks = kTile;
+        auto change_over = [&]() {
+            __builtin_amdgcn_s_setprio(0);
+            vs = vs == 5 * kTile ? 3 * kTile : vs + kTile;
+            ks = ks == 2 * kTile ? 0 : ks + kTile;
+            wait_vmcnt<0>();
+            lds_barrier();
+            load_k();
+            load_v();
+        };
+        auto change_back = [&]() {
+            lds_barrier();
+            __builtin_amdgcn_s_setprio(1);
+        };
+        if (late) lds_barrier();
+        int kt = k_beg;
+        for (; kt + 1 < first && kt < k_end; ++kt) {
+            change_over();
+            change_back();
+        }
+        if (any && kt + 1 == first) {
+            scores(ks);
+            change_over();
+            probabilities(first);
+            change_back();
+            ++kt;
+        }
+        for (; any && kt + 1 < last; ++kt) {
+            values_and_scores(vs, ks);
+            change_over();
+            probabilities(kt + 1);
+            change_back();
+        }
+        if (any && kt + 1 == last) {
+            values(vs);
+            change_over();
+            change_back();
+            ++kt;
+        }
+        for (; kt < k_end; ++kt) {
+            change_over();
+            change_back();
+        }
+        __builtin_amdgcn_s_setprio(0);
+        if (!late) lds_barrier();
+    }
+
+    const float sum = pair_add(l);
+    const bool some = t < ql && sum != 0.f;
+    const float inv = some ? 1.f / sum : 0.f;
+    if (a.lse && half == 0 && r < r1)
+        a.lse[((size_t)b * a.H + head) * a.Tq + t] = some ? (m + __builtin_amdgcn_logf(sum)) * kLn2 : kNegInf;
+    // The outputs go through the wave's own part of the LDS (nobody reads tiles any
+    // more) and leave as whole rows, 16 bytes a lane: straight from the accumulators a
+    // store would touch 32 rows, 16 bytes of each.
+    unsigned char* mine_o = sm + wave * 32 * D * 2;
+    auto place_of = [](int row, int granule) { return row * D * 2 + ((granule ^ wide_swizzle<D>(row)) * 16); };
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            // rows without a sum get zeros whatever their accumulators hold
+            const floatx4 y = {o[d][4 * e] * inv, o[d][4 * e + 1] * inv, o[d][4 * e + 2] * inv, o[d][4 * e + 3] * inv};
+            store4(reinterpret_cast<T*>(mine_o + place_of(lane & 31, 4 * d + e) + 8 * half), some ? y : floatx4{0.f, 0.f, 0.f, 0.f});
+        }
+    asm volatile("" ::: "memory");
+    constexpr int GR = D / 8, RPI = 64 / GR;   // granules of a row, rows of a wave instruction
+#pragma unroll
+    for (int i = 0; i < 32 / RPI; ++i) {
+        const int row = i * RPI + lane / GR, granule = lane % GR, rr = w0 + row;
+        const uint4 y = *reinterpret_cast<const uint4*>(mine_o + place_of(row, granule));
+        if (rr >= r1) continue;
+        const int tt = (int)fdiv((uint32_t)rr, a.divG), hh = hk * a.G + (rr - tt * a.G);
+        *reinterpret_cast<uint4*>(reinterpret_cast<T*>(a.o) + (((size_t)b * a.Tq + tt) * a.H + hh) * D + granule * 8) = y;
     }
 }
 
@@ -330,6 +594,13 @@ template <typename T, int D>
 static hipError_t launch_fwd_t(const AttnArgs& a, hipStream_t s) {
     constexpr int NQ = attn_rows_per_wave(sizeof(T)) / 16, KB = sizeof(T) == 2 ? 64 : 32;
     const long long rows = (long long)a.Tq * a.G;
+    if constexpr (sizeof(T) == 2 && D >= 32) {
+        const long long tiles = (rows + 255) / 256;
+        if (a.nsplit == 1 && tiles * a.B * a.HK >= kTurnsGrid) {
+            hipLaunchKernelGGL((kda_attn_fwd_turns_kernel<D>), dim3((unsigned)(tiles * a.B * a.HK)), dim3(512), 0, s, a);
+            return hipGetLastError();
+        }
+    }
     const int nw = attn_waves(rows, 16 * NQ);
     hipError_t e = nw == 1 ? launch_fwd_n<T, D, NQ, KB, 1>(a, s)
                    : nw == 2 ? launch_fwd_n<T, D, NQ, KB, 2>(a, s)

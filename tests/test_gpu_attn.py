@@ -104,7 +104,7 @@ def test_attn_split_key_axis(dtype, Tq, H, HK):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("D,H,HK,T", [(128, 16, 16, 150), (64, 32, 16, 97), (16, 48, 16, 130)])
+@pytest.mark.parametrize("D,H,HK,T", [(128, 16, 16, 150), (64, 32, 16, 97), (16, 48, 16, 130), (128, 16, 16, 420), (32, 16, 16, 513)])
 def test_attn_enough_heads_to_fill_the_card(dtype, D, H, HK, T):
     """Grids of at least 256 workgroups: the forms with whole tiles of keys and rows."""
     x = draw(16, T, T, H, HK, D, dtype, D, packed=True)
