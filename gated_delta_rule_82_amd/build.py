@@ -20,7 +20,8 @@ INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkda.so")
 SOURCES = ["kda_api.cpp", "kda_step.hip", "kda_chunk.hip", "kda_layer.hip", "kda_compose.hip", "kda_conv.hip", "kda_gate.hip", "kda_bwd.hip",
-           "kda_attn_api.cpp", "kda_rotary.hip", "kda_attn_fwd.hip", "kda_attn_bwd.hip", "kda_cache.hip"]
+           "kda_attn_api.cpp", "kda_rotary.hip", "kda_attn_fwd.hip", "kda_attn_bwd.hip", "kda_attn_bwd_turns.hip",
+           "kda_cache.hip"]
 ARCH = os.environ.get("KDA_OFFLOAD_ARCH", "gfx950")
 
 

@@ -66,6 +66,14 @@ hipError_t launch_attn_fwd(int dt, int D, const AttnArgs& a, hipStream_t s);
 // The backward's row array holds a multiple of this many queries per head.
 constexpr int kAttnRowPad = 64;
 hipError_t launch_attn_bwd(int dt, int D, const AttnArgs& a, hipStream_t s);
+// bf16 kernels whose workgroups of eight waves, with 256 rows or 128 keys, have a
+// compute unit to themselves; they are taken where such workgroups fill the card's 256.
+constexpr int kTurnsGrid = 256, kTurnsRows = 256, kTurnsKeys = 128;
+inline bool attn_turns(int elem_bytes, int D, const AttnArgs& a, long long n, int tile) {
+    return elem_bytes == 2 && D >= 32 && (n + tile - 1) / tile * a.B * a.HK >= kTurnsGrid;
+}
+hipError_t launch_dkv_turns(int D, const AttnArgs& a, int padded, hipStream_t s);
+hipError_t launch_dq_turns(int D, const AttnArgs& a, int padded, hipStream_t s);
 
 struct AppendArgs {
     const void* k; const void* v;

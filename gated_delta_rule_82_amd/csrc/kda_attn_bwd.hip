@@ -433,12 +433,12 @@ static hipError_t launch_bwd_t(const AttnArgs& a, hipStream_t s) {
     }
     if (a.Tk > 0) {
         const bool small = nbh * ((a.Tk + kWide - 1) / kWide) < kSmallGrid;
-        e = small ? launch_dkv<T, D, kSmall>(a, padded, s) : launch_dkv<T, D, 4>(a, padded, s);
+        e = attn_turns(sizeof(T), D, a, a.Tk, kTurnsKeys) ? launch_dkv_turns(D, a, padded, s) : small ? launch_dkv<T, D, kSmall>(a, padded, s) : launch_dkv<T, D, 4>(a, padded, s);
         if (e != hipSuccess) return e;
     }
     if (rows > 0) {
         const bool small = nbh * ((rows + kWide - 1) / kWide) < kSmallGrid;
-        e = small ? launch_dq<T, D, kSmall>(a, padded, s) : launch_dq<T, D, 4>(a, padded, s);
+        e = attn_turns(sizeof(T), D, a, rows, kTurnsRows) ? launch_dq_turns(D, a, padded, s) : small ? launch_dq<T, D, kSmall>(a, padded, s) : launch_dq<T, D, 4>(a, padded, s);
     }
     return e;
 }

@@ -293,4 +293,31 @@ __device__ __forceinline__ Frag<bf16_t> wide_col(const unsigned char* sm, uint32
     return f;
 }
 
+// Writes a wave's accumulators (rows: the D channels, columns: 32 tensor rows) times
+// `scale` as bf16 rows, zeros for columns that are not live whatever the accumulators
+// hold.  They go through the wave's 64 D bytes of LDS and leave as whole rows, 16 bytes
+// a lane: straight from the accumulators a store would touch 32 rows, 16 bytes of each.
+// dest(row) is the address of tensor row `row`, or null.
+template <int D, typename Dest>
+__device__ __forceinline__ void wide_rows_out(const floatx16 (&x)[D / 32], float scale, bool live, unsigned char* lds, int lane, Dest dest) {
+    constexpr int GR = D / 8, RPI = 64 / GR;   // granules of a row, rows of a wave instruction
+    auto place_of = [](int row, int granule) { return row * D * 2 + ((granule ^ wide_swizzle<D>(row)) * 16); };
+    asm volatile("" ::: "memory");  // a wave's LDS accesses stay in order, and the compiler keeps that order
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const floatx4 y = {x[d][4 * e] * scale, x[d][4 * e + 1] * scale, x[d][4 * e + 2] * scale, x[d][4 * e + 3] * scale};
+            store4(reinterpret_cast<bf16_t*>(lds + place_of(lane & 31, 4 * d + e) + 8 * (lane >> 5)), live ? y : floatx4{0.f, 0.f, 0.f, 0.f});
+        }
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32 / RPI; ++i) {
+        const int row = i * RPI + lane / GR, granule = lane % GR;
+        const uint4 y = *reinterpret_cast<const uint4*>(lds + place_of(row, granule));
+        bf16_t* to = dest(row);
+        if (to) *reinterpret_cast<uint4*>(to + granule * 8) = y;
+    }
+}
+
 }  // namespace kda

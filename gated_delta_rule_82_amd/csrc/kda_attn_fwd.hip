@@ -18,9 +18,6 @@ namespace kda {
 // maximum grows in most tiles).
 constexpr float kSlack = 8.f;
 
-// Workgroups of 256 rows that fill the card's 256 compute units.
-constexpr int kTurnsGrid = 256;
-
 // Parts that one thread joins by itself.  8 184 rows of 3 parts (D = 64, fp32): 4 us,
 // against 13 us with a workgroup per row; 512 rows of 64 parts the other way: 6 us
 // against 46.
@@ -444,29 +441,11 @@ __global__ __launch_bounds__(512, 2) void kda_attn_fwd_turns_kernel(const AttnAr
     const float inv = some ? 1.f / sum : 0.f;
     if (a.lse && half == 0 && r < r1)
         a.lse[((size_t)b * a.H + head) * a.Tq + t] = some ? (m + __builtin_amdgcn_logf(sum)) * kLn2 : kNegInf;
-    // The outputs go through the wave's own part of the LDS (nobody reads tiles any
-    // more) and leave as whole rows, 16 bytes a lane: straight from the accumulators a
-    // store would touch 32 rows, 16 bytes of each.
-    unsigned char* mine_o = sm + wave * 32 * D * 2;
-    auto place_of = [](int row, int granule) { return row * D * 2 + ((granule ^ wide_swizzle<D>(row)) * 16); };
-#pragma unroll
-    for (int d = 0; d < ND; ++d)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            // rows without a sum get zeros whatever their accumulators hold
-            const floatx4 y = {o[d][4 * e] * inv, o[d][4 * e + 1] * inv, o[d][4 * e + 2] * inv, o[d][4 * e + 3] * inv};
-            store4(reinterpret_cast<T*>(mine_o + place_of(lane & 31, 4 * d + e) + 8 * half), some ? y : floatx4{0.f, 0.f, 0.f, 0.f});
-        }
-    asm volatile("" ::: "memory");
-    constexpr int GR = D / 8, RPI = 64 / GR;   // granules of a row, rows of a wave instruction
-#pragma unroll
-    for (int i = 0; i < 32 / RPI; ++i) {
-        const int row = i * RPI + lane / GR, granule = lane % GR, rr = w0 + row;
-        const uint4 y = *reinterpret_cast<const uint4*>(mine_o + place_of(row, granule));
-        if (rr >= r1) continue;
-        const int tt = (int)fdiv((uint32_t)rr, a.divG), hh = hk * a.G + (rr - tt * a.G);
-        *reinterpret_cast<uint4*>(reinterpret_cast<T*>(a.o) + (((size_t)b * a.Tq + tt) * a.H + hh) * D + granule * 8) = y;
-    }
+    // rows without a sum get zeros; nobody reads tiles any more
+    wide_rows_out<D>(o, inv, some, sm + wave * 64 * D, lane, [&](int row) -> T* {
+        const int rr = w0 + row, tt = (int)fdiv((uint32_t)min(rr, rows - 1), a.divG), hh = hk * a.G + (rr - tt * a.G);
+        return rr < r1 ? reinterpret_cast<T*>(a.o) + (((size_t)b * a.Tq + tt) * a.H + hh) * D : nullptr;
+    });
 }
 
 // Few parts: a thread takes four channels of one packed row over all of them.
@@ -595,9 +574,8 @@ static hipError_t launch_fwd_t(const AttnArgs& a, hipStream_t s) {
     constexpr int NQ = attn_rows_per_wave(sizeof(T)) / 16, KB = sizeof(T) == 2 ? 64 : 32;
     const long long rows = (long long)a.Tq * a.G;
     if constexpr (sizeof(T) == 2 && D >= 32) {
-        const long long tiles = (rows + 255) / 256;
-        if (a.nsplit == 1 && tiles * a.B * a.HK >= kTurnsGrid) {
-            hipLaunchKernelGGL((kda_attn_fwd_turns_kernel<D>), dim3((unsigned)(tiles * a.B * a.HK)), dim3(512), 0, s, a);
+        if (a.nsplit == 1 && attn_turns(sizeof(T), D, a, rows, kTurnsRows)) {
+            hipLaunchKernelGGL((kda_attn_fwd_turns_kernel<D>), dim3((unsigned)((rows + 255) / 256 * a.B * a.HK)), dim3(512), 0, s, a);
             return hipGetLastError();
         }
     }

@@ -113,6 +113,16 @@ def test_attn_enough_heads_to_fill_the_card(dtype, D, H, HK, T):
         run_both(*x, dtype, f"D {D} {kw}", **lens, **kw)
 
 
+@pytest.mark.parametrize("D,H,HK,Tq,Tk", [(128, 48, 16, 90, 333), (64, 16, 16, 300, 70), (32, 32, 16, 1, 260)])
+def test_attn_full_grids_of_unequal_lengths(D, H, HK, Tq, Tk):
+    """The same with shared heads, more or fewer keys than queries, and empty sequences among them."""
+    x = draw(16, Tq, Tk, H, HK, D, BF16, D + 1)
+    ql = [Tq, 0, 1, Tq // 2] * 4
+    kl = [Tk, Tk, 1, 0, Tk // 3, Tk, 65, 64] * 2
+    for kw in (dict(causal=True, window=0), dict(causal=True, window=33), dict(causal=False, window=0)):
+        run_both(*x, BF16, f"D {D} {kw}", ql=[min(n, Tq) for n in ql], kl=[min(n, Tk) for n in kl], **kw)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("scale", [1e-3, 1.0, 30.0])
 def test_attn_scales(dtype, scale):
