@@ -66,13 +66,36 @@ hipError_t launch_attn_fwd(int dt, int D, const AttnArgs& a, hipStream_t s);
 // The backward's row array holds a multiple of this many queries per head.
 constexpr int kAttnRowPad = 64;
 hipError_t launch_attn_bwd(int dt, int D, const AttnArgs& a, hipStream_t s);
-// bf16 kernels whose workgroups of eight waves, with 256 rows or 128 keys, have a
-// compute unit to themselves; they are taken where such workgroups fill the card's 256.
+// bf16 kernels whose eight waves take turns on the matrix cores.  A workgroup, of 256
+// rows or 128 keys, has a compute unit to itself: they are taken where such workgroups
+// fill the card's 256 units and what a row or key sees is long enough to pay for the
+// slower start and, under a causal mask, for the whole tiles on the diagonal that both
+// halves walk.  Measured, this kernel against the plain one (16 heads of 128 channels):
+//   forward  4 x 4096 causal 262 / 272 us, 2 x 2048 causal 57 / 54; 2 x 2048 all keys 68 / 77,
+//            16 x 256 19 / 21; D = 64: 4 x 4096 causal 175 / 158
+//   dq       2 x 2048 causal 76 / 81, 4 x 1024 causal 50 / 47; 2 x 2048 all keys 91 / 111,
+//            16 x 256 24 / 25; D = 32: 4 x 4096 causal 167 / 157
+//   dk, dv   4 x 4096 causal 530 / 738, 2 x 2048 causal 86 / 103, 4 x 1024 causal 63 / 61;
+//            all keys 494 / 474 (8 x 2048, where nothing is left uneven), but 71 / 91 where
+//            the plain kernel has less than two workgroups a unit (1 x 2048); D = 64: 344 / 294
 constexpr int kTurnsGrid = 256, kTurnsRows = 256, kTurnsKeys = 128;
-inline bool attn_turns(int elem_bytes, int D, const AttnArgs& a, long long n, int tile) {
-    return elem_bytes == 2 && D >= 32 && (n + tile - 1) / tile * a.B * a.HK >= kTurnsGrid;
+inline long long turns_grid(const AttnArgs& a, long long n, int tile) { return (n + tile - 1) / tile * a.B * a.HK; }
+inline bool attn_row_turns(const AttnArgs& a, int causal_from) {
+    const int keys = a.window > 0 && a.window < a.Tk ? a.window : a.Tk;
+    return turns_grid(a, (long long)a.Tq * a.G, kTurnsRows) >= kTurnsGrid && keys >= (a.causal ? causal_from : 512);
 }
-hipError_t launch_dkv_turns(int D, const AttnArgs& a, int padded, hipStream_t s);
+inline bool attn_fwd_turns(int elem_bytes, int D, const AttnArgs& a) {
+    return elem_bytes == 2 && D == 128 && a.nsplit == 1 && attn_row_turns(a, 4096);
+}
+inline bool attn_dq_turns(int elem_bytes, int D, const AttnArgs& a) {
+    return elem_bytes == 2 && D >= 64 && attn_row_turns(a, 2048);
+}
+inline bool attn_dkv_turns(int elem_bytes, int D, const AttnArgs& a) {
+    const long long grid = turns_grid(a, a.Tk, kTurnsKeys), seen = a.window > 0 && a.window < a.Tq ? a.window : a.Tq;
+    return elem_bytes == 2 && D == 128 && grid >= kTurnsGrid && seen * a.G >= 2048 &&
+           ((a.causal && a.window == 0) || grid < 2 * kTurnsGrid);
+}
+hipError_t launch_dkv_turns(const AttnArgs& a, int padded, hipStream_t s);
 hipError_t launch_dq_turns(int D, const AttnArgs& a, int padded, hipStream_t s);
 
 struct AppendArgs {

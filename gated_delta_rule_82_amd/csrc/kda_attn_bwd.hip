@@ -71,9 +71,6 @@ __device__ __forceinline__ void join_turns(float* lds, floatx4 (&x)[ND][N], int 
     }
 }
 
-// Grids of fewer workgroups than this leave compute units idle.
-constexpr int kSmallGrid = 256;
-
 // dk and dv of a tile of 16 NK NG keys.  Keys are the columns of S = Q K^T and
 // dP = dO V^T, so the probabilities are right operands of dV^T += dO^T P and
 // dK^T += Q^T dS as they stand.  The 4 waves are NG groups of keys times 4 / NG turns:
@@ -85,7 +82,7 @@ __global__ __launch_bounds__(256, 2) void kda_attn_dkv_kernel(const AttnArgs a, 
     typedef TileGeom<T, D> G_;
     constexpr int NW = 4, NT = NW / NG, NS = G_::NS, ND = G_::ND, BK = 16 * NK * NG;
     // contraction steps whose K and V fragments stay in registers; at D = 128 half of
-    // them live in LDS (a wave's own, 1 KiB a fragment), or two waves would not fit a SIMD
+    // them live in LDS (1 KiB a fragment), or two waves would not fit a SIMD
     constexpr int VR = sizeof(T) == 2 && D == 128 ? 3 : NS, VL = NS - VR;
     constexpr int kTile = RB * D * (int)sizeof(T);
     static_assert(RB == 32 * NT && RB <= 128, "one step a wave and tile");
@@ -93,15 +90,16 @@ __global__ __launch_bounds__(256, 2) void kda_attn_dkv_kernel(const AttnArgs a, 
     constexpr int kRing = 4 * kTile;
     __shared__ __attribute__((aligned(16))) unsigned char sm[kRing > kSum ? kRing : kSum];
     __shared__ __attribute__((aligned(16))) float srow[2][256];  // RB pairs, and room for a whole wave's copy
-    __shared__ __attribute__((aligned(16))) T sv[VL > 0 ? NW * 2 * NK * VL * 512 : 1];
+    __shared__ __attribute__((aligned(16))) T sv[VL > 0 ? NG * 2 * NK * VL * 512 : 1];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
     const int kgrp = wave % NG, turn = wave / NG;
-    // Under a causal mask early keys are seen by most rows.  Workgroups that share a
-    // compute unit come half a grid apart, so the second half runs backwards: a long
-    // tile's neighbour is a short one.
+    // Under a causal mask early keys are seen by most rows, and come first.  Where all
+    // workgroups are there at once (NG = 4, two to a compute unit), those that share a
+    // unit come half a grid apart: the second half runs backwards, so that a long
+    // tile's neighbour is a short one (fp32, 16 heads x 2048, D = 128: 337 us, without 413).
     const int nbh = a.B * a.HK, ntile = (a.Tk + BK - 1) / BK, half = (ntile + 1) / 2, at_tile = blockIdx.x / nbh;
-    const int bh = blockIdx.x % nbh, tile = at_tile < half ? at_tile : ntile - 1 - (at_tile - half);
+    const int bh = blockIdx.x % nbh, tile = NG < 4 || at_tile < half ? at_tile : ntile - 1 - (at_tile - half);
     const int b = bh / a.HK, hk = bh % a.HK;
     const int ql = seq_len(a.q_len, b, a.Tq), kl = seq_len(a.kv_len, b, a.Tk), off = kl - ql;
     const int k0 = tile * BK, k1 = min(k0 + BK, kl);  // keys of the tile inside the length
@@ -117,7 +115,7 @@ __global__ __launch_bounds__(256, 2) void kda_attn_dkv_kernel(const AttnArgs a, 
     auto seen_from = [&](int key) { return a.causal ? min(max(key - off, 0), ql) : 0; };
     auto seen_to = [&](int key) { return key >= kl ? 0 : a.window ? min(max(key - off + a.window, 0), ql) : ql; };
     Frag<T> kf[NK][VR], vf[NK][VR];
-    T* mine = sv + wave * 2 * NK * VL * 512;
+    T* mine = sv + kgrp * 2 * NK * VL * 512;
     floatx4 dk[ND][NK], dv[ND][NK];
     const int w0 = k0 + kgrp * 16 * NK, w1 = min(w0 + 16 * NK, kl);
 #pragma unroll
@@ -131,7 +129,7 @@ __global__ __launch_bounds__(256, 2) void kda_attn_dkv_kernel(const AttnArgs a, 
             if (s < VR) {
                 kf[n][s < VR ? s : 0] = x;
                 vf[n][s < VR ? s : 0] = y;
-            } else {
+            } else if (turn == 0) {
                 frag_store(x, mine + ((s - VR) * 2 * NK + 2 * n) * 512, lane);
                 frag_store(y, mine + ((s - VR) * 2 * NK + 2 * n + 1) * 512, lane);
             }
@@ -400,10 +398,21 @@ __global__ __launch_bounds__(256, 1) void kda_attn_dq_kernel(const AttnArgs a, i
     }
 }
 
-// Key or row groups of a workgroup for a grid too small to fill the card: the waves
-// then share fewer keys or rows and take turns, as far as the LDS ring reaches (its
-// tiles hold 32 rows for each turn).
+// Key or row groups of a workgroup.  Grids that fill the card with four groups take
+// two, in two turns, so that there are workgroups left to even out a causal mask's long
+// and short tiles: bf16, D = 64, dk and dv of 4 x 4 heads of 4 query heads, 4096 tokens,
+// 294 us against 461, dq of 2 x 16 heads x 1024 19 us against 28.  Rows of more than 128
+// bytes keep four: registers and LDS then leave room for one or two workgroups a unit
+// either way (fp32, D = 128, dk and dv of 2 x 16 heads x 1024: 184 us against 205).
+template <typename T, int D> constexpr int wide_groups() { return D * (int)sizeof(T) <= 128 ? 2 : 4; }
+// Smaller grids share fewer keys or rows and take more turns, as far as the LDS ring
+// reaches (its tiles hold 32 rows for each turn).
 template <typename T, int D> constexpr int small_groups() { return D * (int)sizeof(T) >= 512 ? 2 : 1; }
+// Grids of fewer workgroups of four groups are small.  256 leave no unit idle; rows of
+// up to 64 bytes pay little for the turns and gain evenness up to 512 (bf16, D = 32, dk
+// and dv of 2 x 4 heads of 4 query heads x 4096: 109 us against 184; D = 64, 2 x 16 heads x
+// 1024: 32 us against 26).
+template <typename T, int D> constexpr int small_grid() { return D * (int)sizeof(T) <= 64 ? 512 : 256; }
 
 template <typename T, int D, int NG>
 static hipError_t launch_dkv(const AttnArgs& a, int padded, hipStream_t s) {
@@ -432,13 +441,13 @@ static hipError_t launch_bwd_t(const AttnArgs& a, hipStream_t s) {
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (a.Tk > 0) {
-        const bool small = nbh * ((a.Tk + kWide - 1) / kWide) < kSmallGrid;
-        e = attn_turns(sizeof(T), D, a, a.Tk, kTurnsKeys) ? launch_dkv_turns(D, a, padded, s) : small ? launch_dkv<T, D, kSmall>(a, padded, s) : launch_dkv<T, D, 4>(a, padded, s);
+        const bool small = nbh * ((a.Tk + kWide - 1) / kWide) < small_grid<T, D>();
+        e = attn_dkv_turns(sizeof(T), D, a) ? launch_dkv_turns(a, padded, s) : small ? launch_dkv<T, D, kSmall>(a, padded, s) : launch_dkv<T, D, wide_groups<T, D>()>(a, padded, s);
         if (e != hipSuccess) return e;
     }
     if (rows > 0) {
-        const bool small = nbh * ((rows + kWide - 1) / kWide) < kSmallGrid;
-        e = attn_turns(sizeof(T), D, a, rows, kTurnsRows) ? launch_dq_turns(D, a, padded, s) : small ? launch_dq<T, D, kSmall>(a, padded, s) : launch_dq<T, D, 4>(a, padded, s);
+        const bool small = nbh * ((rows + kWide - 1) / kWide) < small_grid<T, D>();
+        e = attn_dq_turns(sizeof(T), D, a) ? launch_dq_turns(D, a, padded, s) : small ? launch_dq<T, D, kSmall>(a, padded, s) : launch_dq<T, D, wide_groups<T, D>()>(a, padded, s);
     }
     return e;
 }

@@ -408,25 +408,16 @@ __global__ __launch_bounds__(512, 2) void kda_attn_dq_turns_kernel(const AttnArg
     });
 }
 
-hipError_t launch_dkv_turns(int D, const AttnArgs& a, int padded, hipStream_t s) {
-    const dim3 grid((unsigned)(((long long)a.Tk + 127) / 128 * a.B * a.HK)), block(32 * 16);
-    switch (D) {
-        case 32: hipLaunchKernelGGL((kda_attn_dkv_turns_kernel<32>), grid, block, 0, s, a, padded); break;
-        case 64: hipLaunchKernelGGL((kda_attn_dkv_turns_kernel<64>), grid, block, 0, s, a, padded); break;
-        case 128: hipLaunchKernelGGL((kda_attn_dkv_turns_kernel<128>), grid, block, 0, s, a, padded); break;
-        default: return hipErrorInvalidValue;
-    }
+hipError_t launch_dkv_turns(const AttnArgs& a, int padded, hipStream_t s) {
+    const dim3 grid((unsigned)turns_grid(a, a.Tk, kTurnsKeys));
+    hipLaunchKernelGGL((kda_attn_dkv_turns_kernel<128>), grid, dim3(64 * kWaves), 0, s, a, padded);
     return hipGetLastError();
 }
 
 hipError_t launch_dq_turns(int D, const AttnArgs& a, int padded, hipStream_t s) {
-    const dim3 grid((unsigned)(((long long)a.Tq * a.G + 255) / 256 * a.B * a.HK)), block(32 * 16);
-    switch (D) {
-        case 32: hipLaunchKernelGGL((kda_attn_dq_turns_kernel<32>), grid, block, 0, s, a, padded); break;
-        case 64: hipLaunchKernelGGL((kda_attn_dq_turns_kernel<64>), grid, block, 0, s, a, padded); break;
-        case 128: hipLaunchKernelGGL((kda_attn_dq_turns_kernel<128>), grid, block, 0, s, a, padded); break;
-        default: return hipErrorInvalidValue;
-    }
+    const dim3 grid((unsigned)turns_grid(a, (long long)a.Tq * a.G, kTurnsRows));
+    if (D == 128) hipLaunchKernelGGL((kda_attn_dq_turns_kernel<128>), grid, dim3(64 * kWaves), 0, s, a, padded);
+    else hipLaunchKernelGGL((kda_attn_dq_turns_kernel<64>), grid, dim3(64 * kWaves), 0, s, a, padded);
     return hipGetLastError();
 }
 

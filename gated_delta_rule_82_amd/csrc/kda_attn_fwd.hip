@@ -573,9 +573,9 @@ template <typename T, int D>
 static hipError_t launch_fwd_t(const AttnArgs& a, hipStream_t s) {
     constexpr int NQ = attn_rows_per_wave(sizeof(T)) / 16, KB = sizeof(T) == 2 ? 64 : 32;
     const long long rows = (long long)a.Tq * a.G;
-    if constexpr (sizeof(T) == 2 && D >= 32) {
-        if (a.nsplit == 1 && attn_turns(sizeof(T), D, a, rows, kTurnsRows)) {
-            hipLaunchKernelGGL((kda_attn_fwd_turns_kernel<D>), dim3((unsigned)((rows + 255) / 256 * a.B * a.HK)), dim3(512), 0, s, a);
+    if constexpr (sizeof(T) == 2 && D == 128) {
+        if (attn_fwd_turns(sizeof(T), D, a)) {
+            hipLaunchKernelGGL((kda_attn_fwd_turns_kernel<D>), dim3((unsigned)turns_grid(a, rows, kTurnsRows)), dim3(512), 0, s, a);
             return hipGetLastError();
         }
     }

@@ -123,6 +123,40 @@ def test_attn_full_grids_of_unequal_lengths(D, H, HK, Tq, Tk):
         run_both(*x, BF16, f"D {D} {kw}", ql=[min(n, Tq) for n in ql], kl=[min(n, Tk) for n in kl], **kw)
 
 
+def run_heads(q, k, v, do, picks, ql, kl, what, **kw):
+    """Both directions on the whole batch; the oracle on the (sequence, key/value head) pairs of `picks`."""
+    D, G = q.shape[-1], q.shape[2] // k.shape[2]
+    scale = D ** -0.5
+    lens = dict(q_len=ints(ql), kv_len=ints(kl))
+    o, lse = kda.attn_fwd(q, k, v, scale=scale, **lens, **kw)
+    g = kda.attn_bwd(q, k, v, o, lse, do, scale=scale, **lens, **kw)
+    torch.cuda.synchronize()
+    for b, h in picks:
+        qs, ks = (slice(b, b + 1), slice(None), slice(h * G, (h + 1) * G)), (slice(b, b + 1), slice(None), slice(h, h + 1))
+        x = [np64(t[s]) for t, s in ((q, qs), (k, ks), (v, ks), (do, qs))]
+        one = dict(q_len=None if ql is None else [ql[b]], kv_len=None if kl is None else [kl[b]], **kw)
+        wo, wl, bo, bl = fwd_bounds(*x[:3], BF16, scale, **one)
+        check(o[qs], wo, bo, f"{what} {b} {h} o")
+        check(lse[b:b + 1, h * G:(h + 1) * G], wl, bl, f"{what} {b} {h} lse")
+        grads, bounds = bwd_bounds(*x, BF16, scale, **one)
+        for n, w, bound, s in zip(("dq", "dk", "dv"), grads, bounds, (qs, ks, ks)):
+            check(g[n][s], w, bound, f"{what} {b} {h} {n}")
+
+
+@pytest.mark.parametrize("D,B,Tq,Tk,H,HK,kw,ql,kl", [
+    (128, 2, 4100, 4100, 16, 8, dict(causal=True, window=0), None, None),
+    (128, 2, 4130, 4200, 16, 8, dict(causal=True, window=4099), [4130, 4001], [4200, 4200]),
+    (128, 4, 700, 700, 64, 64, dict(causal=False, window=0), [700, 0, 33, 690], [700, 650, 700, 0]),
+    (128, 2, 2111, 1000, 16, 16, dict(causal=False, window=0), [2111, 1990], [1000, 961]),
+    (128, 2, 2111, 1000, 32, 16, dict(causal=True, window=2060), [2111, 5], [30, 1000]),
+    (64, 4, 520, 777, 64, 64, dict(causal=False, window=600), [520, 300, 1, 257], [777, 700, 777, 64]),
+    (64, 2, 2100, 2100, 16, 16, dict(causal=True, window=0), [2100, 2050], [2100, 2060]),
+])
+def test_attn_long_sequences_that_fill_the_card(D, B, Tq, Tk, H, HK, kw, ql, kl):
+    x = draw(B, Tq, Tk, H, HK, D, BF16, D + Tq, packed=True)
+    run_heads(*x, [(b, b * (HK - 1) // max(B - 1, 1)) for b in range(B)], ql, kl, f"D {D} {kw}", **kw)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("scale", [1e-3, 1.0, 30.0])
 def test_attn_scales(dtype, scale):
