@@ -15,9 +15,11 @@
 namespace kda {
 
 // Row values of every query, padded per head to whole tiles with rows that
-// contribute nothing: -lse / c and -delta, the initial accumulators of the products
-// that give S - lse / c and dP - delta (-inf makes P zero).  Four queries' values of
-// each kind lie together: rows[b][h][t / 4][kind][t % 4].
+// contribute nothing (-inf makes P zero).  bf16: -lse / c and -delta, the initial
+// accumulators of the products that give S - lse / c and dP - delta.  fp32: -lse and
+// -delta, added after the products, where S c - lse is rounded once and small (as
+// initial accumulators they doubled the gradients' error).  Four queries' values of each
+// kind lie together: rows[b][h][t / 4][kind][t % 4].
 template <typename T, int D>
 __global__ __launch_bounds__(256) void kda_attn_rows_kernel(const AttnArgs a, int padded) {
     constexpr int N = Gran16<T>::N, L = D / N;   // elements and lanes per row
@@ -41,7 +43,7 @@ __global__ __launch_bounds__(256) void kda_attn_rows_kernel(const AttnArgs a, in
     if (inside && part == 0) {
         const bool none = !live || lse == kNegInf;
         float* to = a.rows + ((size_t)b * a.H + h) * padded * 2 + (t >> 2) * 8 + (t & 3);
-        to[0] = none ? kNegInf : -lse / a.scale;
+        to[0] = none ? kNegInf : sizeof(T) == 4 ? -lse : -lse / a.scale;
         to[4] = none ? 0.f : -sum;
     }
 }
@@ -85,6 +87,7 @@ __global__ __launch_bounds__(256, 2) void kda_attn_dkv_kernel(const AttnArgs a, 
     // them live in LDS (1 KiB a fragment), or two waves would not fit a SIMD
     constexpr int VR = sizeof(T) == 2 && D == 128 ? 3 : NS, VL = NS - VR;
     constexpr int kTile = RB * D * (int)sizeof(T);
+    constexpr bool kInit = sizeof(T) == 2;   // the row values are initial accumulators
     static_assert(RB == 32 * NT && RB <= 128, "one step a wave and tile");
     constexpr int kSum = NT > 1 ? (NT - 1) * NG * 16 * NK * D * 4 : 0;   // the other turns' sums
     constexpr int kRing = 4 * kTile;
@@ -175,8 +178,8 @@ __global__ __launch_bounds__(256, 2) void kda_attn_dkv_kernel(const AttnArgs a, 
             const floatx4 de = rp[1];
             floatx4 st[NK], dp[NK];
 #pragma unroll
-            for (int n = 0; n < NK; ++n) st[n] = rp[0];
-            if (masked) {  // -inf where the key is not seen: P and dS come out zero
+            for (int n = 0; n < NK; ++n) st[n] = kInit ? rp[0] : floatx4{0.f, 0.f, 0.f, 0.f};
+            if (kInit && masked) {  // -inf where the key is not seen: P and dS come out zero
 #pragma unroll
                 for (int n = 0; n < NK; ++n) {
                     const int key = w0 + 16 * n + (lane & 15), lo = seen_from(key);
@@ -200,16 +203,25 @@ __global__ __launch_bounds__(256, 2) void kda_attn_dkv_kernel(const AttnArgs a, 
                         frag_load(y, mine + ((s - VR) * 2 * NK + 2 * n + 1) * 512, lane);
                     }
                     st[n] = mma(qf, x, st[n]);
-                    dp[n] = mma(df, y, s == 0 ? de : dp[n]);
+                    dp[n] = mma(df, y, s > 0 ? dp[n] : kInit ? de : floatx4{0.f, 0.f, 0.f, 0.f});
                 }
             }
 #pragma unroll
-            for (int n = 0; n < NK; ++n)
+            for (int n = 0; n < NK; ++n) {
+                const int key = w0 + 16 * n + (lane & 15), lo = seen_from(key);
+                const uint32_t span = max(seen_to(key) - lo, 0), first = rb + 16 * i + 4 * g - lo;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    st[n][e] = exp2_fast(st[n][e] * c);
-                    dp[n][e] *= st[n][e];
+                    if (kInit) {
+                        st[n][e] = exp2_fast(st[n][e] * c);
+                        dp[n][e] *= st[n][e];
+                    } else {
+                        const bool seen = !masked || first + e < span;
+                        st[n][e] = seen ? exp2_fast(fmaf(st[n][e], a.scale, rp[0][e]) * kLog2e) : 0.f;
+                        dp[n][e] = seen ? (dp[n][e] + de[e]) * st[n][e] : 0.f;
+                    }
                 }
+            }
 #pragma unroll
             for (int n = 0; n < NK; ++n)
 #pragma unroll
@@ -308,7 +320,7 @@ __global__ __launch_bounds__(256, 1) void kda_attn_dq_kernel(const AttnArgs a, i
             df[n][s] = row_frag_global<T, D>(dp, s, lane);
         }
         const float* x = a.rows + ((size_t)b * a.H + h) * padded * 2 + (t[n] >> 2) * 8 + (t[n] & 3);
-        ls[n] = x[0] * a.scale_log2;
+        ls[n] = sizeof(T) == 4 ? x[0] : x[0] * a.scale_log2;
         de[n] = x[4];
 #pragma unroll
         for (int d = 0; d < ND; ++d) dq[d][n] = floatx4{0.f, 0.f, 0.f, 0.f};
@@ -365,7 +377,7 @@ __global__ __launch_bounds__(256, 1) void kda_attn_dq_kernel(const AttnArgs a, i
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float p = exp2_fast(fmaf(st[i][n][e], c, ls[n]));
+                        float p = sizeof(T) == 4 ? exp2_fast(fmaf(st[i][n][e], a.scale, ls[n]) * kLog2e) : exp2_fast(fmaf(st[i][n][e], c, ls[n]));
                         if (masked) {
                             const int key = k0 + 32 * u + 16 * i + 4 * g + e;
                             p = key >= lo[n] && key <= hi[n] ? p : 0.f;

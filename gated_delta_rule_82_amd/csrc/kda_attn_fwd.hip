@@ -488,18 +488,27 @@ __global__ __launch_bounds__(256) void kda_attn_join_few_kernel(const JoinArgs a
         a.lse[((size_t)b * a.H + h) * a.Tq + t] = sum == 0.f ? kNegInf : (m + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
-// Many parts: one workgroup per packed row.  The parts' maxima and sums are read at once, one
-// a thread; then 256 / (D / 4) groups of threads take every so-manieth split's
-// output, four channels each, and are summed in LDS in a fixed order.
+// Many parts: one workgroup per packed row.  The parts' maxima and sums are read one a
+// thread, and at the same time their outputs: 256 / (D / 4) groups of threads take
+// every so-manieth part, four channels a thread, all loads in flight before the weights
+// are known, and are summed in LDS in a fixed order.  128 rows of 128 parts, D = 128
+// (8 MB): 5.5 us, against 8.1 with the outputs read after the weights.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void kda_attn_join_kernel(const JoinArgs a) {
-    constexpr int L = D / 4, NG = 256 / L;
+    constexpr int L = D / 4, NG = 256 / L, P = kMaxSplits / NG;
     __shared__ float weight[kMaxSplits];
     __shared__ float red[2][4];
     __shared__ floatx4 part[NG][L];
     const int rows = a.Tq * a.G, tid = threadIdx.x;
     const size_t n = (size_t)a.B * a.HK * rows, at = blockIdx.x;
     const float2 x = tid < a.nsplit ? reinterpret_cast<const float2*>(a.part_ml)[tid * n + at] : make_float2(kNegInf, 0.f);
+    const int grp = tid / L, d = (tid % L) * 4;
+    floatx4 y[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const int s = grp + i * NG;
+        y[i] = s < a.nsplit ? *reinterpret_cast<const floatx4*>(a.part_o + (s * n + at) * D + d) : floatx4{0.f, 0.f, 0.f, 0.f};
+    }
     float m = x.x;
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
@@ -514,13 +523,13 @@ __global__ __launch_bounds__(256) void kda_attn_join_kernel(const JoinArgs a) {
     if ((tid & 63) == 0) red[1][tid >> 6] = sum;
     __syncthreads();
     sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
-    const int grp = tid / L, d = (tid % L) * 4;
     floatx4 o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int s = grp; s < a.nsplit; s += NG) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const int s = grp + i * NG;
+        if (s >= a.nsplit) break;
         const float f = weight[s];
-        const floatx4 y = *reinterpret_cast<const floatx4*>(a.part_o + (s * n + at) * D + d);
-        o += f == 0.f ? floatx4{0.f, 0.f, 0.f, 0.f} : f * y;
+        o += f == 0.f ? floatx4{0.f, 0.f, 0.f, 0.f} : f * y[i];
     }
     part[grp][tid % L] = o;
     __syncthreads();
