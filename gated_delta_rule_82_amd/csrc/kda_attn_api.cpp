@@ -15,13 +15,29 @@ constexpr double kLog2eD = 1.44269504088896340736;
 
 bool heads_ok(int H, int HK) { return H >= 0 && HK >= 0 && (H == 0 || (HK > 0 && H % HK == 0)); }
 
-bool attn_sizes_ok(int B, int Tq, int Tk, int H, int HK) {
-    if (!heads_ok(H, HK) || !sizes_ok(B, Tq, H) || !sizes_ok(B, Tk, HK)) return false;
+bool rows_ok(int B, int Tq, int H, int HK) {
+    if (!heads_ok(H, HK) || !sizes_ok(B, Tq, H)) return false;
     if (H == 0) return true;
-    // packed rows of one key/value head, and 2^24 workgroups of 64 rows or keys
-    // (a grid holds less than 2^32 threads)
-    const unsigned long long rows = (unsigned long long)(H / HK) * Tq, bh = (unsigned long long)B * HK;
-    return rows <= (1ull << 29) && Tk <= (1 << 29) && bh * (rows / 64 + 1) < (1ull << 24) && bh * ((unsigned long long)Tk / 64 + 1) < (1ull << 24);
+    // packed rows of one key/value head, and less than 2^24 workgroups of 32 of them
+    // (a grid holds less than 2^32 threads, a workgroup 256)
+    const unsigned long long rows = (unsigned long long)(H / HK) * Tq;
+    return rows <= (1ull << 29) && (unsigned long long)B * HK * (rows / 32 + 1) < (1ull << 24);
+}
+
+// Keys in one piece: as many workgroups of them in the backward.
+bool attn_sizes_ok(int B, int Tq, int Tk, int H, int HK) {
+    if (!rows_ok(B, Tq, H, HK) || !sizes_ok(B, Tk, HK)) return false;
+    return Tk <= (1 << 29) && (unsigned long long)B * HK * ((unsigned long long)Tk / 32 + 1) < (1ull << 24);
+}
+
+// The backward has a thread for each 16 bytes of a row of o, rows padded.
+bool row_pieces_ok(int B, int Tq, int H, int D, kda_dtype dt) {
+    return (unsigned long long)B * H * ((unsigned long long)Tq + kda::kAttnRowPad) * (D * elem_bytes(dt) / 16) < (1ull << 32);
+}
+
+// A paged cache: its length only bounds a loop.
+bool step_sizes_ok(int B, int Tq, int H, int HK, int max_len) {
+    return max_len >= 0 && max_len <= (1 << 29) && rows_ok(B, Tq, H, HK);
 }
 
 // Row stride in elements: 0 selects contiguous tokens.
@@ -182,7 +198,9 @@ kda_status kda_attn_fwd(const void* q, const void* k, const void* v, const int* 
 }
 
 size_t kda_attn_bwd_workspace(int B, int Tq, int Tk, int H, int HK, int D, kda_dtype dt) {
-    if (!dtype_ok(dt) || !dim_ok(D) || !attn_sizes_ok(B, Tq, Tk, H, HK) || B == 0 || H == 0 || Tq == 0) return 0;
+    if (!dtype_ok(dt) || !dim_ok(D) || !attn_sizes_ok(B, Tq, Tk, H, HK) || B == 0 || H == 0 || Tq == 0 ||
+        !row_pieces_ok(B, Tq, H, D, dt))
+        return 0;
     return round256((size_t)B * H * padded_rows(Tq) * 8);
 }
 
@@ -192,7 +210,8 @@ kda_status kda_attn_bwd(const void* q, const void* k, const void* v, const int* 
                         float scale, int causal, int window, kda_dtype dt,
                         void* workspace, size_t workspace_bytes, hipStream_t stream) {
     if (!dtype_ok(dt)) return KDA_ERR_DTYPE;
-    if (!dim_ok(D) || !attn_sizes_ok(B, Tq, Tk, H, HK) || window < 0) return KDA_ERR_SHAPE;
+    if (!dim_ok(D) || !attn_sizes_ok(B, Tq, Tk, H, HK) || !row_pieces_ok(B, Tq, H, D, dt) || window < 0)
+        return KDA_ERR_SHAPE;
     if (!scale_ok(scale)) return KDA_ERR_SCALE;
     kda::AttnArgs a{};
     KDA_TRY(stride(ldq, H, D, dt, &a.ldq)); KDA_TRY(stride(ldk, HK, D, dt, &a.ldk)); KDA_TRY(stride(ldv, HK, D, dt, &a.ldv));
@@ -258,7 +277,7 @@ kda_status kda_cache_append(const void* k, const void* v, void* k_cache, void* v
 }
 
 size_t kda_attn_step_workspace(int B, int Tq, int H, int HK, int D, int max_len) {
-    if (!dim_ok(D) || max_len < 0 || !attn_sizes_ok(B, Tq, max_len, H, HK) || B == 0 || H == 0 || Tq == 0) return 0;
+    if (!dim_ok(D) || !step_sizes_ok(B, Tq, H, HK, max_len) || B == 0 || H == 0 || Tq == 0) return 0;
     return split_bytes(kda::attn_step_splits(B, Tq, HK, H / HK, max_len), (size_t)B * Tq * H, D);
 }
 
@@ -270,7 +289,7 @@ kda_status kda_attn_step(const void* q, const void* k_cache, const void* v_cache
     if (!dtype_ok(dt)) return KDA_ERR_DTYPE;
     if (HK < 0 || !cache_sizes_ok(n_pages, max_pages, B, Tq, HK, D, page) || window < 0) return KDA_ERR_SHAPE;
     const int max_len = max_pages * page;
-    if (!attn_sizes_ok(B, Tq, max_len, H, HK)) return KDA_ERR_SHAPE;
+    if (!step_sizes_ok(B, Tq, H, HK, max_len)) return KDA_ERR_SHAPE;
     if (!scale_ok(scale)) return KDA_ERR_SCALE;
     kda::AttnStepArgs a{};
     KDA_TRY(stride(ldq, H, D, dt, &a.ldq));

@@ -372,12 +372,19 @@ kda_status kda_chunk_bwd_grouped(const void* q, const void* k, const void* v, co
  *
  * Row strides: ld* is the distance between consecutive tokens of a tensor in
  * elements (0 selects heads * D, a contiguous tensor; otherwise at least that
- * and a multiple of 16 bytes, and at most 2^23 elements); sequences are T * ld apart and heads D apart,
- * so q, k and v may be the parts of one packed projection [B,T,H+2HK,D].
+ * and a multiple of 16 bytes, and at most 2^23 elements); sequences are T * ld
+ * apart and heads D apart, so q, k and v may be the parts of one packed
+ * projection [B,T,H+2HK,D].
  *
  * Lengths: device arrays of B ints, read when the kernels run; values outside
  * the tensor's range are clamped to it.  Nothing at or past a sequence's
- * length is read, whatever it holds. */
+ * length is read, whatever it holds.
+ *
+ * Sizes (KDA_ERR_SHAPE past them): Tk, max_pages * page and the rows G * Tq of
+ * a key/value head up to 2^29; B * HK * (G * Tq / 32 + 1) and B * HK *
+ * (Tk / 32 + 1) below 2^24; in the backward the 16-byte pieces of o, 64 tokens
+ * a sequence on top, below 2^32; B * T * D of a rotation below 2^32; pages that
+ * an append may touch, B * HK * (T / page + 2), below 2^24. */
 
 /* Inverse frequencies of the rotary position encoding for `rot` channels
  * (positive, even, at most 128):
@@ -455,7 +462,8 @@ kda_status kda_attn_fwd(const void* q, const void* k, const void* v, const int* 
  * atomics: results do not vary from run to run.
  *   o, dout, dq [B,Tq,H,D], dk, dv [B,Tk,HK,D]: contiguous, dtype dt.  Rows
  *   past the lengths, and rows that see or are seen by nothing, get 0; o, lse
- *   and dout are not read past q_len.
+ *   and dout are not read past q_len.  What is not finite inside the lengths
+ *   may reach the gradients of rows and keys of the same tile too.
  *   workspace  kda_attn_bwd_workspace bytes, 256-byte aligned.
  * Outputs may overlap neither an input, another output nor the workspace
  * (KDA_ERR_SHAPE).  Errors otherwise as kda_attn_fwd. */

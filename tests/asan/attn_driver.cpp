@@ -28,9 +28,15 @@ static void attn_sizes(const AttnArgs& a) {
     expect(a.G >= 1 && a.H == a.G * a.HK && a.nsplit >= 1, "attention sizes");
     expect((unsigned long long)a.Tq * a.G <= (1ull << 29) && a.Tk <= (1 << 29) && a.window >= 0 && (a.window == 0 || a.window < a.Tk), "attention rows");
     expect(a.nsplit == 1 || (a.part_o && a.part_ml), "attention partials");
+    const unsigned long long bh = (unsigned long long)a.B * a.HK, rows = (unsigned long long)a.Tq * a.G;
+    expect(bh * ((rows + 31) / 32) < (1ull << 24) && bh * (((unsigned long long)a.Tk + 31) / 32) < (1ull << 24), "attention grids");
+}
+static void row_pieces(int dt, int D, const AttnArgs& a) {
+    const unsigned long long padded = ((unsigned long long)a.Tq + kAttnRowPad - 1) / kAttnRowPad * kAttnRowPad;
+    expect(a.B * (unsigned long long)a.H * padded * (D * (dt == 1 ? 2 : 4) / 16) + 255 < (1ull << 32), "row pieces");
 }
 hipError_t launch_attn_fwd(int, int, const AttnArgs& a, hipStream_t) { ++g_launches; attn_sizes(a); return hipSuccess; }
-hipError_t launch_attn_bwd(int, int, const AttnArgs& a, hipStream_t) { ++g_launches; attn_sizes(a); return hipSuccess; }
+hipError_t launch_attn_bwd(int dt, int D, const AttnArgs& a, hipStream_t) { ++g_launches; attn_sizes(a); row_pieces(dt, D, a); return hipSuccess; }
 hipError_t launch_cache_append(int, int, const AppendArgs& a, hipStream_t) {
     ++g_launches;
     expect((unsigned long long)a.B * a.HK * ((unsigned long long)a.T / a.page + 2) < (1ull << 24), "append grid");
@@ -39,6 +45,7 @@ hipError_t launch_cache_append(int, int, const AppendArgs& a, hipStream_t) {
 hipError_t launch_attn_step(int, int, const AttnStepArgs& a, hipStream_t) {
     ++g_launches;
     expect((long long)a.max_pages * a.page <= (1 << 29) && a.nsplit >= 1, "step sizes");
+    expect((unsigned long long)a.B * a.HK * (((unsigned long long)a.Tq * a.G + 31) / 32) * a.nsplit < (1ull << 24), "step grid");
     return hipSuccess;
 }
 }  // namespace kda

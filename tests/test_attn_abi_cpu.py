@@ -95,6 +95,19 @@ BAD_SIZES = [dict(D=48), dict(D=256), dict(D=0), dict(B=-1), dict(Tq=-1), dict(T
              dict(B=2 ** 22, Tk=4096), dict(H=2 ** 22, HK=1, Tq=2 ** 12), dict(ldq=128), dict(ldk=64), dict(ldv=-128)]
 
 
+def test_attn_bwd_refuses_more_row_pieces_than_a_grid_holds(lib):
+    big = dict(B=1, Tq=2 ** 20, Tk=1, H=160, HK=160, D=128, dt=0, ws_bytes=1 << 40, causal=0)
+    assert call(lib.kda_attn_bwd, BWD, **big) == SHAPE
+    assert lib.kda_attn_bwd_workspace(1, 2 ** 20, 1, 160, 160, 128, 0) == 0
+    assert lib.kda_attn_bwd_workspace(1, 2 ** 20, 1, 100, 100, 128, 0) > 0
+
+
+def test_attn_step_takes_long_caches(lib):
+    """The cache's length bounds no grid: 256 sequences of up to 2^20 tokens."""
+    assert lib.kda_attn_step_workspace(256, 1, 32, 8, 128, 2 ** 20) == 0      # enough workgroups without a split
+    assert lib.kda_attn_step_workspace(1, 1, 32, 8, 128, 2 ** 20) > 0
+
+
 def test_attn_fwd_refusals(lib):
     f = lambda **kw: call(lib.kda_attn_fwd, ATTN, **kw)  # noqa: E731
     assert f(dt=9) == DTYPE
