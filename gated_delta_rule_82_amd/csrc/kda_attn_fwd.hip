@@ -7,7 +7,15 @@
 // a row's scores into one lane column, so the maximum needs two lane swaps, the
 // rescale is one factor per lane, and the exponentials are, as they stand, the
 // right operand of O^T += V^T P^T.  Keys and values go through a two-deep LDS
-// ring filled by direct loads while the previous tile is used.
+// ring filled by direct loads while the previous tile is used.  Few query rows: the
+// key axis is split over workgroups and joined.
+//
+// Long rows are bound by the matrix cores beside the vector unit (an exponential, a
+// multiply-add, a maximum, a sum and half a rounding for every 4 D flops), few rows by
+// the keys and values read.  bf16, D = 128: 4 x 16 heads (4 of keys) x 4096 causal 259 us,
+// 1.06 PFLOP/s (a large matrix product reaches 1.14); 16 tokens of 32 heads behind
+// 65 536 keys of 8 62 us with the join, 4.3 TB/s.  fp32, D = 64, 2 x 4 heads x 1023 with
+// unequal lengths: 30 us, 42 TFLOP/s of 154 (workgroups that end early are not made up for).
 #include "kda_attn_device.h"
 
 namespace kda {

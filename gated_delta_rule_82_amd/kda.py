@@ -433,7 +433,7 @@ def _launch(name, dev, *args):
     """Calls an entry point on the current stream of `dev`, which becomes the current
     device for the call (a null stream handle names the current device's stream)."""
     fn = getattr(_lib or load(), name)
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev.index:
         st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     else:
         with torch.cuda.device(dev):
@@ -451,6 +451,11 @@ def _expect(name, t, shape, dtype, dev):
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
     raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _like(t):
+    """A contiguous tensor of t's shape, type and device (the quickest way to allocate one)."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _rows(name, t):
@@ -517,7 +522,7 @@ def rotary(q, k, inv_freq, positions=None, *, scale=1.0, interleaved=False, inve
     _expect("inv_freq", inv_freq, (pairs,), torch.float64, dev)
     _expect("positions", positions, (B, T), torch.int32, dev)
     if q_out is None:
-        q_out = torch.empty((B, T, H, D), dtype=dt, device=dev)
+        q_out = _like(q)
     else:
         _expect("q_out", q_out, q.shape, dt, dev)
     qp, ldq = _rows("q", q)
@@ -528,7 +533,7 @@ def rotary(q, k, inv_freq, positions=None, *, scale=1.0, interleaved=False, inve
         HK = k.shape[2]
         _expect("k", k, (B, T, HK, D), dt, dev)
         if k_out is None:
-            k_out = torch.empty((B, T, HK, D), dtype=dt, device=dev)
+            k_out = _like(k)
         else:
             _expect("k_out", k_out, k.shape, dt, dev)
         kp, ldk = _rows("k", k)
@@ -552,7 +557,7 @@ def attn_fwd(q, k, v, *, scale=None, causal=True, window=0, q_len=None, kv_len=N
     B, Tq, Tk, H, HK, D = _attn_shapes(q, k, v, q_len, kv_len)
     dev, dt = q.device, q.dtype
     if o is None:
-        o = torch.empty((B, Tq, H, D), dtype=dt, device=dev)
+        o = _like(q)
     else:
         _expect("o", o, (B, Tq, H, D), dt, dev)
     if lse is None:
@@ -579,8 +584,7 @@ def attn_bwd(q, k, v, o, lse, dout, *, scale=None, causal=True, window=0, q_len=
     _expect("o", o, (B, Tq, H, D), dt, dev)
     _expect("lse", lse, (B, H, Tq), torch.float32, dev)
     _expect("dout", dout, (B, Tq, H, D), dt, dev)
-    g = {"dq": torch.empty((B, Tq, H, D), dtype=dt, device=dev), "dk": torch.empty((B, Tk, HK, D), dtype=dt, device=dev),
-         "dv": torch.empty((B, Tk, HK, D), dtype=dt, device=dev)}
+    g = {"dq": _like(q), "dk": _like(k), "dv": _like(k)}
     (qp, ldq), (kp, ldk), (vp, ldv) = _rows("q", q), _rows("k", k), _rows("v", v)
     ws = _workspace(attn_bwd_workspace_bytes(B, Tq, Tk, H, HK, D, dt), workspace, dev)
     _launch("kda_attn_bwd", dev, qp, kp, vp, _ptr(q_len), _ptr(kv_len), _ptr(o), _ptr(lse), _ptr(dout), _ptr(g["dq"]),
@@ -644,7 +648,7 @@ def attn_step(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_len, new
     n_pages, HK, page, max_pages = _cache_shapes(k_cache, v_cache, k_scale, v_scale, block_table, cache_len, new_len,
                                                  B, D, dev)
     if o is None:
-        o = torch.empty((B, Tq, H, D), dtype=dt, device=dev)
+        o = _like(q)
     else:
         _expect("o", o, (B, Tq, H, D), dt, dev)
     qp, ldq = _rows("q", q)
