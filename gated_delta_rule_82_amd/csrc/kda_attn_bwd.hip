@@ -4,7 +4,9 @@
 //   dv_j = sum_i P_ij dout_i,  dS_ij = P_ij (dout_i.v_j - delta_i)
 //   dq_i = c sum_j dS_ij k_j,  dk_j = c sum_i dS_ij q_i
 //
-// Three kernels: the row values (lse, delta); dk and dv, one workgroup per tile
+// Three kernels: the row values (lse, delta; formed in the dq kernel instead they cost
+// it as much as this launch takes, 395 us against 362 for the first size below, o and dout
+// arriving there with nothing else in flight); dk and dv, one workgroup per tile
 // of keys, over the packed rows that see it (all query heads of the key/value
 // head, so shared heads are summed in registers); dq, one workgroup per tile of
 // packed rows.  Scores and dout.v are formed twice (7 products instead of 5):
@@ -170,8 +172,10 @@ __global__ __launch_bounds__(256, 2) void kda_attn_dkv_kernel(const AttnArgs a, 
                   lds0 + buf * 2 * kTile, wave);
         dst.issue(buffer_window(dobase + t0 * ldo + (size_t)h * D, (left * (long long)ldo + D) * (long long)sizeof(T)),
                   lds0 + (buf * 2 + 1) * kTile, wave);
-        // the row array is padded to whole tiles; lanes past a tile's rows read zeros past the window, into the spare room
-        if (wave == 0) copy_to_lds(buffer_window(rbase + 2 * ((size_t)h * padded + t0), RB * 8), lane * 16, lds_rows + buf * 1024);
+        // a step's 32 rows are within the padding; past it, and past the tile's rows, lanes read zeros past the
+        // window, into rows of no step and the spare room
+        if (wave == 0)
+            copy_to_lds(buffer_window(rbase + 2 * ((size_t)h * padded + t0), min(RB, padded - t0) * 8), lane * 16, lds_rows + buf * 1024);
     };
 
     const TileLane<T, D> at(lane);
