@@ -79,7 +79,8 @@ size_t split_bytes(int n, size_t rows, int D) {
 // Queries per head in the backward's row array.
 size_t padded_rows(int Tq) { return ((size_t)Tq + kda::kAttnRowPad - 1) / kda::kAttnRowPad * kda::kAttnRowPad; }
 
-bool scale_ok(float s) { return s > 0.f && isfinite((float)(s * kLog2eD)); }  // the kernels use it times log2 e
+// The kernels use it times log2 e, the backward lse over it.
+bool scale_ok(float s) { return s >= 0x1p-64f && isfinite((float)(s * kLog2eD)); }
 
 // A window as long as the key axis hides nothing.
 int clamp_window(int w, int keys) { return w >= keys ? 0 : w; }

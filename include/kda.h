@@ -49,7 +49,7 @@ typedef enum {
     KDA_ERR_WORKSPACE = 6, /* workspace NULL, misaligned or too small           */
     KDA_ERR_HIP = 7,       /* a kernel launch failed                             */
     KDA_ERR_SCRATCH = 8,   /* kda_chunk_fwd_noalloc: sizes beyond its scratch   */
-    KDA_ERR_SCALE = 9      /* a scale is not finite (or, for softmax, not > 0)  */
+    KDA_ERR_SCALE = 9      /* a scale is not finite (for softmax: or below 2^-64) */
 } kda_status;
 
 typedef enum { KDA_F32 = 0, KDA_BF16 = 1 } kda_dtype;
@@ -438,7 +438,7 @@ kda_status kda_rotary(const void* q, const void* k, void* q_out, void* k_out, co
  * lse = -infinity.
  *   q_len, kv_len  [B] int device or NULL (Tq, Tk).
  *   o    [B,Tq,H,D] contiguous, dtype dt;  lse [B,H,Tq] fp32 or NULL.
- *   scale  finite and positive (KDA_ERR_SCALE otherwise).
+ *   scale  at least 2^-64, and finite times log2 e (KDA_ERR_SCALE otherwise).
  *   workspace  kda_attn_fwd_workspace bytes, 256-byte aligned: partial results
  *        of calls with few query rows, whose key axis is split over several
  *        workgroups (0 bytes, and NULL accepted, for the others).

@@ -102,6 +102,12 @@ def test_attn_bwd_refuses_more_row_pieces_than_a_grid_holds(lib):
     assert lib.kda_attn_bwd_workspace(1, 2 ** 20, 1, 100, 100, 128, 0) > 0
 
 
+def test_attn_refuses_scales_whose_inverse_overflows_the_statistics(lib):
+    for f, args in ((lib.kda_attn_fwd, ATTN), (lib.kda_attn_bwd, BWD)):
+        assert call(f, args, scale=1e-37) == SCALE and call(f, args, scale=2.0 ** -65) == SCALE
+        assert call(f, args, scale=2.0 ** -64, B=0) == 0
+
+
 def test_attn_step_takes_long_caches(lib):
     """The cache's length bounds no grid: 256 sequences of up to 2^20 tokens."""
     assert lib.kda_attn_step_workspace(256, 1, 32, 8, 128, 2 ** 20) == 0      # enough workgroups without a split

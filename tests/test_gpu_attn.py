@@ -165,6 +165,12 @@ def test_attn_scales(dtype, scale):
     run_both(q, k, v, do, dtype, f"scale {scale}", scale=scale, causal=True, window=0)
 
 
+def test_attn_smallest_scale():
+    """Uniform rows: the gradients of v are means of dout, the others vanish."""
+    q, k, v, do = draw(1, 70, 70, 2, 2, 64, BF16, 21)
+    run_both(q, k, v, do, BF16, "scale 2^-64", scale=2.0 ** -64, causal=True, window=0)
+
+
 def test_attn_equal_rows_and_large_magnitudes():
     q, k, v, do = draw(1, 40, 40, 2, 1, 64, BF16, 12)
     k.zero_()
