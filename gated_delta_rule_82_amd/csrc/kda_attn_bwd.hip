@@ -25,10 +25,10 @@
 namespace kda {
 
 // Row values of every query, padded per head to whole tiles with rows that
-// contribute nothing (-inf makes P zero).  bf16: -lse / c and -delta, the initial
-// accumulators of the products that give S - lse / c and dP - delta.  fp32: -lse and
-// -delta, added after the products, where S c - lse is rounded once and small (as
-// initial accumulators they doubled the gradients' error).  Four queries' values of each
+// contribute nothing (-inf makes P zero): -lse / c in bf16, the initial accumulators of
+// the product that gives S - lse / c; in fp32 -lse, added after the product, where
+// S c - lse is rounded once and small (as initial accumulators they doubled the gradients'
+// error); and -delta.  Four queries' values of each
 // kind lie together: rows[b][h][t / 4][kind][t % 4].
 template <typename T, int D>
 __global__ __launch_bounds__(256) void kda_attn_rows_kernel(const AttnArgs a, int padded) {
@@ -55,6 +55,78 @@ __global__ __launch_bounds__(256) void kda_attn_rows_kernel(const AttnArgs a, in
         float* to = a.rows + ((size_t)b * a.H + h) * padded * 2 + (t >> 2) * 8 + (t & 3);
         to[0] = none ? kNegInf : sizeof(T) == 4 ? -lse : -lse / a.scale;
         to[4] = none ? 0.f : -sum;
+    }
+}
+
+// P of a score q.k: in fp32 from -lse, in bf16 from -lse log2 e (see the row values).
+template <typename T> __device__ __forceinline__ float row_lse(float lse) { return sizeof(T) == 4 ? -lse : -lse * kLog2e; }
+template <typename T> __device__ __forceinline__ float probability(const AttnArgs& a, float score, float ls) {
+    return sizeof(T) == 4 ? exp_carried(fmaf(score, a.scale, ls)) : exp2_fast(fmaf(score, a.scale_log2, ls));
+}
+
+// The same row values where rows see few keys: delta = sum_j P_ij dP_ij / sum_j P_ij, from
+// the very dP that the gradients are formed with (same products in the same order) and
+// weights that add up to one.  dS is a difference that nearly vanishes there, and o's
+// rounding (in fp32 that of the other order) shows in it: gradients of bf16 rows of two to
+// five keys came out 1.3 to 2 times less precise, of fp32 ones up to eight times; in fp32
+// lse is corrected by the sum's logarithm for the same reason.  Where the sum is not one,
+// lse and o are those of more keys than these, and delta is dout.o as above.
+// 16 padded packed rows a wave, fragments straight from memory.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void kda_attn_rows_few_kernel(const AttnArgs a, int padded) {
+    constexpr int NS = TileGeom<T, D>::NS;
+    const int lane = threadIdx.x & 63, g = lane >> 4;
+    const size_t at = (size_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int nbh = a.B * a.HK, bh = (int)(at % nbh), b = bh / a.HK, hk = bh % a.HK;
+    if (at / nbh >= (size_t)padded * a.G / 16) return;
+    const int r0 = (int)(at / nbh) * 16, r = r0 + (lane & 15), t = (int)fdiv((uint32_t)r, a.divG), h = hk * a.G + (r - t * a.G);
+    const int ql = seq_len(a.q_len, b, a.Tq), kl = seq_len(a.kv_len, b, a.Tk), off = kl - ql;
+    const RowRange mine = row_range(a, r0, r0 + 16, ql, kl);
+    const int hi = a.causal ? min(kl - 1, t + off) : kl - 1, lo = a.window ? t + off - a.window + 1 : 0;
+    const int tr = max(min(t, ql - 1), 0);
+    const T* qp = reinterpret_cast<const T*>(a.q) + ((size_t)b * a.Tq + tr) * a.ldq + (size_t)h * D;
+    const size_t row = (((size_t)b * a.Tq + tr) * a.H + h) * D;
+    Frag<T> qf[NS], df[NS];
+    float delta_o = 0.f;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+        qf[s] = row_frag_global<T, D>(qp, s, lane);
+        df[s] = row_frag_global<T, D>(reinterpret_cast<const T*>(a.dout) + row, s, lane);
+        const Frag<T> of = row_frag_global<T, D>(reinterpret_cast<const T*>(a.o) + row, s, lane);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) delta_o = fmaf((float)df[s].v[j], (float)of.v[j], delta_o);
+    }
+    const float lse = t < ql ? a.lse[((size_t)b * a.H + h) * a.Tq + t] : kNegInf, ls = row_lse<T>(lse);
+    float sum = 0.f, delta = 0.f;
+    for (int k0 = mine.key_lo & ~15; k0 < mine.key_hi; k0 += 16) {
+        const int kr = min(k0 + (lane & 15), kl - 1);
+        const T* kp = reinterpret_cast<const T*>(a.k) + ((size_t)b * a.Tk + kr) * a.ldk + (size_t)hk * D;
+        const T* vp = reinterpret_cast<const T*>(a.v) + ((size_t)b * a.Tk + kr) * a.ldv + (size_t)hk * D;
+        floatx4 st = {0.f, 0.f, 0.f, 0.f}, dp = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+            st = mma(row_frag_global<T, D>(kp, s, lane), qf[s], st);
+            dp = mma(row_frag_global<T, D>(vp, s, lane), df[s], dp);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int key = k0 + 4 * g + e;
+            if (key < lo || key > hi) continue;
+            const float p = probability<T>(a, st[e], ls);
+            sum += p;
+            delta = fmaf(p, dp[e], delta);
+        }
+    }
+    sum = group_add4(sum);
+    delta = group_add4(delta);
+    delta_o = group_add4(delta_o);
+    if (g == 0) {
+        const bool none = lse == kNegInf;
+        const float d = sum - 1.f;
+        const bool own = fabsf(d) < 1.f / 256;
+        float* to = a.rows + ((size_t)b * a.H + h) * padded * 2 + (t >> 2) * 8 + (t & 3);
+        to[0] = none ? kNegInf : sizeof(T) == 2 ? -lse / a.scale : own ? -(lse + (d - 0.5f * d * d)) : -lse;
+        to[4] = none ? 0.f : own ? -delta / sum : -delta_o;
     }
 }
 
@@ -187,7 +259,6 @@ __global__ __launch_bounds__(256, 2) void kda_attn_dkv_kernel(const AttnArgs a, 
         for (int i = 0; i < 2; ++i) {
             if (VL > 0) asm volatile("" ::: "memory");  // the second half reads its fragments again instead of keeping them
             const floatx4* rp = reinterpret_cast<const floatx4*>(rows + 2 * (16 * i + 4 * g));
-            const floatx4 de = rp[1];
             floatx4 st[NK], dp[NK];
 #pragma unroll
             for (int n = 0; n < NK; ++n) st[n] = kInit ? rp[0] : floatx4{0.f, 0.f, 0.f, 0.f};
@@ -215,9 +286,10 @@ __global__ __launch_bounds__(256, 2) void kda_attn_dkv_kernel(const AttnArgs a, 
                         frag_load(y, mine + ((s - VR) * 2 * NK + 2 * n + 1) * 512, lane);
                     }
                     st[n] = mma(qf, x, st[n]);
-                    dp[n] = mma(df, y, s > 0 ? dp[n] : kInit ? de : floatx4{0.f, 0.f, 0.f, 0.f});
+                    dp[n] = mma(df, y, s > 0 ? dp[n] : floatx4{0.f, 0.f, 0.f, 0.f});
                 }
             }
+            const floatx4 de = rp[1];
 #pragma unroll
             for (int n = 0; n < NK; ++n) {
                 const int key = w0 + 16 * n + (lane & 15), lo = seen_from(key);
@@ -226,10 +298,10 @@ __global__ __launch_bounds__(256, 2) void kda_attn_dkv_kernel(const AttnArgs a, 
                 for (int e = 0; e < 4; ++e) {
                     if (kInit) {
                         st[n][e] = exp2_fast(st[n][e] * c);
-                        dp[n][e] *= st[n][e];
+                        dp[n][e] = (dp[n][e] + de[e]) * st[n][e];
                     } else {
                         const bool seen = !masked || first + e < span;
-                        st[n][e] = seen ? exp2_fast(fmaf(st[n][e], a.scale, rp[0][e]) * kLog2e) : 0.f;
+                        st[n][e] = seen ? probability<T>(a, st[n][e], rp[0][e]) : 0.f;
                         dp[n][e] = seen ? (dp[n][e] + de[e]) * st[n][e] : 0.f;
                     }
                 }
@@ -350,7 +422,6 @@ __global__ __launch_bounds__(256, 1) void kda_attn_dq_kernel(const AttnArgs a, i
         vst.issue(buffer_window(vbase + k0 * a.ldv, (left * (long long)a.ldv + D) * (long long)sizeof(T)), lds0 + (buf * 2 + 1) * kTile, wave);
     };
     const TileLane<T, D> at(lane);
-    const float c = a.scale_log2;
     if (k_beg < k_end) stage(k_beg, 0);
     for (int kt = k_beg; kt < k_end; ++kt) {
         const int buf = (kt - k_beg) & 1, k0 = kt * KB;
@@ -389,7 +460,7 @@ __global__ __launch_bounds__(256, 1) void kda_attn_dq_kernel(const AttnArgs a, i
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float p = sizeof(T) == 4 ? exp2_fast(fmaf(st[i][n][e], a.scale, ls[n]) * kLog2e) : exp2_fast(fmaf(st[i][n][e], c, ls[n]));
+                        float p = probability<T>(a, st[i][n][e], ls[n]);
                         if (masked) {
                             const int key = k0 + 32 * u + 16 * i + 4 * g + e;
                             p = key >= lo[n] && key <= hi[n] ? p : 0.f;
@@ -460,8 +531,13 @@ static hipError_t launch_bwd_t(const AttnArgs& a, hipStream_t s) {
     const int padded = (a.Tq + kAttnRowPad - 1) / kAttnRowPad * kAttnRowPad;
     hipError_t e = hipSuccess;
     if (rows > 0) {
-        const size_t threads = (size_t)a.B * a.H * padded * (D * sizeof(T) / 16);
-        hipLaunchKernelGGL((kda_attn_rows_kernel<T, D>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, a, padded);
+        if (attn_few_keys(a)) {
+            const size_t waves = (size_t)nbh * padded * a.G / 16;
+            hipLaunchKernelGGL((kda_attn_rows_few_kernel<T, D>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, s, a, padded);
+        } else {
+            const size_t threads = (size_t)a.B * a.H * padded * (D * sizeof(T) / 16);
+            hipLaunchKernelGGL((kda_attn_rows_kernel<T, D>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, a, padded);
+        }
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (a.Tk > 0) {

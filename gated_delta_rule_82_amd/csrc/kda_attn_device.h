@@ -91,6 +91,14 @@ template <int D> __device__ __forceinline__ int wide_swizzle(int row) {
     return ((4 * (row / RPL)) & (GR - 1) & 12) | ((row >> 3) & 3);
 }
 
+// e^x for x <= about 0 with the rounding of x log2 e carried along (without it the result
+// is off by up to |x| 2^-25 besides the instruction's own error).
+__device__ __forceinline__ float exp_carried(float x) {
+    constexpr float kLog2eLow = 1.92596299e-8f;   // log2 e - kLog2e
+    const float hi = x * kLog2e, lo = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -hi)), y = exp2_fast(hi);
+    return y == 0.f ? 0.f : fmaf(y, lo * kLn2, y);
+}
+
 // A window of memory for buffer loads: reads at or past `bytes` give zero.
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ u32x4 buffer_window(const void* p, long long bytes) {

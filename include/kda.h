@@ -459,7 +459,9 @@ kda_status kda_attn_fwd(const void* q, const void* k, const void* v, const int* 
  *   dv_j = sum_i P_ij dout_i,   dS_ij = P_ij (dout_i.v_j - dout_i.o_i),
  *   dq_i = scale sum_j dS_ij k_j,   dk_j = scale sum_i dS_ij q_i,
  * dk and dv summed over the G query heads of each key/value head.  No
- * atomics: results do not vary from run to run.
+ * atomics: results do not vary from run to run.  k and v may be a part of the
+ * keys that o and lse were formed with (causal = 0, window = 0): dk and dv are
+ * then that part's, and dq its share of the sum.
  *   o, dout, dq [B,Tq,H,D], dk, dv [B,Tk,HK,D]: contiguous, dtype dt.  Rows
  *   past the lengths, and rows that see or are seen by nothing, get 0; o, lse
  *   and dout are not read past q_len.  What is not finite inside the lengths

@@ -165,6 +165,47 @@ def test_attn_scales(dtype, scale):
     run_both(q, k, v, do, dtype, f"scale {scale}", scale=scale, causal=True, window=0)
 
 
+@pytest.mark.parametrize("cut", [1, 13, 40])
+def test_attn_bwd_over_parts_of_the_keys(cut):
+    """Key axis in two calls with the whole's o and lse, short parts (whose row values come from
+    their keys where these are all there is) and longer ones."""
+    q, k, v, do = draw(2, 50, 70, 4, 2, 64, F32, 22)
+    o, lse = kda.attn_fwd(q, k, v, causal=False)
+    parts = [kda.attn_bwd(q, k[:, s].contiguous(), v[:, s].contiguous(), o, lse, do, causal=False)
+             for s in (slice(0, cut), slice(cut, 70))]
+    torch.cuda.synchronize()
+    grads, bounds = bwd_bounds(*[np64(x) for x in (q, k, v, do)], F32, 64 ** -0.5, causal=False, window=0)
+    # each part's terms are among the whole's: its error is within the whole's bound
+    check(parts[0]["dq"] + parts[1]["dq"], grads[0], 2 * bounds[0], "dq")
+    for i, n in ((1, "dk"), (2, "dv")):
+        check(torch.cat([p[n] for p in parts], 1), grads[i], bounds[i], n)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_attn_gradients_of_rows_with_few_keys_are_as_precise_as_others(dtype):
+    """dS nearly vanishes where a row sees two or three keys; its error is measured against the gradients,
+    not against the terms that cancel.  bf16: a rounding of dS and one of the result, each eps / 2 / sqrt(3)
+    in the mean square at most (uniform up to half a step of a value's binade), 0.82 eps / 2 together.  fp32:
+    a dozen roundings (the chains of q.k and dout.v, lse, the exponential, the sums)."""
+    most = 1.0 if dtype is BF16 else 12.0
+    for T, window in ((2, 0), (3, 0), (40, 2), (300, 3)):
+        q, k, v, do = draw(4, T, T, 8, 4, 64, dtype, 23 + T)
+        o, lse = kda.attn_fwd(q, k, v, window=window)
+        g = kda.attn_bwd(q, k, v, o, lse, do, window=window)
+        torch.cuda.synchronize()
+        grads, _ = bwd_bounds(*[np64(x) for x in (q, k, v, do)], dtype, 64 ** -0.5, causal=True, window=window)
+        for n, w in zip(("dq", "dk", "dv"), grads):
+            e = np.linalg.norm(np64(g[n]) - w) / np.linalg.norm(w)
+            assert e < most * torch.finfo(dtype).eps / 2, (T, window, n, e)
+
+
+def test_attn_one_key_has_no_gradient_of_its_score():
+    q, k, v, do = draw(3, 1, 1, 4, 2, 64, BF16, 24)
+    o, lse = kda.attn_fwd(q, k, v)
+    g = kda.attn_bwd(q, k, v, o, lse, do)
+    assert not g["dq"].any() and not g["dk"].any()
+
+
 def test_attn_smallest_scale():
     """Uniform rows: the gradients of v are means of dout, the others vanish."""
     q, k, v, do = draw(1, 70, 70, 2, 2, 64, BF16, 21)
