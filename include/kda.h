@@ -493,8 +493,8 @@ kda_status kda_attn_bwd(const void* q, const void* k, const void* v, const int* 
  * it.  Values are divided by the scale and rounded to nearest even; infinities
  * become +-448, NaN stays NaN.  Tokens whose page is missing (no entry, or past
  * max_pages) are dropped; pages without new tokens, and bytes past the last
- * token, are left as they were.  Two sequences of one call must not write the
- * same page (shared pages are for reading).
+ * token, are left as they were.  Among the pages that one call writes none may
+ * be named twice (shared pages are for reading).
  * Sizes as above, n_pages * HK <= 2^30; no buffer may overlap another.
  * Errors: KDA_ERR_DTYPE, KDA_ERR_SHAPE, KDA_ERR_NULL, KDA_ERR_ALIGN, KDA_ERR_HIP. */
 kda_status kda_cache_append(const void* k, const void* v, void* k_cache, void* v_cache,
@@ -508,6 +508,8 @@ kda_status kda_cache_append(const void* k, const void* v, void* k_cache, void* v
  * for more): query i stands at position p = cache_len[b] + i and sees the cached
  * tokens j <= p, and j > p - window if window > 0.  Tokens whose page is missing
  * are not seen.  Queries past new_len, and those that see nothing, get o = 0.
+ * A NaN code of v at a cached token that a query does not see may reach it from
+ * the same 64 tokens.
  *   q [B,Tq,H,D] (stride ldq), o [B,Tq,H,D] contiguous, dtype dt.
  *   workspace  kda_attn_step_workspace(B, Tq, H, HK, D, max_pages * page)
  *        bytes, 256-byte aligned: partial results where the cache is split
