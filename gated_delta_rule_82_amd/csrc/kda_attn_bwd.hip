@@ -184,7 +184,7 @@ __global__ __launch_bounds__(256, 2) void kda_attn_dkv_kernel(const AttnArgs a, 
     // unit come half a grid apart: the second half runs backwards, so that a long
     // tile's neighbour is a short one (fp32, 16 heads x 2048, D = 128: 337 us, without 413).
     const int nbh = a.B * a.HK, ntile = (a.Tk + BK - 1) / BK, half = (ntile + 1) / 2, at_tile = blockIdx.x / nbh;
-    const int bh = blockIdx.x % nbh, tile = NG < 4 || at_tile < half ? at_tile : ntile - 1 - (at_tile - half);
+    const int bh = head_of(a, blockIdx.x, nbh), tile = NG < 4 || at_tile < half ? at_tile : ntile - 1 - (at_tile - half);
     const int b = bh / a.HK, hk = bh % a.HK;
     const int ql = seq_len(a.q_len, b, a.Tq), kl = seq_len(a.kv_len, b, a.Tk), off = kl - ql;
     const int k0 = tile * BK, k1 = min(k0 + BK, kl);  // keys of the tile inside the length
@@ -372,7 +372,7 @@ __global__ __launch_bounds__(256, 1) void kda_attn_dq_kernel(const AttnArgs a, i
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
     const int nbh = a.B * a.HK, rows = a.Tq * a.G;
     const int ntile = (rows + BQ - 1) / BQ;
-    const int bh = blockIdx.x % nbh, tile = ntile - 1 - blockIdx.x / nbh;
+    const int bh = head_of(a, blockIdx.x, nbh), tile = ntile - 1 - blockIdx.x / nbh;
     const int b = bh / a.HK, hk = bh % a.HK;
     const int ql = seq_len(a.q_len, b, a.Tq), kl = seq_len(a.kv_len, b, a.Tk), off = kl - ql;
     const int r0 = tile * BQ, r1 = min(r0 + BQ, rows);

@@ -37,7 +37,7 @@ __global__ __launch_bounds__(512, 2) void kda_attn_dkv_turns_kernel(const AttnAr
     const int lane = threadIdx.x & 63, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % NW, late = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
     const int nbh = a.B * a.HK;    // early keys are seen by most queries: they come first
-    const int bh = blockIdx.x % nbh, tile = blockIdx.x / nbh;
+    const int bh = head_of(a, blockIdx.x, nbh), tile = blockIdx.x / nbh;
     const int b = bh / a.HK, hk = bh % a.HK;
     const int ql = seq_len(a.q_len, b, a.Tq), kl = seq_len(a.kv_len, b, a.Tk), off = kl - ql;
     const int k0 = tile * BK, k1 = min(k0 + BK, kl);  // keys of the tile inside the length
@@ -272,7 +272,7 @@ __global__ __launch_bounds__(512, 2) void kda_attn_dq_turns_kernel(const AttnArg
     const bool late = wave >= 4;
     const int nbh = a.B * a.HK, rows = a.Tq * a.G;
     const int ntile = (rows + BQ - 1) / BQ;
-    const int bh = blockIdx.x % nbh, tile = ntile - 1 - blockIdx.x / nbh;
+    const int bh = head_of(a, blockIdx.x, nbh), tile = ntile - 1 - blockIdx.x / nbh;
     const int b = bh / a.HK, hk = bh % a.HK;
     const int ql = seq_len(a.q_len, b, a.Tq), kl = seq_len(a.kv_len, b, a.Tk), off = kl - ql;
     const int r0 = tile * BQ, r1 = min(r0 + BQ, rows);

@@ -46,7 +46,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void kda_attn_fwd_kernel(
     const int nbh = a.B * a.HK, rows = a.Tq * a.G;
     const int ntile = (rows + BQ - 1) / BQ;
     int bid = blockIdx.x;
-    const int bh = bid % nbh;
+    const int bh = head_of(a, bid, nbh);
     bid /= nbh;
     const int split = bid % a.nsplit;
     const int tile = ntile - 1 - bid / a.nsplit;
@@ -238,7 +238,7 @@ __global__ __launch_bounds__(512, 2) void kda_attn_fwd_turns_kernel(const AttnAr
     const bool late = wave >= 4;   // the half that starts a turn later
     const int nbh = a.B * a.HK, rows = a.Tq * a.G;
     const int ntile = (rows + BQ - 1) / BQ;
-    const int bh = blockIdx.x % nbh, tile = ntile - 1 - blockIdx.x / nbh;
+    const int bh = head_of(a, blockIdx.x, nbh), tile = ntile - 1 - blockIdx.x / nbh;
     const int b = bh / a.HK, hk = bh % a.HK;
     const int ql = seq_len(a.q_len, b, a.Tq), kl = seq_len(a.kv_len, b, a.Tk), off = kl - ql;
     const int r0 = tile * BQ, r1 = min(r0 + BQ, rows);
