@@ -18,8 +18,8 @@
 // Bound by the matrix cores: bf16, D = 128, 4 x 16 heads (4 of keys) x 4096 causal 883 us,
 // of which the 7 products would take 846 at the rate of a large matrix product; row
 // values 30 us (134 MB, 4.5 TB/s), dk and dv 530, dq 355 (kda_attn_bwd_turns.hip).
-// fp32, D = 64, 2 x 4 heads (2) x 1024, window 256: 46 us for the three launches, a wave to
-// a SIMD with nothing beside it while it waits.
+// fp32, D = 64, 2 x 4 heads (2) x 1024, window 256: 45 us for the three launches, one or two
+// waves to a SIMD with little beside them while they wait.
 #include "kda_attn_device.h"
 
 namespace kda {
@@ -157,20 +157,23 @@ __device__ __forceinline__ void join_turns(float* lds, floatx4 (&x)[ND][N], int 
 
 // dk and dv of a tile of 16 NK NG keys.  Keys are the columns of S = Q K^T and
 // dP = dO V^T, so the probabilities are right operands of dV^T += dO^T P and
-// dK^T += Q^T dS as they stand.  The 4 waves are NG groups of keys times 4 / NG turns:
+// dK^T += Q^T dS as they stand.  The NW waves are NG groups of keys times NW / NG turns:
 // a wave keeps its keys' fragments of K and V and both accumulators in registers
-// and takes every (4 / NG)-th step of 32 queries from a two-deep LDS ring, head after
+// and takes every (NW / NG)-th step of 32 queries from a two-deep LDS ring, head after
 // head of those that share the keys; the turns are summed in LDS at the end, in order.
-template <typename T, int D, int NK, int NG, int RB>
-__global__ __launch_bounds__(256, 2) void kda_attn_dkv_kernel(const AttnArgs a, int padded) {
+// Eight waves (fp32) take steps of 16 queries: the ring, which leaves room for no second
+// workgroup, then feeds two waves on each SIMD.
+template <typename T, int D, int NK, int NG, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void kda_attn_dkv_kernel(const AttnArgs a, int padded) {
     typedef TileGeom<T, D> G_;
-    constexpr int NW = 4, NT = NW / NG, NS = G_::NS, ND = G_::ND, BK = 16 * NK * NG;
+    constexpr int NT = NW / NG, NS = G_::NS, ND = G_::ND, BK = 16 * NK * NG;
+    constexpr int NI = NW == 8 ? 1 : 2, SR = 16 * NI, RB = SR * NT;   // 16-row blocks and rows of a step, rows of a tile
     // contraction steps whose K and V fragments stay in registers; at D = 128 those of the
     // fourth live in LDS (1 KiB a fragment), or two waves would not fit a SIMD
     constexpr int VR = sizeof(T) == 2 && D == 128 ? 3 : NS, VL = NS - VR;
     constexpr int kTile = RB * D * (int)sizeof(T);
     constexpr bool kInit = sizeof(T) == 2;   // the row values are initial accumulators
-    static_assert(RB == 32 * NT && RB <= 128, "one step a wave and tile");
+    static_assert(RB <= 128 && (NI == 2 || sizeof(T) == 4), "row values of a tile fit one copy; half a step is an fp32 product");
     constexpr int kSum = NT > 1 ? (NT - 1) * NG * 16 * NK * D * 4 : 0;   // the other turns' sums
     constexpr int kRing = 4 * kTile;
     __shared__ __attribute__((aligned(16))) unsigned char sm[kRing > kSum ? kRing : kSum];
@@ -192,7 +195,9 @@ __global__ __launch_bounds__(256, 2) void kda_attn_dkv_kernel(const AttnArgs a, 
     int t_lo = 0, t_hi = k0 < k1 ? ql : 0;
     if (a.causal) t_lo = max(0, k0 - off);
     if (a.window) t_hi = min(t_hi, max(0, k1 - 1 + a.window - off));
-    const int beg = t_lo / RB, per = t_lo < t_hi ? (t_hi + RB - 1) / RB - beg : 0;  // tiles of a head
+    // tiles of a head start at the 32 queries where the first one is seen, and nothing past
+    // the last one is copied: small tiles of keys read 128 queries at a time
+    const int beg = t_lo & ~31, per = t_lo < t_hi ? (t_hi - beg + RB - 1) / RB : 0;
     const int steps = per * a.G;
 
     // the tokens [seen_from(key), seen_to(key)) that see a key (lengths and the
@@ -237,14 +242,13 @@ __global__ __launch_bounds__(256, 2) void kda_attn_dkv_kernel(const AttnArgs a, 
     const uint32_t lds0 = lds_address(&sm[0]), lds_rows = lds_address(&srow[0][0]);
     qst.init(wave, lane, [&](int x) { return (uint32_t)(x * a.ldq * sizeof(T)); });
     dst.init(wave, lane, [&](int x) { return (uint32_t)(x * ldo * sizeof(T)); });
-    auto stage = [&](int h, int tt, int buf) {
-        const int t0 = tt * RB;
-        const long long left = ql - 1 - t0;  // queries past the last one are past the windows and read as zeros
+    auto stage = [&](int h, int t0, int buf) {
+        const long long left = t_hi - 1 - t0;  // queries past the last one are past the windows and read as zeros
         qst.issue(buffer_window(qbase + t0 * a.ldq + (size_t)h * D, (left * (long long)a.ldq + D) * (long long)sizeof(T)),
                   lds0 + buf * 2 * kTile, wave);
         dst.issue(buffer_window(dobase + t0 * ldo + (size_t)h * D, (left * (long long)ldo + D) * (long long)sizeof(T)),
                   lds0 + (buf * 2 + 1) * kTile, wave);
-        // a step's 32 rows are within the padding; past it, and past the tile's rows, lanes read zeros past the
+        // a step's rows are within the padding; past it, and past the tile's rows, lanes read zeros past the
         // window, into rows of no step and the spare room
         if (wave == 0)
             copy_to_lds(buffer_window(rbase + 2 * ((size_t)h * padded + t0), min(RB, padded - t0) * 8), lane * 16, lds_rows + buf * 1024);
@@ -256,7 +260,7 @@ __global__ __launch_bounds__(256, 2) void kda_attn_dkv_kernel(const AttnArgs a, 
         // bf16: P and dS are rounded for their products, 2^-9 relative each
         Frag<T> pf[NK], sf[NK];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < NI; ++i) {
             if (VL > 0) asm volatile("" ::: "memory");  // the second half reads its fragments again instead of keeping them
             const floatx4* rp = reinterpret_cast<const floatx4*>(rows + 2 * (16 * i + 4 * g));
             floatx4 st[NK], dp[NK];
@@ -316,26 +320,26 @@ __global__ __launch_bounds__(256, 2) void kda_attn_dkv_kernel(const AttnArgs a, 
         }
 #pragma unroll
         for (int d = 0; d < ND; ++d) {
-            const Frag<T> dt = col_frag<D>(sm, ds, 0, d, at, lane);
-            const Frag<T> qt = col_frag<D>(sm, qs, 0, d, at, lane);
+            const Frag<T> dt = col_frag<D, 4 * NI>(sm, ds, 0, d, at, lane);
+            const Frag<T> qt = col_frag<D, 4 * NI>(sm, qs, 0, d, at, lane);
 #pragma unroll
             for (int n = 0; n < NK; ++n) {
-                dv[d][n] = mma(dt, pf[n], dv[d][n]);
-                dk[d][n] = mma(qt, sf[n], dk[d][n]);
+                dv[d][n] = mma_slots<4 * NI>(dt, pf[n], dv[d][n]);
+                dk[d][n] = mma_slots<4 * NI>(qt, sf[n], dk[d][n]);
             }
         }
     };
     int h = 0, tt = beg;
     if (steps > 0) stage(0, beg, 0);
     for (int it = 0; it < steps; ++it) {
-        const int buf = it & 1, t0 = tt * RB + 32 * turn;
-        if (++tt == beg + per) tt = beg, ++h;  // the next tile
+        const int buf = it & 1, t0 = tt + SR * turn;
+        if ((tt += RB) >= t_hi) tt = beg, ++h;  // the next tile
         wait_vmcnt<0>();
         lds_barrier();
         if (it + 1 < steps) stage(h, tt, buf ^ 1);
-        if (t0 >= any_hi || t0 + 32 <= any_lo) continue;
-        const uint32_t qs = buf * 2 * kTile + 32 * turn * D * (int)sizeof(T), ds = qs + kTile;
-        step(t0, qs, ds, &srow[buf][2 * 32 * turn], t0 < all_lo || t0 + 32 > all_hi);
+        if (t0 >= any_hi || t0 + SR <= any_lo) continue;
+        const uint32_t qs = buf * 2 * kTile + SR * turn * D * (int)sizeof(T), ds = qs + kTile;
+        step(t0, qs, ds, &srow[buf][2 * SR * turn], t0 < all_lo || t0 + SR > all_hi);
     }
 
     if constexpr (NT > 1) {
@@ -357,15 +361,18 @@ __global__ __launch_bounds__(256, 2) void kda_attn_dkv_kernel(const AttnArgs a, 
 }
 
 // dq of a tile of packed rows: the forward's loop with the rows' lse in hand,
-// S^T = K Q^T and dP^T = V dO^T, then dQ^T += K^T dS^T.  The 4 waves are NG groups of
-// rows times 4 / NG turns over the steps of 32 keys, summed in LDS at the end.
-template <typename T, int D, int NQ, int NG>
-__global__ __launch_bounds__(256, 1) void kda_attn_dq_kernel(const AttnArgs a, int padded) {
+// S^T = K Q^T and dP^T = V dO^T, then dQ^T += K^T dS^T.  The NW waves are NG groups of
+// rows times NW / NG turns over the steps of 32 keys (16 with eight waves), summed in LDS
+// at the end.
+template <typename T, int D, int NQ, int NG, int NW>
+__global__ __launch_bounds__(64 * NW, NW == 8 ? 2 : 1) void kda_attn_dq_kernel(const AttnArgs a, int padded) {
     typedef TileGeom<T, D> G_;
-    constexpr int NW = 4, NT = NW / NG, NS = G_::NS, ND = G_::ND, BQ = 16 * NQ * NG;
-    constexpr int KB = sizeof(T) == 2 && NT == 1 ? 64 : 32 * NT;
+    constexpr int NT = NW / NG, NS = G_::NS, ND = G_::ND, BQ = 16 * NQ * NG;
+    constexpr int NI = NW == 8 ? 1 : 2, SR = 16 * NI;   // 16-key blocks and keys of a step
+    static_assert(NI == 2 || sizeof(T) == 4, "half a step is an fp32 product");
+    constexpr int KB = sizeof(T) == 2 && NT == 1 ? 64 : SR * NT;
     constexpr int kTile = KB * D * (int)sizeof(T);
-    constexpr int kStep = 32 * D * (int)sizeof(T);
+    constexpr int kStep = SR * D * (int)sizeof(T);
     constexpr int kSum = (NT - 1) * NG * 16 * NQ * D * 4;   // the other turns' sums
     __shared__ __attribute__((aligned(16))) unsigned char sm[4 * kTile > kSum ? 4 * kTile : kSum];
 
@@ -377,7 +384,7 @@ __global__ __launch_bounds__(256, 1) void kda_attn_dq_kernel(const AttnArgs a, i
     const int ql = seq_len(a.q_len, b, a.Tq), kl = seq_len(a.kv_len, b, a.Tk), off = kl - ql;
     const int r0 = tile * BQ, r1 = min(r0 + BQ, rows);
     const RowRange blk = row_range(a, r0, r1, ql, kl);
-    const int k_beg = blk.key_lo / KB, k_end = blk.key_hi > blk.key_lo ? (blk.key_hi + KB - 1) / KB : k_beg;
+    const int k_beg = blk.key_lo & ~31, k_end = blk.key_hi > blk.key_lo ? blk.key_hi : k_beg;   // as the queries above
 
     const int rgrp = wave % NG, turn = wave / NG;
     const int w0 = r0 + rgrp * 16 * NQ;
@@ -416,27 +423,26 @@ __global__ __launch_bounds__(256, 1) void kda_attn_dq_kernel(const AttnArgs a, i
     kst.init(wave, lane, [&](int r) { return (uint32_t)(r * a.ldk * sizeof(T)); });
     vst.init(wave, lane, [&](int r) { return (uint32_t)(r * a.ldv * sizeof(T)); });
     const uint32_t lds0 = lds_address(&sm[0]);
-    auto stage = [&](int kt, int buf) {
-        const long long k0 = (long long)kt * KB, left = kl - 1 - k0;
+    auto stage = [&](long long k0, int buf) {
+        const long long left = k_end - 1 - k0;
         kst.issue(buffer_window(kbase + k0 * a.ldk, (left * (long long)a.ldk + D) * (long long)sizeof(T)), lds0 + buf * 2 * kTile, wave);
         vst.issue(buffer_window(vbase + k0 * a.ldv, (left * (long long)a.ldv + D) * (long long)sizeof(T)), lds0 + (buf * 2 + 1) * kTile, wave);
     };
     const TileLane<T, D> at(lane);
     if (k_beg < k_end) stage(k_beg, 0);
-    for (int kt = k_beg; kt < k_end; ++kt) {
-        const int buf = (kt - k_beg) & 1, k0 = kt * KB;
+    for (int k0 = k_beg, buf = 0; k0 < k_end; k0 += KB, buf ^= 1) {
         wait_vmcnt<0>();
         lds_barrier();
-        if (kt + 1 < k_end) stage(kt + 1, buf ^ 1);
+        if (k0 + KB < k_end) stage(k0 + KB, buf ^ 1);
         if (k0 >= mine.key_hi || k0 + KB <= mine.key_lo) continue;
         const uint32_t ks = buf * 2 * kTile, vs = ks + kTile;
         const bool masked = k0 < all_lo || k0 + KB > all_hi;
 #pragma unroll
-        for (int v = 0; v < KB / 32 / NT; ++v) {
+        for (int v = 0; v < KB / SR / NT; ++v) {
             const int u = v * NT + turn;
-            floatx4 st[2][NQ], dp[2][NQ];
+            floatx4 st[NI][NQ], dp[NI][NQ];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < NI; ++i) {
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) {
                     st[i][n] = floatx4{0.f, 0.f, 0.f, 0.f};
@@ -444,8 +450,8 @@ __global__ __launch_bounds__(256, 1) void kda_attn_dq_kernel(const AttnArgs a, i
                 }
 #pragma unroll
                 for (int s = 0; s < NS; ++s) {
-                    const Frag<T> kf = row_frag<D>(sm, ks + turn * kStep, 32 * v * NT + 16 * i, s, at, lane);
-                    const Frag<T> vf = row_frag<D>(sm, vs + turn * kStep, 32 * v * NT + 16 * i, s, at, lane);
+                    const Frag<T> kf = row_frag<D>(sm, ks + turn * kStep, SR * v * NT + 16 * i, s, at, lane);
+                    const Frag<T> vf = row_frag<D>(sm, vs + turn * kStep, SR * v * NT + 16 * i, s, at, lane);
 #pragma unroll
                     for (int n = 0; n < NQ; ++n) {
                         st[i][n] = mma(kf, qf[n][s], st[i][n]);
@@ -457,23 +463,23 @@ __global__ __launch_bounds__(256, 1) void kda_attn_dq_kernel(const AttnArgs a, i
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < NI; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         float p = probability<T>(a, st[i][n][e], ls[n]);
                         if (masked) {
-                            const int key = k0 + 32 * u + 16 * i + 4 * g + e;
+                            const int key = k0 + SR * u + 16 * i + 4 * g + e;
                             p = key >= lo[n] && key <= hi[n] ? p : 0.f;
                         }
                         dp[i][n][e] = p == 0.f ? 0.f : p * (dp[i][n][e] + de[n]);
                     }
-                sf[n] = frag_from_c<T>(dp[0][n], dp[1][n]);
+                sf[n] = frag_from_c<T>(dp[0][n], dp[NI - 1][n]);
             }
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
-                const Frag<T> kt_ = col_frag<D>(sm, ks + turn * kStep, 32 * v * NT, d, at, lane);
+                const Frag<T> kt_ = col_frag<D, 4 * NI>(sm, ks + turn * kStep, SR * v * NT, d, at, lane);
 #pragma unroll
-                for (int n = 0; n < NQ; ++n) dq[d][n] = mma(kt_, sf[n], dq[d][n]);
+                for (int n = 0; n < NQ; ++n) dq[d][n] = mma_slots<4 * NI>(kt_, sf[n], dq[d][n]);
             }
         }
     }
@@ -509,18 +515,25 @@ template <typename T, int D> constexpr int small_groups() { return D * (int)size
 // 1024: 32 us against 26).
 template <typename T, int D> constexpr int small_grid() { return D * (int)sizeof(T) <= 64 ? 512 : 256; }
 
-template <typename T, int D, int NG>
+// Waves of a small grid's workgroup.  fp32, eight against four: dk and dv, D = 128, 1 x 4
+// heads of 4 query heads x 512 156 us against 182, D = 64, 2 x 2 heads of 2 x 1024, window
+// 256, 22 against 25 (the smallest, 2 x 4 heads x 64, 7.7 against 7.2); dq, D = 128, 8 heads
+// x 1024 69 against 76, D = 64 29 against 30 and 4 x 8 heads x 256 15.4 against 14.1.
+template <typename T> constexpr int dkv_small_waves() { return sizeof(T) == 4 ? 8 : 4; }
+template <typename T, int D> constexpr int dq_small_waves() { return sizeof(T) == 4 && D == 128 ? 8 : 4; }
+
+template <typename T, int D, int NG, int NW>
 static hipError_t launch_dkv(const AttnArgs& a, int padded, hipStream_t s) {
     constexpr int NK = sizeof(T) == 2 ? 2 : 1, BK = 16 * NK * NG;
     const long long tiles = ((long long)a.Tk + BK - 1) / BK;
-    hipLaunchKernelGGL((kda_attn_dkv_kernel<T, D, NK, NG, 128 / NG>), dim3((unsigned)(tiles * a.B * a.HK)), dim3(256), 0, s, a, padded);
+    hipLaunchKernelGGL((kda_attn_dkv_kernel<T, D, NK, NG, NW>), dim3((unsigned)(tiles * a.B * a.HK)), dim3(64 * NW), 0, s, a, padded);
     return hipGetLastError();
 }
-template <typename T, int D, int NG>
+template <typename T, int D, int NG, int NW>
 static hipError_t launch_dq(const AttnArgs& a, int padded, hipStream_t s) {
     constexpr int NQ = sizeof(T) == 2 ? 2 : 1, BQ = 16 * NQ * NG;
     const long long rows = (long long)a.Tq * a.G, tiles = (rows + BQ - 1) / BQ;
-    hipLaunchKernelGGL((kda_attn_dq_kernel<T, D, NQ, NG>), dim3((unsigned)(tiles * a.B * a.HK)), dim3(256), 0, s, a, padded);
+    hipLaunchKernelGGL((kda_attn_dq_kernel<T, D, NQ, NG, NW>), dim3((unsigned)(tiles * a.B * a.HK)), dim3(64 * NW), 0, s, a, padded);
     return hipGetLastError();
 }
 
@@ -542,12 +555,12 @@ static hipError_t launch_bwd_t(const AttnArgs& a, hipStream_t s) {
     }
     if (a.Tk > 0) {
         const bool small = nbh * ((a.Tk + kWide - 1) / kWide) < small_grid<T, D>();
-        e = attn_dkv_turns(sizeof(T), D, a) ? launch_dkv_turns(a, padded, s) : small ? launch_dkv<T, D, kSmall>(a, padded, s) : launch_dkv<T, D, wide_groups<T, D>()>(a, padded, s);
+        e = attn_dkv_turns(sizeof(T), D, a) ? launch_dkv_turns(a, padded, s) : small ? launch_dkv<T, D, kSmall, dkv_small_waves<T>()>(a, padded, s) : launch_dkv<T, D, wide_groups<T, D>(), 4>(a, padded, s);
         if (e != hipSuccess) return e;
     }
     if (rows > 0) {
         const bool small = nbh * ((rows + kWide - 1) / kWide) < small_grid<T, D>();
-        e = attn_dq_turns(sizeof(T), D, a) ? launch_dq_turns(D, a, padded, s) : small ? launch_dq<T, D, kSmall>(a, padded, s) : launch_dq<T, D, wide_groups<T, D>()>(a, padded, s);
+        e = attn_dq_turns(sizeof(T), D, a) ? launch_dq_turns(D, a, padded, s) : small ? launch_dq<T, D, kSmall, dq_small_waves<T, D>()>(a, padded, s) : launch_dq<T, D, wide_groups<T, D>(), 4>(a, padded, s);
     }
     return e;
 }

@@ -212,8 +212,20 @@ __device__ __forceinline__ Frag<T> row_frag_global(const T* p, int s, int lane) 
     return f;
 }
 
-// Column fragment: column 16 c + l % 16 of the 32 rows from r0 of the tile.
-template <int D>
+// A product over the first N slots of each fragment (fp32: 4 of 8 are half a step).
+template <int N, typename T> __device__ __forceinline__ floatx4 mma_slots(const Frag<T>& a, const Frag<T>& b, floatx4 c) {
+    if constexpr (N == 8) {
+        return mma(a, b, c);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[j], b.v[j], c, 0, 0, 0);
+        return c;
+    }
+}
+
+// Column fragment: column 16 c + l % 16 of the 32 rows from r0 of the tile; with N = 4
+// (fp32) slots 0 .. 3 alone, the first 16 rows.
+template <int D, int N = 8>
 __device__ __forceinline__ Frag<bf16_t> col_frag(const unsigned char* sm, uint32_t tile, int r0, int c, const TileLane<bf16_t, D>& l,
                                                  int) {
     typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -227,13 +239,13 @@ __device__ __forceinline__ Frag<bf16_t> col_frag(const unsigned char* sm, uint32
     f.v = __builtin_bit_cast(bf16x8, s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
     return f;
 }
-template <int D>
+template <int D, int N = 8>
 __device__ __forceinline__ Frag<float> col_frag(const unsigned char* sm, uint32_t tile, int r0, int c, const TileLane<float, D>&,
                                                 int lane) {
     const int col = 16 * c + (lane & 15), g = lane >> 4;
     Frag<float> f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < N; ++j) {
         const int row = r0 + slot_index(g, j);
         f.v[j] = *reinterpret_cast<const float*>(sm + tile + row * (D * 4) +
                                                  (((col >> 2) ^ tile_swizzle<float, D>(row)) * 16) + (col & 3) * 4);
