@@ -14,7 +14,8 @@ namespace {
 
 constexpr int kWaves = 8;
 // Fragments are read this many ahead of their products: nobody else covers a wave's LDS
-// latency in its matrix turn.
+// latency in its matrix turn.  The first ones are read at the end of the vector turn,
+// which has time to spare.
 constexpr int kAhead = 6;
 
 }  // namespace
@@ -129,13 +130,20 @@ __global__ __launch_bounds__(512, 2) void kda_attn_dkv_turns_kernel(const AttnAr
         }
     };
     // One stream of fragments: with `grads` the columns of dO and Q at place p (products
-    // with P and dS), with `scores` the rows of Q and dO at place p1, beside V's own.
+    // with P and dS; the first kAhead are there), with `scores` the rows of Q and dO at
+    // place p1, beside V's own.
+    Frag<T> ring[kAhead];
+    auto column = [&](int p, int f) { return wide_col<D>(sm, p * 2 * kTile + (f % 2 ? 0 : kTile), 0, f / (2 * ND), f / 2 % ND, place); };
+    auto read_ahead = [&](int p) {
+#pragma unroll
+        for (int f = 0; f < kAhead; ++f) ring[f] = column(p, f);
+    };
     auto products = [&](auto grads, auto scores, int p, int p1) {
         constexpr int NG = decltype(grads)::value ? 4 * ND : 0, NF = NG + (decltype(scores)::value ? 3 * NS : 0);
-        const uint32_t qs = p * 2 * kTile, ds = qs + kTile, qs1 = p1 * 2 * kTile, ds1 = qs1 + kTile;
-        Frag<T> ring[kAhead], v;
+        const uint32_t qs1 = p1 * 2 * kTile, ds1 = qs1 + kTile;
+        Frag<T> v;
         auto fetch = [&](int f) {
-            if (f < NG) return wide_col<D>(sm, f % 2 ? qs : ds, 0, f / (2 * ND), f / 2 % ND, place);
+            if (f < NG) return column(p, f);
             const int s = (f - NG) / 3, kind = (f - NG) % 3;
             if (kind == 0) return wide_row<D>(sm, qs1, 0, s, place);
             if (kind == 2) return wide_row<D>(sm, ds1, 0, s, place);
@@ -143,9 +151,11 @@ __global__ __launch_bounds__(512, 2) void kda_attn_dkv_turns_kernel(const AttnAr
             frag_load(x, mine + s * 512, lane);
             return x;
         };
+        if (NG == 0) {
 #pragma unroll
-        for (int f = 0; f < kAhead && f < NF; ++f) ring[f] = fetch(f);
-        if (NG == 0) init_scores(p1);
+            for (int f = 0; f < kAhead; ++f) ring[f] = fetch(f);
+            init_scores(p1);
+        }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int f = 0; f < NF; ++f) {
@@ -186,6 +196,8 @@ __global__ __launch_bounds__(512, 2) void kda_attn_dkv_turns_kernel(const AttnAr
             pf[u] = frag_of(st, u);
             sf[u] = frag_of(dp, u);
         }
+        settle(pf);
+        settle(sf);
     };
 
     constexpr std::integral_constant<bool, true> yes{};
@@ -202,6 +214,7 @@ __global__ __launch_bounds__(512, 2) void kda_attn_dkv_turns_kernel(const AttnAr
         if (mine_n > 0) {
             products(no, yes, p, p);
             probabilities(tt * RB);
+            read_ahead(p);
         }
         if (late) lds_barrier();
         for (int it = 1; it < mine_n; ++it) {
@@ -213,6 +226,7 @@ __global__ __launch_bounds__(512, 2) void kda_attn_dkv_turns_kernel(const AttnAr
             p = after(p);
             advance(hh, tt, 2);
             probabilities(tt * RB);
+            read_ahead(p);
             lds_barrier();
             __builtin_amdgcn_s_setprio(1);
         }
@@ -323,19 +337,26 @@ __global__ __launch_bounds__(512, 2) void kda_attn_dq_turns_kernel(const AttnArg
     Frag<T> sf[NT][2];
 #pragma unroll
     for (int d = 0; d < ND; ++d) dq[d] = splat16(0.f);
-    // One stream of fragments: with `grads` the columns of K at place p, with `scores` the
-    // rows of K and V at place p1.
+    // One stream of fragments: with `grads` the columns of K at place p (the first kAhead are
+    // there), with `scores` the rows of K and V at place p1.
+    Frag<T> ring[kAhead];
+    auto column = [&](int p, int f) { return wide_col<D>(sm, p * 2 * kTile, 32 * (f / (2 * ND)), f / ND % 2, f % ND, place); };
+    auto read_ahead = [&](int p) {
+#pragma unroll
+        for (int f = 0; f < kAhead; ++f) ring[f] = column(p, f);
+    };
     auto products = [&](auto grads, auto scores, int p, int p1) {
         constexpr int NG = decltype(grads)::value ? 2 * NT * ND : 0, NF = NG + (decltype(scores)::value ? 2 * NT * NS : 0);
-        const uint32_t ks = p * 2 * kTile, ks1 = p1 * 2 * kTile, vs1 = ks1 + kTile;
-        Frag<T> ring[kAhead];
+        const uint32_t ks1 = p1 * 2 * kTile, vs1 = ks1 + kTile;
         auto fetch = [&](int f) {
-            if (f < NG) return wide_col<D>(sm, ks, 32 * (f / (2 * ND)), f / ND % 2, f % ND, place);
+            if (f < NG) return column(p, f);
             const int s = (f - NG) / (2 * NT), i = (f - NG) / 2 % NT;
             return wide_row<D>(sm, (f - NG) % 2 ? vs1 : ks1, 32 * i, s, place);
         };
+        if (NG == 0) {
 #pragma unroll
-        for (int f = 0; f < kAhead && f < NF; ++f) ring[f] = fetch(f);
+            for (int f = 0; f < kAhead; ++f) ring[f] = fetch(f);
+        }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int f = 0; f < NF; ++f) {
@@ -371,6 +392,7 @@ __global__ __launch_bounds__(512, 2) void kda_attn_dq_turns_kernel(const AttnArg
             for (int e = 0; e < 16; ++e) dp[i][e] = exp2_fast(fmaf(st[i][e], c, ls)) * (dp[i][e] + de);
             sf[i][0] = frag_of(dp[i], 0);
             sf[i][1] = frag_of(dp[i], 1);
+            settle(sf[i]);
         }
     };
 
@@ -385,6 +407,7 @@ __global__ __launch_bounds__(512, 2) void kda_attn_dq_turns_kernel(const AttnArg
         int p = 0;
         products(no, yes, 0, 0);
         probabilities(k_beg);
+        read_ahead(0);
         if (late) lds_barrier();
         for (int kt = k_beg + 1; kt < k_end; ++kt) {
             products(yes, yes, p, (p + 1) % kRing);
@@ -394,6 +417,7 @@ __global__ __launch_bounds__(512, 2) void kda_attn_dq_turns_kernel(const AttnArg
             load();
             p = (p + 1) % kRing;
             probabilities(kt);
+            read_ahead(p);
             lds_barrier();
             __builtin_amdgcn_s_setprio(1);
         }

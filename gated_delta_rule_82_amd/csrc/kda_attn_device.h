@@ -282,6 +282,13 @@ __device__ __forceinline__ Frag<bf16_t> frag_of(const floatx16& x, int u) {
     return f;
 }
 
+// Fragments whose computation ends here: without it the compiler moves their last
+// instructions past the barrier that follows, in front of the next turn's products.
+template <int N> __device__ __forceinline__ void settle(Frag<bf16_t> (&f)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(f[i].v));
+}
+
 // Maximum / sum over the two lanes that share a column.
 __device__ __forceinline__ float pair_max(float x) {
     const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
