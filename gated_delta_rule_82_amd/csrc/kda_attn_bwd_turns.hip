@@ -88,22 +88,37 @@ __global__ __launch_bounds__(512, 2) void kda_attn_dkv_turns_kernel(const AttnAr
     auto advance = [&](int& h, int& t, int by) {
         for (t += by; t >= beg + per && h < a.G; ++h) t -= per;
     };
+    // the next tile to copy
+    const uint32_t qrow = (uint32_t)(a.ldq * sizeof(T)), drow = (uint32_t)(ldo * sizeof(T));
+    const size_t qstep = 2 * RB * a.ldq, dstep = 2 * RB * ldo;
+    const T *qnext, *dnext;
+    const float* rnext;
     int next_h = 0, next_t = beg, next_place = ring0;
+    auto seek = [&]() {
+        qnext = qbase + (size_t)next_t * RB * a.ldq + (size_t)next_h * D;
+        dnext = dobase + (size_t)next_t * RB * ldo + (size_t)next_h * D;
+        rnext = rbase + 2 * ((size_t)next_h * padded + next_t * RB);
+    };
     advance(next_h, next_t, late);
+    seek();
     auto load = [&]() {
         if (next_h < a.G) {
-            const int t0 = next_t * RB;
-            const long long left = ql - 1 - t0;  // queries past the last one are past the windows and read as zeros
-            qst.issue(buffer_window(qbase + t0 * a.ldq + (size_t)next_h * D, (left * (long long)a.ldq + D) * (long long)sizeof(T)),
-                      lds0 + next_place * 2 * kTile, wave);
-            dst.issue(buffer_window(dobase + t0 * ldo + (size_t)next_h * D, (left * (long long)ldo + D) * (long long)sizeof(T)),
-                      lds0 + (next_place * 2 + 1) * kTile, wave);
+            const int n = min(ql - next_t * RB, RB);  // queries past the last one are past the windows and read as zeros
+            qst.issue(tile_window(qnext, n, qrow, D * sizeof(T)), lds0 + next_place * 2 * kTile, wave);
+            dst.issue(tile_window(dnext, n, drow, D * sizeof(T)), lds0 + (next_place * 2 + 1) * kTile, wave);
             // the row array is padded to whole tiles; lanes past a tile's rows read zeros past the window, into the spare room
-            if (wave == 0)
-                copy_to_lds(buffer_window(rbase + 2 * ((size_t)next_h * padded + t0), RB * 8), lane * 16, lds_rows + next_place * 1024);
+            if (wave == 0) copy_to_lds(tile_window(rnext, RB, 8, 8), lane * 16, lds_rows + next_place * 1024);
         }
         next_place = next_place == ring0 + kRing - 1 ? ring0 : next_place + 1;
-        advance(next_h, next_t, 2);
+        if (next_t + 2 < beg + per) {
+            next_t += 2;
+            qnext += qstep;
+            dnext += dstep;
+            rnext += 4 * RB;
+        } else {
+            advance(next_h, next_t, 2);
+            seek();
+        }
     };
 
     const WideLane<D> place(lane);
@@ -320,13 +335,19 @@ __global__ __launch_bounds__(512, 2) void kda_attn_dq_turns_kernel(const AttnArg
     kst.init(wave, lane, [&](int x) { return (uint32_t)(x * a.ldk * sizeof(T)); });
     vst.init(wave, lane, [&](int x) { return (uint32_t)(x * a.ldv * sizeof(T)); });
     const uint32_t lds0 = lds_address(&sm[0]);
+    // the next tile to copy
+    const uint32_t krow = (uint32_t)(a.ldk * sizeof(T)), vrow = (uint32_t)(a.ldv * sizeof(T));
+    const T* knext = kbase + (size_t)k_beg * KB * a.ldk;
+    const T* vnext = vbase + (size_t)k_beg * KB * a.ldv;
     int next = k_beg, next_place = 0;
     auto load = [&]() {
         if (next < k_end) {
-            const long long first = (long long)next * KB, left = kl - 1 - first;
-            kst.issue(buffer_window(kbase + first * a.ldk, (left * (long long)a.ldk + D) * (long long)sizeof(T)), lds0 + next_place * 2 * kTile, wave);
-            vst.issue(buffer_window(vbase + first * a.ldv, (left * (long long)a.ldv + D) * (long long)sizeof(T)), lds0 + (next_place * 2 + 1) * kTile, wave);
+            const int n = min(kl - next * KB, KB);
+            kst.issue(tile_window(knext, n, krow, D * sizeof(T)), lds0 + next_place * 2 * kTile, wave);
+            vst.issue(tile_window(vnext, n, vrow, D * sizeof(T)), lds0 + (next_place * 2 + 1) * kTile, wave);
         }
+        knext += KB * a.ldk;
+        vnext += KB * a.ldv;
         next_place = (next_place + 1) % kRing;
         ++next;
     };

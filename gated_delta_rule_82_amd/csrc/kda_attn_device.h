@@ -121,6 +121,16 @@ __device__ __forceinline__ u32x4 buffer_window(const void* p, long long bytes) {
                  (uint32_t)__builtin_amdgcn_readfirstlane(n), 0x00020000u};
 }
 
+// The first `rows` of a tile's rows, which lie `step` bytes apart and are `width` wide (the
+// tile spans less than 2^31 bytes; rows >= 1).  Loops that carry p and rows along leave
+// little for the scalar unit: 64-bit products and clamps of whole tensors took half of a
+// vector turn.
+__device__ __forceinline__ u32x4 tile_window(const void* p, int rows, uint32_t step, uint32_t width) {
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)a), (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(a >> 32)) & 0xffffu,
+                 (uint32_t)__builtin_amdgcn_readfirstlane((rows - 1) * step + width), 0x00020000u};
+}
+
 // 16 bytes a lane from window + off into LDS at lds + 16 * lane.  Written as
 // assembly because the compiler, seeing the copy, would wait for all copies in
 // flight (the next tile's) before the transposing reads of the current one.  It has

@@ -265,24 +265,20 @@ __global__ __launch_bounds__(512, 2) void kda_attn_fwd_turns_kernel(const AttnAr
     kst.init(wave, lane, [&](int r) { return (uint32_t)(r * a.ldk * sizeof(T)); });
     vst.init(wave, lane, [&](int r) { return (uint32_t)(r * a.ldv * sizeof(T)); });
     const uint32_t lds0 = lds_address(&sm[0]);
-    // windows of the next tiles to copy, and the ring places they go to
-    const long long kstep = (long long)KB * a.ldk, vstep = (long long)KB * a.ldv;
-    const T* knext = kbase + k_beg * kstep;
-    const T* vnext = vbase + k_beg * vstep;
-    long long kleft = ((kl - 1 - (long long)k_beg * KB) * (long long)a.ldk + D) * (long long)sizeof(T);
-    long long vleft = ((kl - 1 - (long long)k_beg * KB) * (long long)a.ldv + D) * (long long)sizeof(T);
+    // the next tiles to copy, and the ring places they go to
+    const uint32_t krow = (uint32_t)(a.ldk * sizeof(T)), vrow = (uint32_t)(a.ldv * sizeof(T));
+    const T* knext = kbase + (size_t)k_beg * KB * a.ldk;
+    const T* vnext = vbase + (size_t)k_beg * KB * a.ldv;
     int knum = k_beg, vnum = k_beg, kplace = 0, vplace = 0;
     auto load_k = [&]() {
-        if (knum < k_end) kst.issue(buffer_window(knext, kleft), lds0 + kplace * kTile, wave);
-        knext += kstep;
-        kleft -= kstep * (long long)sizeof(T);
+        if (knum < k_end) kst.issue(tile_window(knext, min(kl - knum * KB, KB), krow, D * sizeof(T)), lds0 + kplace * kTile, wave);
+        knext += KB * a.ldk;
         kplace = kplace == 2 ? 0 : kplace + 1;
         ++knum;
     };
     auto load_v = [&]() {
-        if (vnum < k_end) vst.issue(buffer_window(vnext, vleft), lds0 + (3 + vplace) * kTile, wave);
-        vnext += vstep;
-        vleft -= vstep * (long long)sizeof(T);
+        if (vnum < k_end) vst.issue(tile_window(vnext, min(kl - vnum * KB, KB), vrow, D * sizeof(T)), lds0 + (3 + vplace) * kTile, wave);
+        vnext += KB * a.ldv;
         vplace = vplace == 2 ? 0 : vplace + 1;
         ++vnum;
     };
@@ -375,6 +371,7 @@ __global__ __launch_bounds__(512, 2) void kda_attn_fwd_turns_kernel(const AttnAr
             }
             pf[i][0] = frag_of(st[i], 0);
             pf[i][1] = frag_of(st[i], 1);
+            settle(pf[i]);
         }
         l += (part[0] + part[1]) + (part[2] + part[3]);
     };
