@@ -71,30 +71,31 @@ hipError_t launch_attn_bwd(int dt, int D, const AttnArgs& a, hipStream_t s);
 // rows or 128 keys, has a compute unit to itself: they are taken where such workgroups
 // fill the card's 256 units and what a row or key sees is long enough to pay for the
 // slower start and, under a causal mask, for the whole tiles on the diagonal that both
-// halves walk.  Measured, this kernel against the plain one (16 heads of 128 channels):
-//   forward  4 x 4096 causal 262 / 272 us, 2 x 2048 causal 57 / 54; 2 x 2048 all keys 68 / 77,
-//            16 x 256 19 / 21; D = 64: 4 x 4096 causal 175 / 158
-//   dq       2 x 2048 causal 76 / 81, 4 x 1024 causal 50 / 47; 2 x 2048 all keys 91 / 111,
-//            16 x 256 24 / 25; D = 32: 4 x 4096 causal 167 / 157
-//   dk, dv   4 x 4096 causal 530 / 738, 2 x 2048 causal 86 / 103, 4 x 1024 causal 63 / 61;
-//            all keys 494 / 474 (8 x 2048, where nothing is left uneven), but 71 / 91 where
-//            the plain kernel has less than two workgroups a unit (1 x 2048); D = 64: 344 / 294
+// halves walk.  Measured, this kernel against the plain one (16 heads, D = 128 if not said):
+//   forward  4 x 4096 causal, 4 heads of keys, 255 / 267 us, 2 x 2048 causal 57 / 56, window
+//            2048 of 4096 125 / 115; 16 x 256 all keys 19 / 21; D = 64 4 x 4096 causal 175 / 158
+//   dq       4 x 1024 causal 43 / 47, 8 x 512 causal 30 / 29; 16 x 256 all keys 23 / 25; D = 64
+//            16 x 1024 causal, 4 heads of keys, 70 / 80, 2 x 2048 causal (256 workgroups, the
+//            longest decides) 48 / 39, 16 x 256 all keys 12 / 16; D = 32 4 x 4096 167 / 157
+//   dk, dv   4 x 4096 causal 488 / 735, 4 x 1024 causal 55 / 63, all keys 79 / 83; 8 x 512 43 / 39,
+//            64 x 256 with 4 heads of keys 73 / 61, window 1024 of 4096 160 / 151, 2048 216 / 245;
+//            D = 64 4 x 4096 causal 344 / 294
 constexpr int kTurnsGrid = 256, kTurnsRows = 256, kTurnsKeys = 128;
 inline long long turns_grid(const AttnArgs& a, long long n, int tile) { return (n + tile - 1) / tile * a.B * a.HK; }
-inline bool attn_row_turns(const AttnArgs& a, int causal_from) {
+inline bool attn_row_turns(const AttnArgs& a, int causal_from, int causal_grid) {
     const int keys = a.window > 0 && a.window < a.Tk ? a.window : a.Tk;
-    return turns_grid(a, (long long)a.Tq * a.G, kTurnsRows) >= kTurnsGrid && keys >= (a.causal ? causal_from : 512);
+    const long long grid = turns_grid(a, (long long)a.Tq * a.G, kTurnsRows);
+    return a.causal ? grid >= causal_grid && keys >= causal_from : grid >= kTurnsGrid && keys >= 256;
 }
 inline bool attn_fwd_turns(int elem_bytes, int D, const AttnArgs& a) {
-    return elem_bytes == 2 && D == 128 && a.nsplit == 1 && attn_row_turns(a, 4096);
+    return elem_bytes == 2 && D == 128 && a.nsplit == 1 && attn_row_turns(a, 4096, kTurnsGrid);
 }
 inline bool attn_dq_turns(int elem_bytes, int D, const AttnArgs& a) {
-    return elem_bytes == 2 && D >= 64 && attn_row_turns(a, 2048);
+    return elem_bytes == 2 && D >= 64 && attn_row_turns(a, 1024, D == 128 ? kTurnsGrid : 2 * kTurnsGrid);
 }
 inline bool attn_dkv_turns(int elem_bytes, int D, const AttnArgs& a) {
-    const long long grid = turns_grid(a, a.Tk, kTurnsKeys), seen = a.window > 0 && a.window < a.Tq ? a.window : a.Tq;
-    return elem_bytes == 2 && D == 128 && grid >= kTurnsGrid && seen * a.G >= 2048 &&
-           ((a.causal && a.window == 0) || grid < 2 * kTurnsGrid);
+    const long long seen = a.window > 0 && a.window / 2 < a.Tq ? a.window / 2 : a.Tq;
+    return elem_bytes == 2 && D == 128 && turns_grid(a, a.Tk, kTurnsKeys) >= kTurnsGrid && a.Tq >= 512 && seen * a.G >= 1024;
 }
 // Rows see so few keys that delta is summed over them (kda_attn_rows_few_kernel): no row
 // more than 32, or 16 in windows of a long axis, where the kernel's 16 rows read 31 keys.

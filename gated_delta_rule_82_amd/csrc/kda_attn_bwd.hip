@@ -15,9 +15,9 @@
 // once, would take 2.1 GB and 415 us for the first size below; the two products it
 // saves take 240).
 //
-// Bound by the matrix cores: bf16, D = 128, 4 x 16 heads (4 of keys) x 4096 causal 883 us,
-// of which the 7 products would take 846 at the rate of a large matrix product; row
-// values 30 us (134 MB, 4.5 TB/s), dk and dv 530, dq 355 (kda_attn_bwd_turns.hip).
+// Bound by the matrix cores: bf16, D = 128, 4 x 16 heads (4 of keys) x 4096 causal 846 us,
+// what the 7 products alone would take at the rate of a large matrix product: row values
+// 30 us (134 MB, 4.5 TB/s), dk and dv 500, dq 350 (kda_attn_bwd_turns.hip).
 // fp32, D = 64, 2 x 4 heads (2) x 1024, window 256: 45 us for the three launches, one or two
 // waves to a SIMD with little beside them while they wait.
 #include "kda_attn_device.h"

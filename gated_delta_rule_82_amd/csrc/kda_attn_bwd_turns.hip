@@ -5,7 +5,8 @@
 // Between two barriers one half forms products (the gradients of a tile and the scores
 // of the next) while the other half, on the vector unit, turns its scores into P and
 // dS; then they change over.  Copies are issued at the start of a vector turn and have
-// until the end of the next matrix turn.
+// until the end of the next matrix turn.  In dk and dv a turn takes 1470 cycles for 1024
+// of products; fewer cycles have stopped paying, the clock falls as they do.
 #include "kda_attn_device.h"
 
 namespace kda {

@@ -12,8 +12,8 @@
 //
 // Long rows are bound by the matrix cores beside the vector unit (an exponential, a
 // multiply-add, a maximum, a sum and half a rounding for every 4 D flops), few rows by
-// the keys and values read.  bf16, D = 128: 4 x 16 heads (4 of keys) x 4096 causal 259 us,
-// 1.06 PFLOP/s (a large matrix product reaches 1.14); 16 tokens of 32 heads behind
+// the keys and values read.  bf16, D = 128: 4 x 16 heads (4 of keys) x 4096 causal 255 us,
+// 1.08 PFLOP/s (a large matrix product reaches 1.14); 16 tokens of 32 heads behind
 // 65 536 keys of 8 62 us with the join, 4.3 TB/s.  fp32, D = 64, 2 x 4 heads x 1023 with
 // unequal lengths: 30 us, 42 TFLOP/s of 154 (workgroups that end early are not made up for).
 #include "kda_attn_device.h"
