@@ -30,9 +30,10 @@ bool attn_sizes_ok(int B, int Tq, int Tk, int H, int HK) {
     return Tk <= (1 << 29) && (unsigned long long)B * HK * ((unsigned long long)Tk / 32 + 1) < (1ull << 24);
 }
 
-// The backward has a thread for each 16 bytes of a row of o, rows padded.
+// The backward has a thread for each 16 bytes of a row of o, rows padded, and 128 more for
+// each head (two waves for its first rows).
 bool row_pieces_ok(int B, int Tq, int H, int D, kda_dtype dt) {
-    return (unsigned long long)B * H * ((unsigned long long)Tq + kda::kAttnRowPad) * (D * elem_bytes(dt) / 16) < (1ull << 32);
+    return (unsigned long long)B * H * (((unsigned long long)Tq + kda::kAttnRowPad) * (D * elem_bytes(dt) / 16) + 256) < (1ull << 32);
 }
 
 // A paged cache: its length only bounds a loop.

@@ -24,62 +24,24 @@
 
 namespace kda {
 
-// Row values of every query, padded per head to whole tiles with rows that
-// contribute nothing (-inf makes P zero): -lse / c in bf16, the initial accumulators of
-// the product that gives S - lse / c; in fp32 -lse, added after the product, where
-// S c - lse is rounded once and small (as initial accumulators they doubled the gradients'
-// error); and -delta.  Four queries' values of each
-// kind lie together: rows[b][h][t / 4][kind][t % 4].
-template <typename T, int D>
-__global__ __launch_bounds__(256) void kda_attn_rows_kernel(const AttnArgs a, int padded) {
-    constexpr int N = Gran16<T>::N, L = D / N;   // elements and lanes per row
-    const size_t at = ((size_t)blockIdx.x * 256 + threadIdx.x) / L;   // heads fastest, as the tensors lie
-    const int part = threadIdx.x % L;
-    const size_t n = (size_t)a.B * a.H * padded;
-    const bool inside = at < n;
-    const int h = (int)(at % a.H), t = (int)(at / a.H % padded), b = (int)(at / a.H / padded);
-    const bool live = inside && t < seq_len(a.q_len, inside ? b : 0, a.Tq);
-    float sum = 0.f, lse = kNegInf;
-    if (live) {
-        const size_t off = (((size_t)b * a.Tq + t) * a.H + h) * D + part * N;
-        const uint4 x = *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.o) + off);
-        const uint4 y = *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.dout) + off);
-#pragma unroll
-        for (int i = 0; i < N; ++i) sum = fmaf(Gran16<T>::get(x, i), Gran16<T>::get(y, i), sum);
-        lse = a.lse[((size_t)b * a.H + h) * a.Tq + t];
-    }
-#pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
-    if (inside && part == 0) {
-        const bool none = !live || lse == kNegInf;
-        float* to = a.rows + ((size_t)b * a.H + h) * padded * 2 + (t >> 2) * 8 + (t & 3);
-        to[0] = none ? kNegInf : sizeof(T) == 4 ? -lse : -lse / a.scale;
-        to[4] = none ? 0.f : -sum;
-    }
-}
-
 // P of a score q.k: in fp32 from -lse, in bf16 from -lse log2 e (see the row values).
 template <typename T> __device__ __forceinline__ float row_lse(float lse) { return sizeof(T) == 4 ? -lse : -lse * kLog2e; }
 template <typename T> __device__ __forceinline__ float probability(const AttnArgs& a, float score, float ls) {
     return sizeof(T) == 4 ? exp_carried(fmaf(score, a.scale, ls)) : exp2_fast(fmaf(score, a.scale_log2, ls));
 }
 
-// The same row values where rows see few keys: delta = sum_j P_ij dP_ij / sum_j P_ij, from
+// Row values where rows see few keys: delta = sum_j P_ij dP_ij / sum_j P_ij, from
 // the very dP that the gradients are formed with (same products in the same order) and
 // weights that add up to one.  dS is a difference that nearly vanishes there, and o's
 // rounding (in fp32 that of the other order) shows in it: gradients of bf16 rows of two to
 // five keys came out 1.3 to 2 times less precise, of fp32 ones up to eight times; in fp32
 // lse is corrected by the sum's logarithm for the same reason.  Where the sum is not one,
-// lse and o are those of more keys than these, and delta is dout.o as above.
-// 16 padded packed rows a wave, fragments straight from memory.
-template <typename T, int D>
-__global__ __launch_bounds__(256) void kda_attn_rows_few_kernel(const AttnArgs a, int padded) {
+// lse and o are those of more keys than these, and delta is dout.o.  Packed rows r0 .. r0 +
+// 15 by a wave, fragments straight from memory; wanted(t) says which are stored.
+template <typename T, int D, typename Wanted>
+__device__ __forceinline__ void rows_of_few_keys(const AttnArgs& a, int padded, int b, int hk, int r0, int lane, Wanted wanted) {
     constexpr int NS = TileGeom<T, D>::NS;
-    const int lane = threadIdx.x & 63, g = lane >> 4;
-    const size_t at = (size_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int nbh = a.B * a.HK, bh = (int)(at % nbh), b = bh / a.HK, hk = bh % a.HK;
-    if (at / nbh >= (size_t)padded * a.G / 16) return;
-    const int r0 = (int)(at / nbh) * 16, r = r0 + (lane & 15), t = (int)fdiv((uint32_t)r, a.divG), h = hk * a.G + (r - t * a.G);
+    const int g = lane >> 4, r = r0 + (lane & 15), t = (int)fdiv((uint32_t)r, a.divG), h = hk * a.G + (r - t * a.G);
     const int ql = seq_len(a.q_len, b, a.Tq), kl = seq_len(a.kv_len, b, a.Tk), off = kl - ql;
     const RowRange mine = row_range(a, r0, r0 + 16, ql, kl);
     const int hi = a.causal ? min(kl - 1, t + off) : kl - 1, lo = a.window ? t + off - a.window + 1 : 0;
@@ -120,13 +82,75 @@ __global__ __launch_bounds__(256) void kda_attn_rows_few_kernel(const AttnArgs a
     sum = group_add4(sum);
     delta = group_add4(delta);
     delta_o = group_add4(delta_o);
-    if (g == 0) {
+    if (g == 0 && wanted(t)) {
         const bool none = lse == kNegInf;
         const float d = sum - 1.f;
         const bool own = fabsf(d) < 1.f / 256;
         float* to = a.rows + ((size_t)b * a.H + h) * padded * 2 + (t >> 2) * 8 + (t & 3);
         to[0] = none ? kNegInf : sizeof(T) == 2 ? -lse / a.scale : own ? -(lse + (d - 0.5f * d * d)) : -lse;
         to[4] = none ? 0.f : own ? -delta / sum : -delta_o;
+    }
+}
+
+// All rows, where none sees more.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void kda_attn_rows_few_kernel(const AttnArgs a, int padded) {
+    const size_t at = (size_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int nbh = a.B * a.HK, bh = (int)(at % nbh);
+    if (at / nbh >= (size_t)padded * a.G / 16) return;
+    rows_of_few_keys<T, D>(a, padded, bh / a.HK, bh % a.HK, (int)(at / nbh) * 16, threadIdx.x & 63, [](int) { return true; });
+}
+
+// Row values of every query, padded per head to whole tiles with rows that
+// contribute nothing (-inf makes P zero): -lse / c in bf16, the initial accumulators of
+// the product that gives S - lse / c; in fp32 -lse, added after the product, where
+// S c - lse is rounded once and small (as initial accumulators they doubled the gradients'
+// error); and -delta.  Four queries' values of each kind lie together:
+// rows[b][h][t / 4][kind][t % 4].
+//
+// Under a causal mask the first rows of a sequence see few keys, and their gradients are
+// the largest: in bf16 the first `few` workgroups take the kFew tokens from the first that
+// sees a key on as above (without it dq of 90 to 900 tokens was 1.6 times as far off as
+// its rounding alone, with it 1.43, the square root of two: dS is rounded once more).
+// fp32 gains nothing and would pay 3 us of 45 (2 x 4 heads x 1024, window 256).
+constexpr int kFew = 32;
+template <typename T, int D>
+__global__ __launch_bounds__(256) void kda_attn_rows_kernel(const AttnArgs a, int padded, int few) {
+    auto sees_few = [&](int t, int off) { return sizeof(T) == 2 && a.causal && t + off >= 0 && t + off < kFew && t - max(-off, 0) < kFew; };
+    if (sizeof(T) == 2 && (int)blockIdx.x < few) {
+        const size_t at = (size_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int nbh = a.B * a.HK, bh = (int)(at % nbh), b = bh / a.HK, i = (int)(at / nbh);
+        const int ql = seq_len(a.q_len, b, a.Tq), off = seq_len(a.kv_len, b, a.Tk) - ql;
+        if (i >= kFew / 16 * a.G || off >= kFew) return;
+        rows_of_few_keys<T, D>(a, padded, b, bh % a.HK, max(-off, 0) * a.G + 16 * i, threadIdx.x & 63,
+                               [&](int t) { return t < padded && sees_few(t, off); });
+        return;
+    }
+    constexpr int N = Gran16<T>::N, L = D / N;   // elements and lanes per row
+    const size_t at = ((size_t)(blockIdx.x - few) * 256 + threadIdx.x) / L;   // heads fastest, as the tensors lie
+    const int part = threadIdx.x % L;
+    const size_t n = (size_t)a.B * a.H * padded;
+    const bool inside = at < n;
+    const int h = (int)(at % a.H), t = (int)(at / a.H % padded), b = (int)(at / a.H / padded);
+    const bool live = inside && t < seq_len(a.q_len, inside ? b : 0, a.Tq);
+    float sum = 0.f, lse = kNegInf;
+    if (live) {
+        const size_t off = (((size_t)b * a.Tq + t) * a.H + h) * D + part * N;
+        const uint4 x = *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.o) + off);
+        const uint4 y = *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.dout) + off);
+#pragma unroll
+        for (int i = 0; i < N; ++i) sum = fmaf(Gran16<T>::get(x, i), Gran16<T>::get(y, i), sum);
+        lse = a.lse[((size_t)b * a.H + h) * a.Tq + t];
+    }
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+    if (inside && part == 0) {
+        const int ql = seq_len(a.q_len, b, a.Tq);
+        if (sees_few(t, seq_len(a.kv_len, b, a.Tk) - ql)) return;
+        const bool none = !live || lse == kNegInf;
+        float* to = a.rows + ((size_t)b * a.H + h) * padded * 2 + (t >> 2) * 8 + (t & 3);
+        to[0] = none ? kNegInf : sizeof(T) == 4 ? -lse : -lse / a.scale;
+        to[4] = none ? 0.f : -sum;
     }
 }
 
@@ -549,7 +573,8 @@ static hipError_t launch_bwd_t(const AttnArgs& a, hipStream_t s) {
             hipLaunchKernelGGL((kda_attn_rows_few_kernel<T, D>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, s, a, padded);
         } else {
             const size_t threads = (size_t)a.B * a.H * padded * (D * sizeof(T) / 16);
-            hipLaunchKernelGGL((kda_attn_rows_kernel<T, D>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, a, padded);
+            const size_t few = sizeof(T) == 2 && a.causal ? ((size_t)nbh * (kFew / 16) * a.G + 3) / 4 : 0;
+            hipLaunchKernelGGL((kda_attn_rows_kernel<T, D>), dim3((unsigned)(few + (threads + 255) / 256)), dim3(256), 0, s, a, padded, (int)few);
         }
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }

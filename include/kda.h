@@ -382,7 +382,7 @@ kda_status kda_chunk_bwd_grouped(const void* q, const void* k, const void* v, co
  *
  * Sizes (KDA_ERR_SHAPE past them): Tk, max_pages * page and the rows G * Tq of
  * a key/value head up to 2^29; B * HK * (G * Tq / 32 + 1) and B * HK *
- * (Tk / 32 + 1) below 2^24; in the backward the 16-byte pieces of o, 64 tokens
+ * (Tk / 32 + 1) below 2^24; in the backward the 16-byte pieces of o, 200 tokens
  * a sequence on top, below 2^32; B * T * D of a rotation below 2^32; pages that
  * an append may touch, B * HK * (T / page + 2), below 2^24. */
 
