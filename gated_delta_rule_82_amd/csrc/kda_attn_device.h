@@ -57,7 +57,7 @@ __device__ __forceinline__ int seq_len(const int* len, int b, int most) {
 // head's tiles share an XCD's L2 where the heads are a multiple of 8.  Where sequences
 // have lengths of their own and fewer than 8 heads each, that would leave the XCDs of the
 // short ones idle: the head then moves on with every round of heads.  bf16, D = 128, 4 x 4
-// heads of 4 query heads, 4096, 3584, 3072 and 2560 tokens: forward 188 us against 223,
+// heads of 4 query heads, 4096 down to 2560 tokens: forward 188 us against 223,
 // backward 682 against 764, at the price of the L2 where all have 4096 (290 against 270);
 // with rows below 8192 a head (1024 tokens) 57 us against 54.
 __device__ __forceinline__ int head_of(const AttnArgs& a, int bid, int nbh) {
