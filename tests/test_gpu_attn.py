@@ -153,6 +153,7 @@ def run_heads(q, k, v, do, picks, ql, kl, what, **kw):
     (64, 2, 2100, 2100, 16, 16, dict(causal=True, window=0), [2100, 2050], [2100, 2060]),
     (64, 3, 2100, 2100, 12, 3, dict(causal=True, window=0), [1031, 2050, 2100], [1040, 2060, 2100]),
     (64, 2, 2100, 2100, 32, 8, dict(causal=True, window=1500), [2100, 1999], [2100, 2010]),
+    (128, 2, 2052, 2052, 16, 16, dict(causal=True, window=0), [2052, 2050], [2052, 2049]),
     (128, 4, 4100, 4099, 16, 4, dict(causal=True, window=0), [4100, 2000, 777, 3001], [4099, 2500, 777, 3000]),
 ])
 def test_attn_long_sequences_that_fill_the_card(D, B, Tq, Tk, H, HK, kw, ql, kl):
