@@ -44,6 +44,7 @@ struct AttnArgs {
     size_t ldq, ldk, ldv;       // elements between tokens
     float scale, scale_log2;    // scale, scale * log2 e
     int causal, window;         // window 0: none
+    int whole;                  // backward: the keys are all that o and lse were formed with
     int nsplit;
     FastDiv divG;
 };
@@ -99,9 +100,11 @@ inline bool attn_dkv_turns(int elem_bytes, int D, const AttnArgs& a) {
 }
 // Rows see so few keys that delta is summed over them (kda_attn_rows_few_kernel): no row
 // more than 32, or 16 in windows of a long axis, where the kernel's 16 rows read 31 keys.
+// Only where the call says that the keys are whole: a part of them that holds nearly all
+// of a row's mass looks the same from here, and its dS is what the others leave of it.
 // 64 x 16 heads x 64 of 128 channels, bf16: 22 us against 9 from o, with no gain in
 // precision left; 4 x 16 heads x 4096, window 64: 102 us against 26.
-inline bool attn_few_keys(const AttnArgs& a) { return a.Tk <= 32 || (a.causal && a.window > 0 && a.window <= 16); }
+inline bool attn_few_keys(const AttnArgs& a) { return a.whole && (a.Tk <= 32 || (a.causal && a.window > 0 && a.window <= 16)); }
 hipError_t launch_dkv_turns(const AttnArgs& a, int padded, hipStream_t s);
 hipError_t launch_dq_turns(int D, const AttnArgs& a, int padded, hipStream_t s);
 

@@ -237,6 +237,7 @@ kda_status kda_attn_bwd(const void* q, const void* k, const void* v, const int* 
     a.B = B; a.Tq = Tq; a.Tk = Tk; a.H = H; a.HK = HK; a.G = H / HK;
     a.scale = scale; a.scale_log2 = (float)(scale * kLog2eD);
     a.causal = causal ? 1 : 0; a.window = clamp_window(window, Tk);
+    a.whole = causal || window > 0;   // parts of the keys come without either
     a.divG = kda::fast_div((uint32_t)a.G);
     a.nsplit = 1;
     return kda::launch_attn_bwd(dt == KDA_BF16 ? 1 : 0, D, a, stream) == hipSuccess ? KDA_OK : KDA_ERR_HIP;

@@ -35,9 +35,13 @@ template <typename T> __device__ __forceinline__ float probability(const AttnArg
 // weights that add up to one.  dS is a difference that nearly vanishes there, and o's
 // rounding (in fp32 that of the other order) shows in it: gradients of bf16 rows of two to
 // five keys came out 1.3 to 2 times less precise, of fp32 ones up to eight times; in fp32
-// lse is corrected by the sum's logarithm for the same reason.  Where the sum is not one,
-// lse and o are those of more keys than these, and delta is dout.o.  Packed rows r0 .. r0 +
-// 15 by a wave, fragments straight from memory; wanted(t) says which are stored.
+// lse is corrected by the sum's logarithm for the same reason.  For calls whose keys are
+// whole (attn_few_keys, causal ones): the sum of a row does not tell, as a part with all
+// but 10^-4 of the mass would lose just the 10^-4 that its dS is made of.  There the sum is
+// one up to the rounding of scores about as large as lse (2^-24 of it, and as much for each
+// of a few steps; eight times that is allowed); where it is not, delta is dout.o.  Packed
+// rows r0 .. r0 + 15 by a wave, fragments straight from memory; wanted(t) says which are
+// stored.
 template <typename T, int D, typename Wanted>
 __device__ __forceinline__ void rows_of_few_keys(const AttnArgs& a, int padded, int b, int hk, int r0, int lane, Wanted wanted) {
     constexpr int NS = TileGeom<T, D>::NS;
@@ -85,7 +89,7 @@ __device__ __forceinline__ void rows_of_few_keys(const AttnArgs& a, int padded, 
     if (g == 0 && wanted(t)) {
         const bool none = lse == kNegInf;
         const float d = sum - 1.f;
-        const bool own = fabsf(d) < 1.f / 256;
+        const bool own = fabsf(d) < (8.f + fabsf(lse)) * 0x1p-20f;
         float* to = a.rows + ((size_t)b * a.H + h) * padded * 2 + (t >> 2) * 8 + (t & 3);
         to[0] = none ? kNegInf : sizeof(T) == 2 ? -lse / a.scale : own ? -(lse + (d - 0.5f * d * d)) : -lse;
         to[4] = none ? 0.f : own ? -delta / sum : -delta_o;

@@ -577,8 +577,10 @@ def attn_bwd_workspace_bytes(B, Tq, Tk, H, HK, D, dtype=torch.bfloat16) -> int:
 
 def attn_bwd(q, k, v, o, lse, dout, *, scale=None, causal=True, window=0, q_len=None, kv_len=None, workspace=None):
     """kda_attn_bwd: gradients of sum(dout * o) from the inputs and results of
-    attn_fwd (same scale, masks and lengths).  Returns a dict dq [B,Tq,H,D], dk,
-    dv [B,Tk,HK,D] in the input dtype."""
+    attn_fwd (same scale, masks and lengths).  With causal=False and window=0 k
+    and v may be a part of the keys that o and lse were formed with: its dk, dv
+    and share of dq.  Returns a dict dq [B,Tq,H,D], dk, dv [B,Tk,HK,D] in the
+    input dtype."""
     B, Tq, Tk, H, HK, D = _attn_shapes(q, k, v, q_len, kv_len)
     dev, dt = q.device, q.dtype
     _expect("o", o, (B, Tq, H, D), dt, dev)

@@ -459,9 +459,13 @@ kda_status kda_attn_fwd(const void* q, const void* k, const void* v, const int* 
  *   dv_j = sum_i P_ij dout_i,   dS_ij = P_ij (dout_i.v_j - dout_i.o_i),
  *   dq_i = scale sum_j dS_ij k_j,   dk_j = scale sum_i dS_ij q_i,
  * dk and dv summed over the G query heads of each key/value head.  No
- * atomics: results do not vary from run to run.  k and v may be a part of the
- * keys that o and lse were formed with (causal = 0, window = 0): dk and dv are
- * then that part's, and dq its share of the sum.
+ * atomics: results do not vary from run to run.  With causal = 0 and window = 0
+ * k and v may be a part of the keys that o and lse were formed with: dk and dv
+ * are then that part's, and dq its share of the sum.  With a causal mask or a
+ * window (of any length) they are all of them; dout_i.o_i is then formed from
+ * P and v instead of o for rows that see at most 32 keys (axes of 32 keys,
+ * windows of 16; in bf16 the first 32 queries under a causal mask), where the
+ * rounding of o would show in the gradients.
  *   o, dout, dq [B,Tq,H,D], dk, dv [B,Tk,HK,D]: contiguous, dtype dt.  Rows
  *   past the lengths, and rows that see or are seen by nothing, get 0; o, lse
  *   and dout are not read past q_len.  What is not finite inside the lengths

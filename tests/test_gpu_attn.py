@@ -203,6 +203,86 @@ def test_attn_gradients_of_rows_with_few_keys_are_as_precise_as_others(dtype):
             assert e < most * torch.finfo(dtype).eps / 2, (T, window, n, e)
 
 
+def peaked(n, rest, dtype, seed):
+    """70 keys whose first n hold all but about `rest` of every row's mass; the others' values are thirty
+    times as large, so that what they add to delta shows."""
+    g = torch.Generator().manual_seed(seed)
+    q, k, v, do = (torch.randn(2, t, h, 64, generator=g) for t, h in ((24, 4), (70, 2), (70, 2), (24, 4)))
+    q, k = 0.3 * q, 0.3 * k
+    q[..., 0], k[..., 0] = 8.0, 0.0
+    k[:, :n, :, 0] = float(np.log((70 - n) / (n * rest)))
+    v[:, n:] *= 30.0
+    return [x.to(dtype).cuda() for x in (q, k, v, do)]
+
+
+def part_terms(q, k, v, do, keys, scale, dtype):
+    """The gradients' terms of some of the keys in 64 bits, and the size of their error.  Sums of exact
+    products are off by a dozen fp32 roundings of the products' size in the mean square (their signs are
+    random), an exponential by as many of 1 + |score|; o, and with it delta, in bf16 by its own rounding and
+    that of the probabilities; dS and every result is rounded to the type once."""
+    r, u = 12 * 2.0 ** -24, torch.finfo(dtype).eps / 2
+    out = [[np.zeros(q.shape), np.zeros(k[:, keys].shape), np.zeros(k[:, keys].shape)] for _ in range(2)]
+    least, G = 1.0, q.shape[2] // k.shape[2]
+    for b in range(q.shape[0]):
+        for h in range(q.shape[2]):
+            qh, kh, vh, dh = q[b, :, h], k[b, :, h // G], v[b, :, h // G], do[b, :, h]
+            x = scale * qh @ kh.T
+            P = np.exp(x - x.max(1, keepdims=True))
+            P /= P.sum(1, keepdims=True)
+            dP = dh @ vh.T
+            delta = (P * dP).sum(1, keepdims=True)
+            e_delta = (r + (2 * u if dtype is BF16 else 0)) * np.linalg.norm(dh * (P @ np.abs(vh)), axis=1, keepdims=True)
+            P, dP, kh, vh = P[:, keys], dP[:, keys], kh[keys], vh[keys]
+            least = min(least, 1 - P.sum(1).max())
+            dS = P * (dP - delta)
+            rel = r * (1 + np.abs(x).max()) + (u if dtype is BF16 else 0)
+            e_dS = P * (e_delta + r * np.linalg.norm(dh[:, None] * vh, axis=2)) + rel * np.abs(dS)
+            for i, (to, w, y) in enumerate(((out[0], dS, None), (out[1], e_dS, np.abs))):
+                f = (lambda z: z) if y is None else y
+                to[0][b, :, h] = scale * w @ f(kh)
+                to[1][b, :, h // G] += scale * w.T @ f(qh)
+                to[2][b, :, h // G] += (P if i == 0 else rel * P).T @ f(dh)
+    return out[0], [e + u * np.abs(w) for w, e in zip(*out)], least
+
+
+@pytest.mark.parametrize("dtype,rest", [(F32, 3e-3), (F32, 1e-4), (F32, 1e-5), (F32, 1e-6), (BF16, 3e-3), (BF16, 1e-3)])
+@pytest.mark.parametrize("n", [1, 4, 32])
+def test_attn_bwd_over_a_part_with_nearly_all_of_the_mass(dtype, rest, n):
+    """A few keys that nearly every query attends to, in a call of their own: their gradients are what the
+    other keys leave of them, however little that is."""
+    q, k, v, do = peaked(n, rest, dtype, n)
+    o, lse = kda.attn_fwd(q, k, v, causal=False, scale=0.125)
+    for keys in (slice(0, n), slice(n, 70)):
+        g = kda.attn_bwd(q, k[:, keys].contiguous(), v[:, keys].contiguous(), o, lse, do, causal=False, scale=0.125)
+        torch.cuda.synchronize()
+        want, size, least = part_terms(*[np64(x) for x in (q, k, v, do)], keys, 0.125, dtype)
+        assert keys.start or 0 < least < 2 * rest
+        for name, w, e in zip(("dq", "dk", "dv"), want, size):
+            off = np.linalg.norm(np64(g[name]) - w)
+            assert off <= np.linalg.norm(e), (keys, name, off, np.linalg.norm(e), np.linalg.norm(w))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_attn_gradients_of_few_keys_that_a_window_calls_whole(dtype):
+    """A window, however long, says that the keys are all there: without a causal mask too rows of few keys
+    are then as precise as others (bounds as in the test of precision above)."""
+    most = 1.0 if dtype is BF16 else 12.0
+    for Tq, Tk, window in ((1, 1, 1), (7, 2, 40), (30, 3, 100), (60, 31, 2 ** 20)):
+        q, _, _, do = draw(4, Tq, Tq, 8, 4, 64, dtype, 31 + Tq)
+        _, k, v, _ = draw(4, Tk, Tk, 8, 4, 64, dtype, 32 + Tk)
+        kw = dict(causal=False, window=window)
+        o, lse = kda.attn_fwd(q, k, v, **kw)
+        g = kda.attn_bwd(q, k, v, o, lse, do, **kw)
+        torch.cuda.synchronize()
+        grads = ora.attn_backward(*[np64(x) for x in (q, k, v, do)], 64 ** -0.5, **kw)
+        for name, w in zip(("dq", "dk", "dv"), grads):
+            if Tk == 1 and name != "dv":
+                assert not g[name].any(), name
+                continue
+            e = np.linalg.norm(np64(g[name]) - w) / np.linalg.norm(w)
+            assert e < most * torch.finfo(dtype).eps / 2, (Tq, Tk, name, e)
+
+
 def test_attn_one_key_has_no_gradient_of_its_score():
     q, k, v, do = draw(3, 1, 1, 4, 2, 64, BF16, 24)
     o, lse = kda.attn_fwd(q, k, v)
