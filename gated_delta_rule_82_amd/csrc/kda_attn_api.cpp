@@ -313,7 +313,7 @@ kda_status kda_attn_step(const void* q, const void* k_cache, const void* v_cache
     a.q = q; a.k_cache = (const uint8_t*)k_cache; a.v_cache = (const uint8_t*)v_cache; a.k_scale = k_scale; a.v_scale = v_scale;
     a.block_table = block_table; a.cache_len = cache_len; a.new_len = new_len; a.o = o;
     a.n_pages = n_pages; a.max_pages = n_pages > 0 ? max_pages : 0; a.B = B; a.Tq = Tq; a.H = H; a.HK = HK; a.G = H / HK;
-    a.page = page; a.window = clamp_window(window, max_len);
+    a.page = page; a.window = window;   // as it is: a query may stand past the table's last token
     a.scale_log2 = (float)(scale * kLog2eD);
     a.divG = kda::fast_div((uint32_t)a.G);
     a.nsplit = kda::attn_step_splits(B, Tq, HK, a.G, max_len);

@@ -355,14 +355,17 @@ __global__ __launch_bounds__(64 * kStepWaves) void kda_attn_step_kernel(const At
     const int split = bid % a.nsplit, r0 = (bid / a.nsplit) * 16 * NR;
     const int b = bh / a.HK, hk = bh % a.HK;
     const int cap = a.max_pages * a.page;
-    const int ql = seq_len(a.new_len, b, a.Tq), before = min(max(a.cache_len[b], 0), (1 << 30) - 1);
-    // cached tokens: no more than the table has entries for
-    const int kl = min(before + ql, cap);
+    const int ql = seq_len(a.new_len, b, a.Tq);
+    // positions count from the length, which may lie past the table's end; cached tokens
+    // are no more than the table has entries for
+    const long long before = max(a.cache_len[b], 0);
+    const int kl = (int)min(before + ql, (long long)cap);
     const int r1 = min(r0 + 16 * NR, min(rows, ql * a.G));   // valid rows of the block
     int kb0 = 0, kb1 = 0;                                    // blocks of 64 keys
     if (r0 < r1) {
         const int t0 = (int)fdiv((uint32_t)r0, a.divG), t1 = (int)fdiv((uint32_t)(r1 - 1), a.divG);
-        const int hi = min(kl, before + t1 + 1), lo = a.window ? max(0, before + t0 - a.window + 1) : 0;
+        const int hi = (int)min((long long)kl, before + t1 + 1);
+        const int lo = a.window ? (int)min((long long)kl, max(0ll, before + t0 - a.window + 1)) : 0;
         if (lo < hi) {
             kb0 = lo / kStepKeys;
             kb1 = (hi + kStepKeys - 1) / kStepKeys;
@@ -378,8 +381,8 @@ __global__ __launch_bounds__(64 * kStepWaves) void kda_attn_step_kernel(const At
     for (int n = 0; n < NR; ++n) {
         const int r = min(r0 + 16 * n + lr, rows - 1);
         const int t = (int)fdiv((uint32_t)r, a.divG), h = hk * a.G + (r - t * a.G);
-        hi[n] = min(kl - 1, before + t);
-        lo[n] = a.window ? before + t - a.window + 1 : 0;
+        hi[n] = (int)min((long long)kl - 1, before + t);
+        lo[n] = a.window ? (int)min((long long)kl, before + t - a.window + 1) : 0;
         // rows past the newest token are computed on a valid row and dropped
         const int tr = max(min(t, ql - 1), 0);
         const T* qp = reinterpret_cast<const T*>(a.q) + ((size_t)b * a.Tq + tr) * a.ldq + (size_t)h * D;

@@ -377,8 +377,8 @@ kda_status kda_chunk_bwd_grouped(const void* q, const void* k, const void* v, co
  * projection [B,T,H+2HK,D].
  *
  * Lengths: device arrays of B ints, read when the kernels run; values outside
- * the tensor's range are clamped to it.  Nothing at or past a sequence's
- * length is read, whatever it holds.
+ * the tensor's range are clamped to it (cache_len: only negative ones, to 0).
+ * Nothing at or past a sequence's length is read, whatever it holds.
  *
  * Sizes (KDA_ERR_SHAPE past them): Tk, max_pages * page and the rows G * Tq of
  * a key/value head up to 2^29; B * HK * (G * Tq / 32 + 1) and B * HK *
@@ -510,7 +510,8 @@ kda_status kda_cache_append(const void* k, const void* v, void* k_cache, void* v
 /* Attention of the new_len[b] (NULL: Tq) newest tokens over that cache, after
  * their append (the decode step for Tq = 1; drafted tokens or a prompt's chunk
  * for more): query i stands at position p = cache_len[b] + i and sees the cached
- * tokens j <= p, and j > p - window if window > 0.  Tokens whose page is missing
+ * tokens j <= p, and j > p - window if window > 0, also where cache_len[b] lies
+ * past the max_pages * page tokens of the table.  Tokens whose page is missing
  * are not seen.  Queries past new_len, and those that see nothing, get o = 0.
  * A NaN code of v at a cached token that a query does not see may reach it from
  * the same 64 tokens.

@@ -206,6 +206,35 @@ def test_step_without_pages():
     check(o[:3], want[:3], 64 * 1e-5, "past the table")
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T", [1, 3])
+def test_step_window_past_the_end_of_the_table(dtype, T):
+    """Queries whose position lies past the table's last token: a window counts from there, also one as
+    long as the table or longer."""
+    page, mp, H, HK, D = 16, 6, 4, 2, 64
+    cap = page * mp
+    lens = [cap - 2, cap + 9, cap + 60, cap + 94, cap + 95, cap + 96, 2 * cap, (1 << 31) - 1]
+    table, n = tables(len(lens), mp, 21)
+    c = Pair(n, HK, D, page)
+    k, v = kv(len(lens), cap, HK, D, dtype, 4)
+    c.append(k, v, table, [0] * len(lens))
+    q = torch.randn(len(lens), T, H, D, generator=torch.Generator().manual_seed(7)).to(dtype).cuda()
+    kn, vn = ([x.tokens(table.cpu().numpy()[b], cap)[0] for b in range(len(lens))] for x in (c.K, c.V))
+    for window in (0, cap - 1, cap, cap + 1, cap + 64, 3 * cap, (1 << 31) - 1):
+        o = kda.attn_step(q, *c.dev, table, ints(lens), window=window)
+        torch.cuda.synchronize()
+        for b, first in enumerate(lens):
+            want = np.zeros((T, H, D))
+            bound = np.zeros((T, H, D))
+            for t in range(T):
+                lo = max(first + t - window + 1, 0) if window else 0
+                hi = min(first + t + 1, cap)
+                if lo < hi:  # one row over the keys it sees
+                    bo = fwd_bounds(np64(q[b:b + 1, t:t + 1]), kn[b][None, lo:hi], vn[b][None, lo:hi], dtype, D ** -0.5, False)
+                    want[t], bound[t] = bo[0][0, 0], bo[2][0, 0]
+            check(o[b], want, bound, f"window {window} at {first}")
+
+
 def test_shared_pages_are_read_by_several_sequences():
     page, D, HK = 32, 64, 2
     c = Pair(8, HK, D, page)
