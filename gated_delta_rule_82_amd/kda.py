@@ -427,6 +427,13 @@ def output_gate(o, gate, weight=None, *, y=None):
 
 ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 ROTARY_INTERLEAVED, ROTARY_INVERSE = 1, 2
+INT_MAX = 2 ** 31 - 1   # the C ABI's sizes and strides; ctypes would drop the bits above without a word
+
+
+def _int32(name, n):
+    if not -INT_MAX <= n <= INT_MAX:
+        raise ValueError(f"{name} = {n} does not fit in 32 bits")
+    return n
 
 
 def _launch(name, dev, *args):
@@ -463,6 +470,8 @@ def _rows(name, t):
     whose heads are packed and whose tokens lie one stride apart throughout."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
+    if t.numel() > INT_MAX and max(t.shape) > INT_MAX:
+        raise ValueError(f"{name} has {max(t.shape)} elements along an axis, more than 32 bits hold")
     if t.is_contiguous():
         return t.data_ptr(), 0
     B, T, H, D = t.shape
@@ -472,6 +481,8 @@ def _rows(name, t):
     ld = st if T > 1 else sb if B > 1 else H * D
     if ld < H * D or (T > 1 and B > 1 and sb != T * st):
         raise ValueError(f"the tokens of {name} must lie one stride apart")
+    if ld > INT_MAX:
+        raise ValueError(f"the tokens of {name} lie {ld} elements apart, more than 32 bits hold")
     return t.data_ptr(), ld
 
 
@@ -501,10 +512,11 @@ def rotary_freqs(rot, *, base=10000.0, scaling="none", factor=1.0, trained=0, be
                  device="cuda"):
     """kda_rotary_freqs: (inv_freq [rot/2] fp64 on `device`, scale) for `rotary`.
     scaling: "none", "linear", "ntk" or "yarn" (by parts; needs `trained`)."""
-    out = torch.empty(max(int(rot), 0) // 2, dtype=torch.float64)
+    rot, trained = _int32("rot", int(rot)), _int32("trained", trained)
+    out = torch.empty(max(rot, 0) // 2, dtype=torch.float64)
     scale = ctypes.c_float()
     _check("kda_rotary_freqs",
-           load().kda_rotary_freqs(out.data_ptr(), ctypes.addressof(scale), int(rot), base, ROTARY_SCALINGS[scaling], factor,
+           load().kda_rotary_freqs(out.data_ptr(), ctypes.addressof(scale), rot, base, ROTARY_SCALINGS[scaling], factor,
                                    trained, beta_fast, beta_slow))
     return out.to(device), scale.value
 
@@ -555,6 +567,7 @@ def attn_fwd(q, k, v, *, scale=None, causal=True, window=0, q_len=None, kv_len=N
     limits a query to that many keys; q_len, kv_len [B] int32 are the lengths of
     padded sequences.  Returns (o [B,Tq,H,D], lse [B,H,Tq] fp32)."""
     B, Tq, Tk, H, HK, D = _attn_shapes(q, k, v, q_len, kv_len)
+    _int32("window", window)
     dev, dt = q.device, q.dtype
     if o is None:
         o = _like(q)
@@ -582,6 +595,7 @@ def attn_bwd(q, k, v, o, lse, dout, *, scale=None, causal=True, window=0, q_len=
     and share of dq.  Returns a dict dq [B,Tq,H,D], dk, dv [B,Tk,HK,D] in the
     input dtype."""
     B, Tq, Tk, H, HK, D = _attn_shapes(q, k, v, q_len, kv_len)
+    _int32("window", window)
     dev, dt = q.device, q.dtype
     _expect("o", o, (B, Tq, H, D), dt, dev)
     _expect("lse", lse, (B, H, Tq), torch.float32, dev)
@@ -614,7 +628,7 @@ def _cache_shapes(k_cache, v_cache, k_scale, v_scale, block_table, cache_len, ne
     _expect("block_table", block_table, (B, block_table.shape[-1]), torch.int32, dev)
     _expect("cache_len", cache_len, (B,), torch.int32, dev)
     _expect("new_len", new_len, (B,), torch.int32, dev)
-    return n_pages, HK, page, block_table.shape[1]
+    return n_pages, HK, page, _int32("block_table's pages", block_table.shape[1])
 
 
 def cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cache_len, new_len=None):
@@ -646,6 +660,7 @@ def attn_step(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_len, new
     cache, after their cache_append (the same cache_len and new_len: query i of
     sequence b stands at position cache_len[b] + i).  Returns o [B,Tq,H,D]."""
     B, Tq, H, D = q.shape
+    _int32("window", window)
     dev, dt = q.device, q.dtype
     n_pages, HK, page, max_pages = _cache_shapes(k_cache, v_cache, k_scale, v_scale, block_table, cache_len, new_len,
                                                  B, D, dev)

@@ -7,6 +7,7 @@ import math
 
 import numpy as np
 import pytest
+import torch
 
 from gated_delta_rule_82_amd import kda
 from oracle import attn_oracle as ora
@@ -210,3 +211,63 @@ def test_workspace_sizes(lib):
     assert lib.kda_attn_step_workspace(1, 1, 8, 3, 128, 65536) == 0
     # two floats for each query, a head's padded to 64
     assert lib.kda_attn_bwd_workspace(2, 33, 50, 4, 2, 64, 1) == 2 * 4 * 64 * 8
+
+
+# ------------------------------------------------------------------ the binding's integers
+
+class OnDevice:
+    """What the binding asks of a device tensor; nothing lies behind it."""
+
+    is_cuda = True
+
+    def __init__(self, shape, stride):
+        self.shape, self._stride = shape, stride
+
+    def numel(self):
+        return math.prod(self.shape)
+
+    def stride(self):
+        return self._stride
+
+    def is_contiguous(self):
+        B, T, H, D = self.shape
+        return self._stride == (T * H * D, H * D, D, 1)
+
+    def data_ptr(self):
+        return addr(1)
+
+
+def test_strides_and_sizes_past_32_bits_are_refused():
+    """The last token of [B, 2^20, 32, 128] lies 2^32 elements from the next sequence's: 0 in 32 bits."""
+    for ld in (2 ** 32, 2 ** 32 + 4096, 2 ** 31, 2 ** 40):
+        with pytest.raises(ValueError, match="apart"):
+            kda._rows("q", OnDevice((4, 1, 32, 128), (ld, 4096, 128, 1)))
+        with pytest.raises(ValueError, match="apart"):
+            kda._rows("q", OnDevice((1, 4, 32, 128), (4 * ld, ld, 128, 1)))
+    assert kda._rows("q", OnDevice((4, 1, 32, 128), (2 ** 20, 4096, 128, 1))) == (addr(1), 2 ** 20)
+    for shape in ((1, 2 ** 32, 1, 16), (2 ** 32 + 2, 1, 1, 16), (1, 1, 2 ** 31, 16)):
+        B, T, H, D = shape
+        with pytest.raises(ValueError, match="q has"):
+            kda._rows("q", OnDevice(shape, (T * H * D, H * D, D, 1)))
+    meta = lambda *n, dtype=torch.int32: torch.empty(n, dtype=dtype, device="meta")  # noqa: E731
+    kc, ks = meta(2, 1, 16, 16, dtype=torch.uint8), meta(2, 1, dtype=torch.float32)
+    with pytest.raises(ValueError, match="block_table"):
+        kda._cache_shapes(kc, kc, ks, ks, meta(1, 2 ** 32), meta(1), None, 1, 16, kc.device)
+    assert kda._cache_shapes(kc, kc, ks, ks, meta(1, 8), meta(1), None, 1, 16, kc.device) == (2, 1, 16, 8)
+
+
+def test_windows_past_32_bits_are_refused():
+    """2^32 would arrive as no window at all."""
+    x = torch.empty(1, 2, 2, 32, dtype=torch.bfloat16, device="meta")
+    lse, n = torch.empty(1, 2, 2, device="meta"), torch.empty(1, dtype=torch.int32, device="meta")
+    kc, vc, ks = (torch.empty(s, dtype=t, device="meta") for s, t in
+                  (((2, 2, 16, 32), torch.uint8), ((2, 2, 32, 16), torch.uint8), ((2, 2), torch.float32)))
+    table = torch.empty(1, 2, dtype=torch.int32, device="meta")
+    for window in (2 ** 31, 2 ** 32, 2 ** 32 + 5, -2 ** 32):
+        for call_ in (lambda: kda.attn_fwd(x, x, x, window=window), lambda: kda.attn_bwd(x, x, x, x, lse, x, window=window),
+                      lambda: kda.attn_step(x, kc, vc, ks, ks, table, n, window=window)):
+            with pytest.raises(ValueError, match="window"):
+                call_()
+    for kw in (dict(rot=2 ** 32 + 16), dict(rot=16, scaling="yarn", factor=2.0, trained=2 ** 32 + 64)):
+        with pytest.raises(ValueError, match="32 bits"):
+            kda.rotary_freqs(device="cpu", **kw)
