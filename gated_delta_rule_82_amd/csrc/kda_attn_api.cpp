@@ -1,6 +1,7 @@
 // kda_attn_api.cpp - the C ABI of the softmax-attention operators: host
 // validation, sizing and dispatch.  As in kda_api.cpp, every argument is checked
 // before anything is enqueued and a rejected call makes no HIP call.
+#include <limits.h>
 #include <math.h>
 
 #include "kda_attn.h"
@@ -41,11 +42,14 @@ bool step_sizes_ok(int B, int Tq, int H, int HK, int max_len) {
     return max_len >= 0 && max_len <= (1 << 29) && rows_ok(B, Tq, H, HK);
 }
 
-// Row stride in elements: 0 selects contiguous tokens.
-kda_status stride(int ld, int heads, int D, kda_dtype dt, size_t* out) {
+// Most elements between rows that are copied as tiles, which are addressed with 32-bit
+// offsets: 64 rows of 4-byte elements stay below 2^31 bytes.
+constexpr int kTileStride = 1 << 23;
+
+// Row stride in elements, at most `most`: 0 selects contiguous tokens.
+kda_status stride(int ld, int most, int heads, int D, kda_dtype dt, size_t* out) {
     const long long least = (long long)heads * D;
-    // 64 rows of 4-byte elements stay below 2^31 bytes (tiles are addressed with 32-bit offsets)
-    if (ld < 0 || (ld > 0 && ld < least) || ld > (1 << 23) || least > (1 << 23)) return KDA_ERR_SHAPE;
+    if (ld < 0 || (ld > 0 && ld < least) || ld > most || least > kTileStride) return KDA_ERR_SHAPE;
     *out = ld ? (size_t)ld : (size_t)least;
     return (*out * elem_bytes(dt)) % 16 == 0 ? KDA_OK : KDA_ERR_ALIGN;
 }
@@ -137,8 +141,8 @@ kda_status kda_rotary(const void* q, const void* k, void* q_out, void* k_out, co
         return KDA_ERR_SHAPE;
     if (!isfinite(scale)) return KDA_ERR_SCALE;
     kda::RotaryArgs a{};
-    KDA_TRY(stride(ldq, H, D, dt, &a.ldq)); KDA_TRY(stride(ldqo, H, D, dt, &a.ldqo));
-    if (HK) { KDA_TRY(stride(ldk, HK, D, dt, &a.ldk)); KDA_TRY(stride(ldko, HK, D, dt, &a.ldko)); }
+    KDA_TRY(stride(ldq, INT_MAX, H, D, dt, &a.ldq)); KDA_TRY(stride(ldqo, INT_MAX, H, D, dt, &a.ldqo));
+    if (HK) { KDA_TRY(stride(ldk, INT_MAX, HK, D, dt, &a.ldk)); KDA_TRY(stride(ldko, INT_MAX, HK, D, dt, &a.ldko)); }
     a.tokens = (size_t)B * T;
     if (a.tokens == 0 || H + HK == 0) return KDA_OK;
     // a grid holds less than 2^32 threads: at most one for each channel of a token
@@ -175,7 +179,8 @@ kda_status kda_attn_fwd(const void* q, const void* k, const void* v, const int* 
     if (!dim_ok(D) || !attn_sizes_ok(B, Tq, Tk, H, HK) || window < 0) return KDA_ERR_SHAPE;
     if (!scale_ok(scale)) return KDA_ERR_SCALE;
     kda::AttnArgs a{};
-    KDA_TRY(stride(ldq, H, D, dt, &a.ldq)); KDA_TRY(stride(ldk, HK, D, dt, &a.ldk)); KDA_TRY(stride(ldv, HK, D, dt, &a.ldv));
+    KDA_TRY(stride(ldq, INT_MAX, H, D, dt, &a.ldq)); KDA_TRY(stride(ldk, kTileStride, HK, D, dt, &a.ldk));
+    KDA_TRY(stride(ldv, kTileStride, HK, D, dt, &a.ldv));
     if (B == 0 || H == 0 || Tq == 0) return KDA_OK;
     KDA_TRY(need(q)); KDA_TRY(need(o)); KDA_TRY(maybe(lse)); KDA_TRY(maybe(q_len)); KDA_TRY(maybe(kv_len));
     if (Tk > 0) { KDA_TRY(need(k)); KDA_TRY(need(v)); }
@@ -216,7 +221,8 @@ kda_status kda_attn_bwd(const void* q, const void* k, const void* v, const int* 
         return KDA_ERR_SHAPE;
     if (!scale_ok(scale)) return KDA_ERR_SCALE;
     kda::AttnArgs a{};
-    KDA_TRY(stride(ldq, H, D, dt, &a.ldq)); KDA_TRY(stride(ldk, HK, D, dt, &a.ldk)); KDA_TRY(stride(ldv, HK, D, dt, &a.ldv));
+    KDA_TRY(stride(ldq, kTileStride, H, D, dt, &a.ldq)); KDA_TRY(stride(ldk, kTileStride, HK, D, dt, &a.ldk));
+    KDA_TRY(stride(ldv, kTileStride, HK, D, dt, &a.ldv));
     if (B == 0 || H == 0 || (Tq == 0 && Tk == 0)) return KDA_OK;
     if (Tq > 0) { KDA_TRY(need(q)); KDA_TRY(need(o)); KDA_TRY(need(lse)); KDA_TRY(need(dout)); KDA_TRY(need(dq)); }
     if (Tk > 0) { KDA_TRY(need(k)); KDA_TRY(need(v)); KDA_TRY(need(dk)); KDA_TRY(need(dv)); }
@@ -259,7 +265,7 @@ kda_status kda_cache_append(const void* k, const void* v, void* k_cache, void* v
     if (!dtype_ok(dt)) return KDA_ERR_DTYPE;
     if (HK < 0 || !cache_sizes_ok(n_pages, max_pages, B, T, HK, D, page)) return KDA_ERR_SHAPE;
     kda::AppendArgs a{};
-    KDA_TRY(stride(ldk, HK, D, dt, &a.ldk)); KDA_TRY(stride(ldv, HK, D, dt, &a.ldv));
+    KDA_TRY(stride(ldk, INT_MAX, HK, D, dt, &a.ldk)); KDA_TRY(stride(ldv, INT_MAX, HK, D, dt, &a.ldv));
     if (B == 0 || T == 0 || HK == 0 || n_pages == 0 || max_pages == 0) return KDA_OK;
     // one workgroup of 256 threads for each page a sequence can touch
     if ((unsigned long long)B * HK * ((unsigned long long)T / page + 2) >= (1ull << 24)) return KDA_ERR_SHAPE;
@@ -295,7 +301,7 @@ kda_status kda_attn_step(const void* q, const void* k_cache, const void* v_cache
     if (!step_sizes_ok(B, Tq, H, HK, max_len)) return KDA_ERR_SHAPE;
     if (!scale_ok(scale)) return KDA_ERR_SCALE;
     kda::AttnStepArgs a{};
-    KDA_TRY(stride(ldq, H, D, dt, &a.ldq));
+    KDA_TRY(stride(ldq, INT_MAX, H, D, dt, &a.ldq));
     if (B == 0 || H == 0 || Tq == 0) return KDA_OK;
     KDA_TRY(need(q)); KDA_TRY(need(o)); KDA_TRY(need(cache_len)); KDA_TRY(maybe(new_len));
     if (n_pages > 0 && max_pages > 0) {

@@ -372,9 +372,10 @@ kda_status kda_chunk_bwd_grouped(const void* q, const void* k, const void* v, co
  *
  * Row strides: ld* is the distance between consecutive tokens of a tensor in
  * elements (0 selects heads * D, a contiguous tensor; otherwise at least that
- * and a multiple of 16 bytes, and at most 2^23 elements); sequences are T * ld
- * apart and heads D apart, so q, k and v may be the parts of one packed
- * projection [B,T,H+2HK,D].
+ * and a multiple of 16 bytes; at most 2^23 elements for k and v of kda_attn_fwd
+ * and for q, k and v of kda_attn_bwd); sequences are T * ld apart and heads D
+ * apart, so q, k and v may be the parts of one packed projection [B,T,H+2HK,D],
+ * or, with T = 1, of the last token of a longer one.
  *
  * Lengths: device arrays of B ints, read when the kernels run; values outside
  * the tensor's range are clamped to it (cache_len: only negative ones, to 0).

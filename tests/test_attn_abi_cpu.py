@@ -271,3 +271,20 @@ def test_windows_past_32_bits_are_refused():
     for kw in (dict(rot=2 ** 32 + 16), dict(rot=16, scaling="yarn", factor=2.0, trained=2 ** 32 + 64)):
         with pytest.raises(ValueError, match="32 bits"):
             kda.rotary_freqs(device="cpu", **kw)
+
+
+def test_strides_of_tiles_are_bounded(lib):
+    """Rows that are copied as tiles are addressed with 32-bit offsets: 2^23 elements between them at most."""
+    far = 2 ** 23 + 8
+    for n in ("ldk", "ldv"):
+        assert call(lib.kda_attn_fwd, ATTN, **{n: far}) == SHAPE
+    for n in ("ldq", "ldk", "ldv"):
+        assert call(lib.kda_attn_bwd, BWD, **{n: far}) == SHAPE
+    # elsewhere any multiple of 16 bytes passes the check (the next one refuses these calls)
+    assert call(lib.kda_attn_fwd, ATTN, ldq=far, o=None) == NULL
+    assert call(lib.kda_attn_step, STEP, ldq=far, o=None) == NULL
+    for n in ("ldk", "ldv"):
+        assert call(lib.kda_cache_append, APPEND, **{n: far}, kc=None) == NULL
+    for n in ("ldq", "ldk", "ldqo", "ldko"):
+        assert call(lib.kda_rotary, ROTARY, **{n: 2 ** 31 - 8}, freq=None) == NULL
+        assert call(lib.kda_rotary, ROTARY, **{n: 2 ** 31 - 1}, freq=None) == ALIGN

@@ -284,6 +284,36 @@ def test_cache_captured_and_replayed():
         lens += 1
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T", [4096, 262144])
+def test_last_token_of_a_packed_prompt(dtype, T):
+    """The first decode step takes the last token where the prompt's projection holds it: sequences lie
+    25 million and 1.6 billion elements apart.  The same calls on contiguous copies give the same bits."""
+    B, H, HK, D, page, mp = 2, 40, 4, 128, 16, 80
+    x = torch.empty(B, T, H + 2 * HK, D, dtype=dtype, device="cuda")
+    x[:, -1:] = torch.randn(B, 1, H + 2 * HK, D, generator=torch.Generator().manual_seed(5)).to(dtype)
+    parts = lambda y: (y[:, -1:, :H], y[:, -1:, H:H + HK], y[:, -1:, H + HK:])  # noqa: E731
+    f, s = kda.rotary_freqs(64, scaling="yarn", factor=4.0, trained=64)
+    pos = torch.full((B, 1), 1000, dtype=torch.int32, device="cuda")
+    table, n = tables(B, mp, 11)
+    k0, v0 = kv(B, 1200, HK, D, dtype, 1)
+
+    def step(q, k, v, in_place):
+        dev = kda.new_cache(n, HK, D, page)
+        kda.cache_append(k0, v0, *dev, table, ints([0, 0]))
+        q, k = kda.rotary(q, k, f, pos, scale=s, **(dict(q_out=q, k_out=k) if in_place else {}))
+        kda.cache_append(k, v, *dev, table, ints([1200, 17]))
+        o = kda.attn_step(q, *dev, table, ints([1200, 17]))
+        o2, lse2 = kda.attn_fwd(q, k0, v0)
+        torch.cuda.synchronize()
+        return q.clone(), k.clone(), o, o2, lse2
+
+    want = step(*(y.contiguous() for y in parts(x)), False)
+    for in_place in (False, True):
+        for got, w in zip(step(*parts(x), in_place), want):
+            assert torch.equal(got, w)
+
+
 def test_training_chain():
     """Rotary, attention and both backward passes over a packed projection, as a layer runs them, in fp32:
     the oracle's chain in 64 bits; the rotation adds 12 * 2^-24 of a pair to q, k and to the gradients, well
