@@ -499,8 +499,13 @@ def _attn_shapes(q, k, v, q_len, kv_len):
 
 
 def _workspace(need, given, dev):
-    if given is not None and given.numel() * given.element_size() >= need:
-        return given
+    """The caller's workspace where it has `need` bytes, else (as for the chunkwise calls) one
+    allocated for this call; None where none is needed.  One on another device is refused."""
+    if given is not None:
+        if given.device != dev:
+            raise ValueError(f"workspace is on {given.device}, expected {dev}")
+        if given.numel() * given.element_size() >= need:
+            return given
     return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
 
 
@@ -565,7 +570,8 @@ def attn_fwd(q, k, v, *, scale=None, causal=True, window=0, q_len=None, kv_len=N
     (H a multiple of HK; each may be part of a packed tensor).  scale None is
     1/sqrt(D).  causal aligns the last query with the last key; window > 0
     limits a query to that many keys; q_len, kv_len [B] int32 are the lengths of
-    padded sequences.  Returns (o [B,Tq,H,D], lse [B,H,Tq] fp32)."""
+    padded sequences.  A workspace of less than attn_fwd_workspace_bytes is not
+    used.  Returns (o [B,Tq,H,D], lse [B,H,Tq] fp32)."""
     B, Tq, Tk, H, HK, D = _attn_shapes(q, k, v, q_len, kv_len)
     _int32("window", window)
     dev, dt = q.device, q.dtype

@@ -288,3 +288,17 @@ def test_strides_of_tiles_are_bounded(lib):
     for n in ("ldq", "ldk", "ldqo", "ldko"):
         assert call(lib.kda_rotary, ROTARY, **{n: 2 ** 31 - 8}, freq=None) == NULL
         assert call(lib.kda_rotary, ROTARY, **{n: 2 ** 31 - 1}, freq=None) == ALIGN
+
+
+def test_workspaces_of_another_device_are_refused():
+    """Kernels would write through them; whether they are large enough does not matter."""
+    given = torch.empty(256, dtype=torch.uint8, device="meta")
+    for need in (0, 256, 512):
+        for dev in ("cuda:0", "cuda:1", "cpu"):
+            with pytest.raises(ValueError, match="workspace is on meta"):
+                kda._workspace(need, given, torch.device(dev))
+    # on the right one: used where it is large enough, as many bytes as it has
+    assert kda._workspace(256, given, given.device) is given and kda._workspace(0, given, given.device) is given
+    assert kda._workspace(1024, torch.empty(256, device="meta"), given.device).dtype is torch.float32
+    assert kda._workspace(512, given, given.device).numel() == 512
+    assert kda._workspace(0, None, given.device) is None
