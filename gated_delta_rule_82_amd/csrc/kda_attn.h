@@ -30,6 +30,11 @@ struct RotaryArgs {
 };
 hipError_t launch_rotary(int dt, const RotaryArgs& a, hipStream_t s);
 
+// Most elements between rows that are copied as tiles.  A tile's rows are addressed with
+// unsigned 32-bit byte offsets from its first: 128 rows of 4-byte elements, the most that a
+// kernel takes (Stage asserts it), start below 2^32 - 2^25.
+constexpr int kTileStride = 1 << 23;
+
 // The G query heads of a key/value head and their tokens are the packed rows
 // r = t * G + g of one problem, 0 <= r < G * Tq, so a tile of rows shares the
 // keys and values it streams.

@@ -42,9 +42,7 @@ bool step_sizes_ok(int B, int Tq, int H, int HK, int max_len) {
     return max_len >= 0 && max_len <= (1 << 29) && rows_ok(B, Tq, H, HK);
 }
 
-// Most elements between rows that are copied as tiles, which are addressed with 32-bit
-// offsets: 64 rows of 4-byte elements stay below 2^31 bytes.
-constexpr int kTileStride = 1 << 23;
+using kda::kTileStride;
 
 // Row stride in elements, at most `most`: 0 selects contiguous tokens.
 kda_status stride(int ld, int most, int heads, int D, kda_dtype dt, size_t* out) {

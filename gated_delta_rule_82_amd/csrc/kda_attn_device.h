@@ -149,6 +149,7 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 template <typename T, int D, int ROWS, int NW, bool Wide = false> struct Stage {
     static constexpr int GR = TileGeom<T, D>::GR, N = ROWS * GR / 64, PER = (N + NW - 1) / NW;
     static_assert(ROWS * GR % 64 == 0, "whole wave instructions");
+    static_assert((unsigned long long)ROWS * kTileStride * sizeof(T) <= 1ull << 32, "rows a largest stride apart fit 32-bit offsets");
     uint32_t off[PER];
     static __device__ __forceinline__ int swizzle(int r) { return Wide ? wide_swizzle<D>(r) : tile_swizzle<T, D>(r); }
     static __device__ __forceinline__ int row(int c, int wave, int lane) { return ((c * NW + wave) * 64 + lane) / GR; }

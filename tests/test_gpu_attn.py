@@ -331,6 +331,53 @@ def test_attn_writes_its_outputs_only(dtype):
     assert bool((lbig[:32] == 7).all()) and bool((lbig[-32:] == 7).all())
 
 
+@pytest.mark.parametrize("dtype,B,Tq,Tk,H,HK,D,kw", [
+    (F32, 2, 37, 50, 4, 2, 64, dict(causal=1)), (F32, 1, 131, 45, 6, 3, 128, dict(causal=0)), (F32, 1, 9, 21, 2, 2, 16, dict(window=5)),
+    (BF16, 2, 37, 50, 4, 2, 64, dict(causal=1)), (BF16, 1, 45, 131, 6, 3, 128, dict(window=70)), (BF16, 3, 7, 5, 4, 1, 32, dict(causal=0)),
+    (BF16, 16, 300, 333, 16, 16, 64, dict(causal=1)), (BF16, 2, 2111, 1001, 16, 16, 128, dict(causal=0)),
+])
+def test_attn_bwd_writes_its_outputs_and_workspace_only(dtype, B, Tq, Tk, H, HK, D, kw):
+    """The C entry with room around every output and a workspace of just the bytes asked for."""
+    lib = kda.load()
+    q, k, v, do = draw(B, Tq, Tk, H, HK, D, dtype, 25)
+    kw = dict(causal=0, window=0) | kw
+    o, lse = kda.attn_fwd(q, k, v, **kw)
+    dt = 1 if dtype is BF16 else 0
+    need = lib.kda_attn_bwd_workspace(B, Tq, Tk, H, HK, D, dt)
+    e = q.element_size()
+    sizes = [B * Tq * H * D * e, B * Tk * HK * D * e, B * Tk * HK * D * e, need]
+    room = [torch.full((n + 8192,), 0x5A, dtype=torch.uint8, device="cuda") for n in sizes]
+    at = [x.data_ptr() + 4096 for x in room]
+    st = lib.kda_attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), None, None, o.data_ptr(), lse.data_ptr(), do.data_ptr(), *at[:3],
+                          B, Tq, Tk, H, HK, D, 0, 0, 0, D ** -0.5, kw["causal"], kw["window"], dt, at[3], need,
+                          torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == 0
+    want = kda.attn_bwd(q, k, v, o, lse, do, **kw)
+    for x, n, name in zip(room, sizes, ("dq", "dk", "dv", None)):
+        assert bool((x[:4096] == 0x5A).all()) and bool((x[4096 + n:] == 0x5A).all()), name
+        if name:
+            assert torch.equal(x[4096:4096 + n].view(dtype), want[name].view(-1)), name
+
+
+@pytest.mark.parametrize("dtype,T,H,D", [(F32, 150, 2, 64), (BF16, 150, 2, 32), (BF16, 300, 2, 128)])
+def test_attn_rows_the_largest_stride_apart(dtype, T, H, D):
+    """q, k and v in rows of 2^23 elements: the last row of a tile of 128 lies almost 2^32 bytes behind its first."""
+    x = torch.empty(1, T, 2 ** 23, dtype=dtype, device="cuda")
+    part = lambda i: x[:, :, 2 ** 20 * i:2 ** 20 * i + H * D].unflatten(2, (H, D))  # noqa: E731
+    c = draw(1, T, T, H, H, D, dtype, 26)
+    far = [part(i) for i in range(3)]
+    for y, z in zip(far, c):
+        y.copy_(z)
+    for kw in (dict(causal=True), dict(causal=False), dict(causal=True, window=40)):
+        o, lse = kda.attn_fwd(*far, **kw)
+        g = kda.attn_bwd(*far, o, lse, c[3], **kw)
+        wo, wl = kda.attn_fwd(*c[:3], **kw)
+        w = kda.attn_bwd(*c[:3], wo, wl, c[3], **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(o, wo) and torch.equal(lse, wl) and all(torch.equal(g[n], w[n]) for n in w), kw
+
+
 def test_attn_bwd_repeats_bit_for_bit():
     q, k, v, do = draw(2, 260, 260, 8, 2, 128, BF16, 16)
     o, lse = kda.attn_fwd(q, k, v)
