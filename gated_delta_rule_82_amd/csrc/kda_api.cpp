@@ -505,7 +505,7 @@ const char* kda_status_string(kda_status s) {
         case KDA_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
         case KDA_ERR_HIP: return "kernel launch failed";
         case KDA_ERR_SCRATCH: return "the sizes need more than the built-in scratch of kda_chunk_fwd_noalloc";
-        case KDA_ERR_SCALE: return "a scale is not finite or not positive";
+        case KDA_ERR_SCALE: return "a scale is not finite, not positive or (softmax) below 2^-64";
     }
     return "unknown status";
 }

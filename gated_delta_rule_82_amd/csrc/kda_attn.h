@@ -7,7 +7,8 @@
 
 namespace kda {
 
-// n / d for 0 <= n < 2^31 as a multiply and a shift: with s = ceil(log2 d) and
+// n / d for 0 <= n < 2^31 as a multiply and a shift (division by invariant integers using
+// multiplication, Granlund and Montgomery 1994): with s = ceil(log2 d) and
 // m = floor(2^32 (2^s - d) / d) + 1, n / d = (mulhi(n, m) + n) >> s.
 struct FastDiv {
     uint32_t d, m, s;
@@ -63,6 +64,12 @@ constexpr int kMaxSplits = 128;
 // fill the card; a split takes at least 256 keys (fp32, whose products cost 16 times
 // as much: 128), so that its partial output stays small beside the keys it reads.
 // fp32, 2 x 4 heads x 1023, D = 64: four parts 33 us with the join, three 37.
+// Kernel and join in us with grids of 256 / 512 / 1024 workgroups, D = 128: 16 rows of 32
+// heads over 65 536 keys of 8, bf16 54 / 54 / 62, fp32 221 / 190 / 206; 64 over 8192, bf16 26 /
+// 31 / 31, fp32 107 / 96 / 105; 256 of 16 heads over 4096, bf16 25 / 33 / 33, fp32 104 / 93 /
+// 103; 16 of 16 over 4096 (2 sequences), bf16 18 / 16 / 18.  Half the keys a split: fp32 16 over
+// 65 536 204, 16 over 4096 25 against 22, one row over 1000 17 against 22; twice: bf16 16 over
+// 4096 21 against 16, one over 1000 24 against 16, 256 over 4096 25 against 33.
 inline int attn_fwd_splits(int elem_bytes, int B, int Tq, int Tk, int HK, int G) {
     const long long rows = (long long)Tq * G, per = attn_rows_per_wave(elem_bytes);
     const long long bq = per * attn_waves(rows, (int)per), wgs = (long long)B * HK * ((rows + bq - 1) / bq);
@@ -135,7 +142,11 @@ struct AttnStepArgs {
 inline int attn_step_row_blocks(long long rows) { return rows <= 16 ? 1 : 2; }
 // Workgroups over a cache of max_len tokens.  Four workgroups of four waves per
 // compute unit keep enough loads in flight; a split takes at least 256 keys (one
-// block for each wave).
+// block for each wave).  Kernel and join in us with grids of 256 / 512 / 1024 / 2048
+// workgroups, bf16, 32 heads (8 of keys), D = 128: 1 x 4 tokens over 65 536 31.7 / 30.2 / 31.9 /
+// 31.7 (32 to 128 parts), 8 x 1 over 8192 28 / 29 / 28 / 28, 32 x 1 over 4096 42 / 47 / 47 / 48,
+// 64 x 1 over 2048 43 / 43 / 48 / 48, 4 x 16 over 16 384 58 / 51 / 64 / 71.  At least 1024 keys
+// a split: 30.2 for the first, 11 against 13 to 19 for one token over 1024.
 inline int attn_step_splits(int B, int Tq, int HK, int G, int max_len) {
     const long long rows = (long long)Tq * G, br = 16 * attn_step_row_blocks(rows);
     const long long wgs = (long long)B * HK * ((rows + br - 1) / br);

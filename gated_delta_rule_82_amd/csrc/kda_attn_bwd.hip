@@ -285,7 +285,7 @@ __global__ __launch_bounds__(64 * NW, 2) void kda_attn_dkv_kernel(const AttnArgs
     const TileLane<T, D> at(lane);
     const float c = a.scale_log2;
     auto step = [&](int rb, uint32_t qs, uint32_t ds, const float* rows, bool masked) {
-        // bf16: P and dS are rounded for their products, 2^-9 relative each
+        // bf16: P and dS are rounded for their products, 2^-8 relative each
         Frag<T> pf[NK], sf[NK];
 #pragma unroll
         for (int i = 0; i < NI; ++i) {

@@ -201,7 +201,7 @@ __global__ __launch_bounds__(512, 2) void kda_attn_dkv_turns_kernel(const AttnAr
                 dp[e] = seen ? dp[e] : 0.f;
             }
         }
-        // P and dS are rounded for their products, 2^-9 relative each
+        // P and dS are rounded for their products, 2^-8 relative each
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
             st[e] = exp2_fast(st[e] * c);
@@ -407,7 +407,7 @@ __global__ __launch_bounds__(512, 2) void kda_attn_dq_turns_kernel(const AttnArg
                     dp[i][e] = seen ? dp[i][e] : 0.f;
                 }
         }
-        // dS is rounded for its product, 2^-9 relative
+        // dS is rounded for its product, 2^-8 relative
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
 #pragma unroll

@@ -165,7 +165,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void kda_attn_fwd_kernel(
         }
 #pragma unroll
         for (int n = 0; n < NQ; ++n) mu[n] = m[n] == kNegInf ? 0.f : m[n];  // a row that has seen nothing yet
-        // bf16 probabilities are rounded for the product (2^-9 relative each, as
+        // bf16 probabilities are rounded for the product (2^-8 relative each, as
         // the values beside them); the sum is over the unrounded ones
         Frag<T> pf[NT / 2][NQ];
 #pragma unroll
@@ -359,7 +359,7 @@ __global__ __launch_bounds__(512, 2) void kda_attn_fwd_turns_kernel(const AttnAr
             for (int d = 0; d < ND; ++d) o[d] *= alpha;
         }
         const float mu = m == kNegInf ? 0.f : m;  // a row that has seen nothing yet
-        // probabilities are rounded to bf16 for the product (2^-9 relative each, as the
+        // probabilities are rounded to bf16 for the product (2^-8 relative each, as the
         // values beside them); the sum is over the unrounded ones
         float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll

@@ -75,6 +75,10 @@ constexpr int append_threads(int D, int page) { return append_items(D, page) >= 
 // are turned into words of four tokens and leave through LDS as whole 16-byte
 // pieces of the page's rows (single bytes where tokens before or after them stay).
 // Bound by the bytes: 4 x 4096 tokens of 8 heads x 128 in bf16 (101 MB) 20.5 us, 4.9 TB/s.
+// That is without a scale that grows under older tokens: their codes are moved a byte at a
+// time, each load waited for before its store.  256 sequences of 4 new tokens, every page's
+// scale growing: 103 us with 32 older tokens in pages of 64, 177 with 60, 480 with 124 of
+// 128; 20 to 27 us where none grows.
 template <typename T, int D, int PAGE>
 __global__ __launch_bounds__(append_threads(D, PAGE)) void kda_cache_append_kernel(const AppendArgs a, int touched) {
     constexpr int NTH = append_threads(D, PAGE), G8 = D / 8, ITEMS = append_items(D, PAGE), U = (ITEMS + NTH - 1) / NTH;
@@ -198,8 +202,13 @@ __global__ __launch_bounds__(append_threads(D, PAGE)) void kda_cache_append_kern
 
 // One token a sequence (decode): a lane holds eight channels of K or of V, D / 8 lanes
 // each, a wave one (sequence, key/value head); no LDS and no barrier.  B = 256, 8 heads,
-// D = 128: 5 us, against 14 us with the workgroup above, whose registers for a whole
-// page let only five of them share a compute unit.
+// D = 128, where no page's scale grows: 5 to 7 us, against 14 us with the workgroup above,
+// whose registers for a whole page let only five of them share a compute unit.
+// Where one grows, its lanes move the older tokens' codes a byte at a time, each load waited
+// for before its store, and the slowest wave decides: 24 us behind 8 older tokens, 74 behind
+// 32, 139 behind 63 of a page of 64, 719 behind 127 of 128.  In a decode of normal values
+// (256 sequences of mixed lengths, pages of 64) some page's scale grows in every step: 76 us,
+// 54 to 90 over 128 steps.  Codes moved in 16-byte pieces are the remedy; not done here.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void kda_cache_append_one_kernel(const AppendArgs a) {
     constexpr int G8 = D / 8;
@@ -286,7 +295,9 @@ hipError_t launch_cache_append(int dt, int D, const AppendArgs& a, hipStream_t s
 namespace {
 
 // Operands of an fp32 path as bf16 parts: x = sum of the parts to 24 bits.  The
-// codes are exact in bf16, so three products give the fp32 one.
+// codes are exact in bf16, so three products give the fp32 one.  In bf16 queries are
+// exact as they are, and a probability times its page's scale (a power of two) is rounded
+// once, 2^-8 relative at most, as in the forward; the sum is over the unrounded ones.
 template <typename T> struct Parts { static constexpr int N = sizeof(T) == 2 ? 1 : 3; };
 
 template <int N>

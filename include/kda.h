@@ -459,7 +459,8 @@ kda_status kda_attn_fwd(const void* q, const void* k, const void* v, const int* 
  * inputs and its o and lse (the probabilities are recomputed):
  *   dv_j = sum_i P_ij dout_i,   dS_ij = P_ij (dout_i.v_j - dout_i.o_i),
  *   dq_i = scale sum_j dS_ij k_j,   dk_j = scale sum_i dS_ij q_i,
- * dk and dv summed over the G query heads of each key/value head.  No
+ * dk and dv summed over the G query heads of each key/value head.  Sums are
+ * fp32; in bf16 P and dS are rounded to bf16 before their products.  No
  * atomics: results do not vary from run to run.  With causal = 0 and window = 0
  * k and v may be a part of the keys that o and lse were formed with: dk and dv
  * are then that part's, and dq its share of the sum.  With a causal mask or a
@@ -469,8 +470,9 @@ kda_status kda_attn_fwd(const void* q, const void* k, const void* v, const int* 
  * rounding of o would show in the gradients.
  *   o, dout, dq [B,Tq,H,D], dk, dv [B,Tk,HK,D]: contiguous, dtype dt.  Rows
  *   past the lengths, and rows that see or are seen by nothing, get 0; o, lse
- *   and dout are not read past q_len.  What is not finite inside the lengths
- *   may reach the gradients of rows and keys of the same tile too.
+ *   and dout are not read past q_len.  What is not finite inside the lengths, or
+ *   has a product past fp32's range there, may reach the gradients of rows and
+ *   keys of the same tile too.
  *   workspace  kda_attn_bwd_workspace bytes, 256-byte aligned.
  * Outputs may overlap neither an input, another output nor the workspace
  * (KDA_ERR_SHAPE).  Errors otherwise as kda_attn_fwd. */
