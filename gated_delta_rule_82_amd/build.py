@@ -21,7 +21,8 @@ OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkda.so")
 SOURCES = ["kda_api.cpp", "kda_step.hip", "kda_chunk.hip", "kda_layer.hip", "kda_compose.hip", "kda_conv.hip", "kda_gate.hip", "kda_bwd.hip",
            "kda_attn_api.cpp", "kda_rotary.hip", "kda_attn_fwd.hip", "kda_attn_bwd.hip", "kda_attn_bwd_turns.hip",
-           "kda_cache.hip"]
+           "kda_cache.hip", "kda_branch_api.cpp", "kda_pages.hip", "kda_shared.hip",
+           "kda_beam.hip"]
 ARCH = os.environ.get("KDA_OFFLOAD_ARCH", "gfx950")
 
 

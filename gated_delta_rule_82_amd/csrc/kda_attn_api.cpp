@@ -5,25 +5,13 @@
 #include <math.h>
 
 #include "kda_attn.h"
-#include "kda_validate.h"
+#include "kda_attn_validate.h"
 
 using namespace kda::host;
 
 namespace {
 
 constexpr double kPi = 3.14159265358979323846;
-constexpr double kLog2eD = 1.44269504088896340736;
-
-bool heads_ok(int H, int HK) { return H >= 0 && HK >= 0 && (H == 0 || (HK > 0 && H % HK == 0)); }
-
-bool rows_ok(int B, int Tq, int H, int HK) {
-    if (!heads_ok(H, HK) || !sizes_ok(B, Tq, H)) return false;
-    if (H == 0) return true;
-    // packed rows of one key/value head, and less than 2^24 workgroups of 32 of them
-    // (a grid holds less than 2^32 threads, a workgroup 256)
-    const unsigned long long rows = (unsigned long long)(H / HK) * Tq;
-    return rows <= (1ull << 29) && (unsigned long long)B * HK * (rows / 32 + 1) < (1ull << 24);
-}
 
 // Keys in one piece: as many workgroups of them in the backward.
 bool attn_sizes_ok(int B, int Tq, int Tk, int H, int HK) {
@@ -37,53 +25,10 @@ bool row_pieces_ok(int B, int Tq, int H, int D, kda_dtype dt) {
     return (unsigned long long)B * H * (((unsigned long long)Tq + kda::kAttnRowPad) * (D * elem_bytes(dt) / 16) + 256) < (1ull << 32);
 }
 
-// A paged cache: its length only bounds a loop.
-bool step_sizes_ok(int B, int Tq, int H, int HK, int max_len) {
-    return max_len >= 0 && max_len <= (1 << 29) && rows_ok(B, Tq, H, HK);
-}
-
 using kda::kTileStride;
-
-// Row stride in elements, at most `most`: 0 selects contiguous tokens.
-kda_status stride(int ld, int most, int heads, int D, kda_dtype dt, size_t* out) {
-    const long long least = (long long)heads * D;
-    if (ld < 0 || (ld > 0 && ld < least) || ld > most || least > kTileStride) return KDA_ERR_SHAPE;
-    *out = ld ? (size_t)ld : (size_t)least;
-    return (*out * elem_bytes(dt)) % 16 == 0 ? KDA_OK : KDA_ERR_ALIGN;
-}
-
-Rows rows_of(const void* p, size_t tokens, size_t ld, size_t heads, size_t D, kda_dtype dt) {
-    const size_t e = (size_t)elem_bytes(dt);
-    return Rows{p, tokens, ld * e, heads * D * e};
-}
-// n bytes in one piece, for comparison with strided rows
-Rows bytes_of(const void* p, size_t n) { return Rows{p, n ? (size_t)1 : 0, n, n}; }
-
-bool overlaps_any(const Rows& out, const Rows* in, size_t n) {
-    for (size_t i = 0; i < n; ++i)
-        if (overlaps(out, in[i])) return true;
-    return false;
-}
-
-kda_status check_workspace(const void* ws, size_t have, size_t want) {
-    if (want == 0) return KDA_OK;
-    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 || have < want) return KDA_ERR_WORKSPACE;
-    return KDA_OK;
-}
-
-size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
-
-// Partial results of a key axis split over n workgroups: n x rows outputs of D
-// floats, then as many (maximum, sum) pairs.
-size_t split_bytes(int n, size_t rows, int D) {
-    return n <= 1 ? 0 : round256((size_t)n * rows * D * 4) + round256((size_t)n * rows * 8);
-}
 
 // Queries per head in the backward's row array.
 size_t padded_rows(int Tq) { return ((size_t)Tq + kda::kAttnRowPad - 1) / kda::kAttnRowPad * kda::kAttnRowPad; }
-
-// The kernels use it times log2 e, the backward lse over it.
-bool scale_ok(float s) { return s >= 0x1p-64f && isfinite((float)(s * kLog2eD)); }
 
 // A window as long as the key axis hides nothing.
 int clamp_window(int w, int keys) { return w >= keys ? 0 : w; }
@@ -245,14 +190,6 @@ kda_status kda_attn_bwd(const void* q, const void* k, const void* v, const int* 
     a.divG = kda::fast_div((uint32_t)a.G);
     a.nsplit = 1;
     return kda::launch_attn_bwd(dt == KDA_BF16 ? 1 : 0, D, a, stream) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
-}
-
-static bool cache_sizes_ok(int n_pages, int max_pages, int B, int T, int HK, int D, int page) {
-    if (!dim_ok(D) || (page != 16 && page != 32 && page != 64 && page != 128)) return false;
-    if (n_pages < 0 || max_pages < 0 || !sizes_ok(B, T, HK)) return false;
-    return (unsigned long long)n_pages * (unsigned)HK <= (1ull << 30) &&
-           (unsigned long long)max_pages * (unsigned)page <= (1ull << 30) &&
-           (unsigned long long)B * (unsigned)max_pages <= (1ull << 40);
 }
 
 kda_status kda_cache_append(const void* k, const void* v, void* k_cache, void* v_cache,

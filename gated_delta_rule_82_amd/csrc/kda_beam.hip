@@ -1,0 +1,423 @@
+// kda_beam.hip - beam search on gfx950: the best continuations of a request's beams
+// over the whole vocabulary, and states that follow their parents.
+//
+// Selection.  s(b, w) = score_b + x_bw - lse_b, lse_b = ln sum_w exp x_bw, and the M
+// largest of a request, ties to the lowest (b, w).  Within a beam the order is that of
+// the logits, whatever lse_b is, so one pass over the logits gives both: workgroups
+// take parts of a row and leave the part's maximum, its sum of exponentials and its M
+// first logits; one workgroup a request joins them in 64 bits.
+#include "kda_attn_device.h"
+#include "kda_branch.h"
+
+namespace kda {
+
+namespace {
+
+constexpr int kSegments = 8;      // of a part: each thread keeps the maximum of what it read of each
+constexpr int kUnroll = 8;        // 16-byte loads of a thread in flight; a segment is a multiple of them
+constexpr int kFound = 1024;      // candidates of a part that are ranked
+
+// Order of values as that of unsigned integers; -0 is +0.
+__device__ __forceinline__ uint32_t order_key(float x) {
+    const uint32_t u = __float_as_uint(x + 0.f);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+__device__ __forceinline__ uint64_t order_key(double x) {
+    const uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);
+    return u ^ ((uint64_t)((int64_t)u >> 63) | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double key_value(uint64_t k) {
+    return __longlong_as_double((long long)(k & 0x8000000000000000ull ? k ^ 0x8000000000000000ull : ~k));
+}
+
+// The largest t such that at least `most` of a wave's 4 x 64 keys are >= t (0 if fewer are).
+__device__ __forceinline__ uint32_t threshold(const uint32_t (&key)[4], int most) {
+    uint32_t t = 0;
+    for (int bit = 31; bit >= 0; --bit) {
+        const uint32_t c = t | 1u << bit;
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) n += __popcll(__ballot(key[i] >= c));
+        if (n >= most) t = c;
+    }
+    return t;
+}
+
+template <typename T> struct Vec {
+    static constexpr int N = 16 / (int)sizeof(T);
+    float x[N];
+    // from a row whose elements are aligned as such only; those at or past n are -infinity
+    __device__ __forceinline__ void load(const T* row, int at, int n) {
+        struct __attribute__((packed, aligned(sizeof(T)))) Raw { uint32_t w[4]; };
+        if (at + N <= n) {
+            const Raw r = *reinterpret_cast<const Raw*>(row + at);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                x[i] = sizeof(T) == 4 ? __uint_as_float(r.w[i % 4])
+                                      : __uint_as_float(i & 1 ? r.w[(i / 2) % 4] & 0xffff0000u : r.w[(i / 2) % 4] << 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] = at + i < n ? to_f<T>(row[at + i]) : kNegInf;
+        }
+    }
+};
+
+__device__ __forceinline__ bool beam_lives(const SelectArgs& a, int row) {
+    return !a.scores || (a.scores[row] - a.scores[row] == 0.f);   // finite
+}
+
+}  // namespace
+
+// One part of one beam's row.  Each thread keeps the maximum and the sum of exponentials
+// of what it reads, and the maxima of its segments.  The M-th largest of the threads'
+// maxima bounds the M first from below; only segments that reach it are read again (a
+// few of 2048, from the cache nearby) and what reaches it there, usually little more
+// than M values, is ranked by counting.
+template <typename T>
+__global__ __launch_bounds__(kSelThreads) void kda_select_part_kernel(const SelectArgs a) {
+    constexpr int N = Vec<T>::N, STEP = kSelThreads * N;
+    __shared__ float seg[kSegments][kSelThreads];
+    __shared__ float top[kSelThreads];
+    __shared__ uint64_t found[kFound];
+    __shared__ uint16_t todo[kSegments * kSelThreads];
+    __shared__ double sums[kSelThreads / 64];
+    __shared__ int counts[kSelThreads / 64], n_todo, n_found, n_above;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int row = blockIdx.x / a.nsplit, split = blockIdx.x % a.nsplit;
+    if ((a.done && a.done[row]) || !beam_lives(a, row)) return;    // the join does not ask for it
+    const int per = select_part(a.V, a.nsplit, N), lo = min((long long)split * per, (long long)a.V), n = min(per, a.V - lo);
+    const T* x = reinterpret_cast<const T*>(a.logits) + (size_t)row * a.ld + lo;
+    // loads of a segment
+    const int loads = (n + STEP - 1) / STEP, per_seg = max(1, (loads + kSegments * kUnroll - 1) / (kSegments * kUnroll)) * kUnroll;
+
+    float m = kNegInf, l = 0.f;
+    for (int s = 0; s < kSegments; ++s) {
+        float best = kNegInf;
+        for (int i = s * per_seg; i < min((s + 1) * per_seg, loads); i += kUnroll) {
+            Vec<T> v[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) v[u].load(x, ((i + u) * kSelThreads + tid) * N, n);
+            float y = kNegInf;
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+                for (int e = 0; e < N; ++e) y = fmaxf(y, v[u].x[e]);
+            best = fmaxf(best, y);
+            const float now = fmaxf(m, y), mu = now == kNegInf ? 0.f : now;
+            l *= exp_carried(m - mu);
+            m = now;
+            float part = 0.f;
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+                for (int e = 0; e < N; ++e) part += exp_carried(v[u].x[e] - mu);
+            l += part;
+        }
+        seg[s][tid] = best;
+    }
+    top[tid] = m;
+    if (tid == 0) n_todo = n_found = n_above = 0;
+    __syncthreads();
+
+    uint32_t key[4];
+    float all = kNegInf;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float y = top[i * 64 + lane];
+        key[i] = order_key(y);
+        all = fmaxf(all, y);
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor(all, o, 64));
+    double sum = (double)l * (double)exp_carried(m - (all == kNegInf ? 0.f : all));
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+    if (lane == 0) sums[wave] = sum;
+    // candidates reach t; -infinity is none
+    uint32_t t = max(threshold(key, a.M), order_key(kNegInf) + 1);
+
+    auto collect = [&](uint32_t least, int* counter) {   // of the segments in `todo`
+        for (int i = tid; i < n_todo * per_seg; i += kSelThreads) {
+            const int which = todo[i / per_seg], at = ((which / kSelThreads * per_seg + i % per_seg) * kSelThreads + which % kSelThreads) * N;
+            if (at >= n) continue;
+            Vec<T> v;
+            v.load(x, at, n);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const uint32_t k = order_key(v.x[e]);
+                if (k < least || v.x[e] != v.x[e]) continue;
+                const int p = atomicAdd(counter, 1);
+                if (p < kFound) found[p] = (uint64_t)k << 32 | (uint32_t)~(uint32_t)(at + e);
+            }
+        }
+    };
+    for (int s = 0; s < kSegments; ++s)
+        if (order_key(seg[s][tid]) >= t) todo[atomicAdd(&n_todo, 1)] = (uint16_t)(s * kSelThreads + tid);
+    __syncthreads();
+    collect(t, &n_found);
+    __syncthreads();
+    int held = n_found;
+    if (held > kFound) {
+        // many reach t: equal values (rows masked with one value), or rising ones.  What is
+        // above t, and then the first that are equal to it in the order of the row.
+        collect(t + 1, &n_above);
+        __syncthreads();
+        held = n_above;
+        if (held > kFound) {
+            // more than can be ranked: t becomes the M-th largest value of the part itself
+            uint32_t exact = 0;
+            for (int bit = 31; bit >= 0; --bit) {
+                const uint32_t c = exact | 1u << bit;
+                int mine = 0;
+                for (int i = tid; i < n_todo * per_seg; i += kSelThreads) {
+                    const int which = todo[i / per_seg], at = ((which / kSelThreads * per_seg + i % per_seg) * kSelThreads + which % kSelThreads) * N;
+                    if (at >= n) continue;
+                    Vec<T> v;
+                    v.load(x, at, n);
+#pragma unroll
+                    for (int e = 0; e < N; ++e) mine += v.x[e] == v.x[e] && order_key(v.x[e]) >= c ? 1 : 0;
+                }
+#pragma unroll
+                for (int o = 32; o > 0; o >>= 1) mine += __shfl_xor(mine, o, 64);
+                __syncthreads();
+                if (lane == 0) counts[wave] = mine;
+                __syncthreads();
+                int total = 0;
+                for (int w = 0; w < kSelThreads / 64; ++w) total += counts[w];
+                if (total >= a.M) exact = c;
+            }
+            t = exact;
+            __syncthreads();
+            if (tid == 0) n_above = 0;
+            __syncthreads();
+            collect(t + 1, &n_above);     // fewer than M
+            __syncthreads();
+            held = n_above;
+        }
+        for (int at0 = 0; at0 < n && held < a.M; at0 += STEP) {
+            Vec<T> v;
+            const int at = at0 + tid * N;
+            int mine = 0;
+            if (at < n) {
+                v.load(x, at, n);
+#pragma unroll
+                for (int e = 0; e < N; ++e) mine += order_key(v.x[e]) == t ? 1 : 0;
+            }
+            int y = mine;
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const int z = __shfl_up(y, o, 64);
+                if (lane >= o) y += z;
+            }
+            __syncthreads();
+            if (lane == 63) counts[wave] = y;
+            __syncthreads();
+            int before = held, total = 0;
+            for (int w = 0; w < kSelThreads / 64; ++w) {
+                before += w < wave ? counts[w] : 0;
+                total += counts[w];
+            }
+            before += y - mine;
+            if (mine > 0) {
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    if (order_key(v.x[e]) == t) {
+                        if (before < a.M) found[before] = (uint64_t)t << 32 | (uint32_t)~(uint32_t)(at + e);
+                        ++before;
+                    }
+            }
+            held = min(held + total, max(a.M, held));
+        }
+        __syncthreads();
+    }
+
+    const size_t part = blockIdx.x;
+    for (int i = tid; i < held; i += kSelThreads) {
+        const uint64_t k = found[i];
+        int rank = 0;
+        for (int j = 0; j < held; ++j) rank += found[j] > k ? 1 : 0;
+        if (rank < a.M) {
+            a.part_x[part * a.M + rank] = key_value((uint32_t)(k >> 32));
+            a.part_w[part * a.M + rank] = lo + (int)~(uint32_t)k;
+        }
+    }
+    for (int i = held + tid; i < a.M; i += kSelThreads) a.part_w[part * a.M + i] = -1;
+    if (tid == 0) {
+        double total = 0.0;
+        for (int w = 0; w < kSelThreads / 64; ++w) total += sums[w];
+        a.stat[2 * part] = all;
+        a.stat[2 * part + 1] = total;
+    }
+}
+
+// One workgroup a request: each beam's lse from its parts, then its parts' candidates
+// as scores in 64 bits, thinned by the M-th largest of the threads' maxima (of the
+// upper halves of their keys) and ranked by counting.
+__global__ __launch_bounds__(kSelThreads) void kda_select_join_kernel(const SelectArgs a) {
+    __shared__ uint64_t key[kSelectHeld];
+    __shared__ uint64_t id[kSelectHeld];        // beam << 32 | token
+    __shared__ uint16_t list[kSelectHeld];
+    __shared__ uint32_t top[kSelThreads];
+    __shared__ double lse[kSelectMost], score[kSelectMost];
+    __shared__ int n_list;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = blockIdx.x;
+    for (int k = wave; k < a.K; k += kSelThreads / 64) {
+        const int row = r * a.K + k;
+        const bool lives = beam_lives(a, row), done = a.done && a.done[row];
+        double z = 0.0, y = lives && a.scores ? (double)a.scores[row] : 0.0;
+        if (lives && !done) {
+            const size_t part = (size_t)row * a.nsplit + lane;
+            const bool mine = lane < a.nsplit;
+            const float m = mine ? (float)a.stat[2 * part] : kNegInf;
+            const double l = mine ? a.stat[2 * part + 1] : 0.0;
+            float all = m;
+#pragma unroll
+            for (int o = 32; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor(all, o, 64));
+            double sum = l == 0.0 ? 0.0 : l * exp((double)m - (double)all);
+#pragma unroll
+            for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+            z = (double)all + log(sum);
+        }
+        if (lane == 0) {
+            lse[k] = z;
+            score[k] = y;
+        }
+    }
+    if (tid == 0) n_list = 0;
+    __syncthreads();
+    const int per = a.nsplit * a.M, held = a.K * per;
+    uint32_t most = 0;
+    for (int i = tid; i < held; i += kSelThreads) {
+        const int k = i / per, row = r * a.K + k;
+        const bool lives = beam_lives(a, row), done = a.done && a.done[row];
+        uint64_t y = 0, w = 0;
+        if (lives) {
+            double s = -__builtin_inf();
+            if (done) {
+                if (i % per == 0) {
+                    s = score[k];
+                    w = (uint32_t)a.end;
+                }
+            } else {
+                const size_t at = (size_t)r * held + i;
+                const int token = a.part_w[at];
+                if (token >= 0) {
+                    s = score[k] + ((double)a.part_x[at] - lse[k]);
+                    w = (uint32_t)token;
+                }
+            }
+            if (s - s == 0.0) y = order_key(s);   // what is not finite is no continuation
+        }
+        key[i] = y;
+        id[i] = (uint64_t)k << 32 | w;
+        most = max(most, (uint32_t)(y >> 32));
+    }
+    top[tid] = most;
+    __syncthreads();
+    uint32_t mine[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mine[i] = top[i * 64 + lane];
+    const uint32_t t = max(threshold(mine, a.M), 1u);   // the key of no finite number is below 2^32
+    for (int i = tid; i < held; i += kSelThreads)
+        if ((uint32_t)(key[i] >> 32) >= t) list[atomicAdd(&n_list, 1)] = (uint16_t)i;
+    __syncthreads();
+    const int n = n_list;
+    for (int i = tid; i < n; i += kSelThreads) {
+        const uint64_t y = key[list[i]], w = id[list[i]];
+        int rank = 0;
+        for (int j = 0; j < n; ++j) {
+            const uint64_t yj = key[list[j]];
+            rank += yj > y || (yj == y && id[list[j]] < w) ? 1 : 0;
+        }
+        if (rank < a.M) {
+            const size_t at = (size_t)r * a.M + rank;
+            a.scores_out[at] = (float)key_value(y);
+            a.parent[at] = (int)(w >> 32);
+            a.token[at] = (int)(uint32_t)w;
+        }
+    }
+    for (int i = n + tid; i < a.M; i += kSelThreads) {
+        const size_t at = (size_t)r * a.M + i;
+        a.scores_out[at] = kNegInf;
+        a.parent[at] = a.token[at] = -1;
+    }
+}
+
+template <typename T> static hipError_t launch_select_t(const SelectArgs& a, hipStream_t s) {
+    hipLaunchKernelGGL((kda_select_part_kernel<T>), dim3((unsigned)a.R * a.K * a.nsplit), dim3(kSelThreads), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kda_select_join_kernel, dim3((unsigned)a.R), dim3(kSelThreads), 0, s, a);
+    return hipGetLastError();
+}
+hipError_t launch_beam_select(int dt, const SelectArgs& a, hipStream_t s) {
+    return dt == 1 ? launch_select_t<bf16_t>(a, s) : launch_select_t<float>(a, s);
+}
+
+// ---------------------------------------------------------------- states
+
+// In place: a thread has the same 16 bytes of every row of a request, reads what
+// moves and then writes it, so nothing is lost whatever the parents are, and rows that
+// stay are not touched.
+template <int KM, typename P>
+__global__ __launch_bounds__(256) void kda_reorder_kernel(const ReorderArgs a, unsigned blocks) {
+    const unsigned r = blockIdx.x / blocks;
+    const unsigned long long at = ((unsigned long long)(blockIdx.x % blocks) * 256 + threadIdx.x) * sizeof(P);
+    if (at >= a.row_bytes) return;
+    const int* parent = a.parent + (size_t)r * a.K_out;
+    uint8_t* base = a.out + (size_t)r * a.K_out * a.row_bytes + at;
+    P v[KM];
+#pragma unroll
+    for (int k = 0; k < KM; ++k) {
+        v[k] = P{};
+        if (k < a.K_out) {
+            const int p = parent[k];
+            if (p != k && p >= 0 && p < a.K_in) v[k] = *reinterpret_cast<const P*>(base + (size_t)p * a.row_bytes);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < KM; ++k)
+        if (k < a.K_out && parent[k] != k) *reinterpret_cast<P*>(base + (size_t)k * a.row_bytes) = v[k];
+}
+
+// Into other memory: four 16-byte pieces a thread.
+__global__ __launch_bounds__(256) void kda_gather_kernel(const ReorderArgs a, unsigned blocks) {
+    const unsigned row = blockIdx.x / blocks, r = row / a.K_out;
+    const unsigned long long first = (unsigned long long)(blockIdx.x % blocks) * 16384 + threadIdx.x * 16;
+    const int p = a.parent[row];
+    const bool child = p >= 0 && p < a.K_in;
+    const uint8_t* from = a.state + ((size_t)r * a.K_in + (child ? p : 0)) * a.row_bytes;
+    uint8_t* to = a.out + (size_t)row * a.row_bytes;
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (child && first + i * 4096 < a.row_bytes) v[i] = *reinterpret_cast<const uint4*>(from + first + i * 4096);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (first + i * 4096 < a.row_bytes) *reinterpret_cast<uint4*>(to + first + i * 4096) = v[i];
+}
+
+template <int KM, typename P> static hipError_t launch_reorder_n(const ReorderArgs& a, hipStream_t s) {
+    const unsigned blocks = (unsigned)((a.row_bytes / sizeof(P) + 255) / 256);
+    hipLaunchKernelGGL((kda_reorder_kernel<KM, P>), dim3((unsigned)a.R * blocks), dim3(256), 0, s, a, blocks);
+    return hipGetLastError();
+}
+hipError_t launch_state_reorder(const ReorderArgs& a, hipStream_t s) {
+    if (a.out == a.state)
+        return a.K_out <= 4   ? launch_reorder_n<4, uint4>(a, s)
+               : a.K_out <= 8 ? launch_reorder_n<8, uint4>(a, s)
+               : a.K_out <= 16 ? launch_reorder_n<16, uint4>(a, s)
+               : a.K_out <= 32 ? launch_reorder_n<32, uint4>(a, s)
+                               : launch_reorder_n<kReorderMost, uint2>(a, s);
+    const unsigned blocks = (unsigned)((a.row_bytes + 16383) / 16384);
+    hipLaunchKernelGGL(kda_gather_kernel, dim3((unsigned)a.R * a.K_out * blocks), dim3(256), 0, s, a, blocks);
+    return hipGetLastError();
+}
+
+}  // namespace kda

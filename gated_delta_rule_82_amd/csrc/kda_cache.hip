@@ -6,7 +6,7 @@
 // depends on how a division rounds.  K pages are [page][D], V pages [D][page]:
 // both are then read along their contraction axis, 16 bytes a lane, straight into
 // the matrix operands.
-#include "kda_attn_device.h"
+#include "kda_cache_device.h"
 
 namespace kda {
 
@@ -292,69 +292,17 @@ hipError_t launch_cache_append(int dt, int D, const AppendArgs& a, hipStream_t s
     return dt == 1 ? launch_append_d<bf16_t>(D, a, s) : launch_append_d<float>(D, a, s);
 }
 
-namespace {
-
-// Operands of an fp32 path as bf16 parts: x = sum of the parts to 24 bits.  The
-// codes are exact in bf16, so three products give the fp32 one.  In bf16 queries are
-// exact as they are, and a probability times its page's scale (a power of two) is rounded
-// once, 2^-8 relative at most, as in the forward; the sum is over the unrounded ones.
-template <typename T> struct Parts { static constexpr int N = sizeof(T) == 2 ? 1 : 3; };
-
-template <int N>
-__device__ __forceinline__ void split_parts(const float (&x)[8], Frag<bf16_t> (&f)[N]) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        float r = x[j];
-#pragma unroll
-        for (int p = 0; p < N; ++p) {
-            const bf16_t h = (bf16_t)r;
-            f[p].v[j] = h;
-            r -= (float)h;
-        }
-    }
-}
-
-// Eight codes (two words) as a matrix operand.
-__device__ __forceinline__ Frag<bf16_t> codes_frag(uint32_t a, uint32_t b) {
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-    const bf16x2 w = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, false), x = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, true);
-    const bf16x2 y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, false), z = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, true);
-    Frag<bf16_t> f;
-    f.v = bf16x8{w[0], w[1], x[0], x[1], y[0], y[1], z[0], z[1]};
-    return f;
-}
-
-// Bytes 0 .. n-1 of a 16-byte piece, the others zero.
-__device__ __forceinline__ uint4 keep_bytes(uint4 v, int n) {
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int k = n - 4 * i;
-        w[i] = k >= 4 ? w[i] : k <= 0 ? 0u : w[i] & ((1u << (8 * k)) - 1u);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 constexpr int kStepWaves = 4;
-constexpr int kStepKeys = 64;   // keys of a wave's block: 16 for each lane group
 
-}  // namespace
-
-// A wave takes blocks of 64 keys: lane group g stands for keys 16 g .. 16 g + 15
-// of the block, which lie in one page, in the order in which its V bytes come.
-// Score tile i is formed with K rows ordered so that its accumulator rows of
-// group g are keys 16 g + 4 i .. + 3: the exponentials of the four tiles are then
-// the right operands of the product with V without moving.  Scales enter as one
-// factor per lane.  The waves of a workgroup take blocks in turn and are joined
-// in LDS; splits of a long cache are joined by kda_attn_join_kernel.  Nothing of the
+// A wave takes blocks of 64 keys (CacheRows).  The waves of a workgroup take blocks in
+// turn and are joined in LDS; splits of a long cache are joined by kda_attn_join_kernel.  Nothing of the
 // cache is staged: every byte is used by one wave, and loads straight into the operands
 // leave the LDS and barriers out of the stream.  Bound by the bytes: 256 sequences of up
 // to 4096 tokens, 8 heads of 128 channels (1.21 GB), 32 query heads 218 us, 5.5 TB/s; one
 // sequence of 65 536, four new tokens (134 MB) 27 us and 5.5 for the join of 128 parts.
 template <typename T, int D, int NR>
 __global__ __launch_bounds__(64 * kStepWaves) void kda_attn_step_kernel(const AttnStepArgs a) {
-    constexpr int NP = Parts<T>::N, NS = (D + 31) / 32, ND = D / 16, NW = kStepWaves;
-    constexpr int KW = D / 16;                 // words of K a lane holds per tile
+    constexpr int ND = D / 16, NW = kStepWaves;
     __shared__ __attribute__((aligned(16))) float so[NW][16][D + 4];
     __shared__ float sml[NW][16][2];
 
@@ -386,153 +334,35 @@ __global__ __launch_bounds__(64 * kStepWaves) void kda_attn_step_kernel(const At
         }
     }
 
-    int lo[NR], hi[NR];
-    Frag<bf16_t> qf[NR][NS][NP];
+    CacheRows<T, D, NR> x;
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
         const int r = min(r0 + 16 * n + lr, rows - 1);
         const int t = (int)fdiv((uint32_t)r, a.divG), h = hk * a.G + (r - t * a.G);
-        hi[n] = (int)min((long long)kl - 1, before + t);
-        lo[n] = a.window ? (int)min((long long)kl, before + t - a.window + 1) : 0;
+        x.hi[n] = (int)min((long long)kl - 1, before + t);
+        x.lo[n] = a.window ? (int)min((long long)kl, before + t - a.window + 1) : 0;
         // rows past the newest token are computed on a valid row and dropped
         const int tr = max(min(t, ql - 1), 0);
-        const T* qp = reinterpret_cast<const T*>(a.q) + ((size_t)b * a.Tq + tr) * a.ldq + (size_t)h * D;
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-            float x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = 0.f;
-            if constexpr (D >= 32) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = to_f<T>(qp[g * (D / 4) + 8 * s + e]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = to_f<T>(qp[4 * g + e]);
-            }
-            split_parts<NP>(x, qf[n][s]);
-        }
+        x.load_query(n, reinterpret_cast<const T*>(a.q) + ((size_t)b * a.Tq + tr) * a.ldq + (size_t)h * D, g);
     }
-
-    float m[NR], l[NR];
-    floatx4 o[ND][NR];
-#pragma unroll
-    for (int n = 0; n < NR; ++n) {
-        m[n] = kNegInf;
-        l[n] = 0.f;
-#pragma unroll
-        for (int d = 0; d < ND; ++d) o[d][n] = floatx4{0.f, 0.f, 0.f, 0.f};
-    }
-    const int* table = a.block_table + (size_t)b * a.max_pages;
-    const float c = a.scale_log2;
-
-    for (int kb = kb0 + wave; kb < kb1; kb += NW) {
-        const int k0 = kb * kStepKeys;
-        // pages of the lane's V keys (sub-block g) and of its K rows (sub-block
-        // lr / 4); sub-blocks past the last token repeat the last one
-        const int last = (kl - 1) >> 4;
-        const int subv = min((k0 >> 4) + g, last), subk = min((k0 >> 4) + (lr >> 2), last);
-        int pv = table[subv * 16 / a.page], pk = table[subk * 16 / a.page];
-        const bool seen = pv >= 0 && pv < a.n_pages;         // a missing page is masked and reads page 0
-        pv = seen ? pv : 0;
-        pk = pk >= 0 && pk < a.n_pages ? pk : 0;
-        const size_t sv = (size_t)pv * a.HK + hk, sk = (size_t)pk * a.HK + hk;
-        const float ksc = a.k_scale[sv] * c, vsc = a.v_scale[sv];
-        const uint8_t* kp = a.k_cache + sk * (size_t)a.page * D + (size_t)(subk * 16 % a.page + (lr & 3)) * D + g * (D / 4);
-        const uint8_t* vp = a.v_cache + sv * (size_t)a.page * D + (size_t)lr * a.page + subv * 16 % a.page;
-        uint32_t kw[4][KW];
-        uint4 vw[ND];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint8_t* p = kp + 4 * i * D;
-            if constexpr (KW >= 4) {
-#pragma unroll
-                for (int w = 0; w < KW / 4; ++w) {
-                    const uint4 x = reinterpret_cast<const uint4*>(p)[w];
-                    kw[i][4 * w] = x.x; kw[i][4 * w + 1] = x.y; kw[i][4 * w + 2] = x.z; kw[i][4 * w + 3] = x.w;
-                }
-            } else {
-#pragma unroll
-                for (int w = 0; w < KW; ++w) kw[i][w] = reinterpret_cast<const uint32_t*>(p)[w];
-            }
-        }
-#pragma unroll
-        for (int d = 0; d < ND; ++d) vw[d] = *reinterpret_cast<const uint4*>(vp + (size_t)(16 * d) * a.page);
-        const int key0 = k0 + 16 * g, valid = seen ? kl - key0 : 0;  // this group's keys below the length
-        if (!__all(valid >= 16)) {  // bytes past the last token may be anything, NaN codes among them
-#pragma unroll
-            for (int d = 0; d < ND; ++d) vw[d] = keep_bytes(vw[d], valid);
-        }
-
-        floatx4 st[4][NR];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-            for (int n = 0; n < NR; ++n) st[i][n] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int s = 0; s < NS; ++s) {
-                const Frag<bf16_t> kf = codes_frag(kw[i][KW >= 2 ? 2 * s : 0], KW >= 2 ? kw[i][KW >= 2 ? 2 * s + 1 : 0] : 0u);
-#pragma unroll
-                for (int n = 0; n < NR; ++n)
-#pragma unroll
-                    for (int p = 0; p < NP; ++p) st[i][n] = mma(kf, qf[n][s][p], st[i][n]);
-            }
-        }
-        Frag<bf16_t> pf[2][NR][NP];
-#pragma unroll
-        for (int n = 0; n < NR; ++n) {
-            float x = kNegInf;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int key = key0 + 4 * i + e;
-                    const float y = st[i][n][e] * ksc;
-                    st[i][n][e] = seen && key >= lo[n] && key <= hi[n] ? y : kNegInf;
-                    x = fmaxf(x, st[i][n][e]);
-                }
-            x = fmaxf(m[n], group_max4(x));
-            const float mu = x == kNegInf ? 0.f : x, alpha = exp2_fast(m[n] - mu);
-            m[n] = x;
-            l[n] *= alpha;
-#pragma unroll
-            for (int d = 0; d < ND; ++d) o[d][n] *= alpha;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                float pr[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float y = exp2_fast(st[2 * u + e / 4][n][e % 4] - mu);
-                    l[n] += y;
-                    pr[e] = y == 0.f ? 0.f : y * vsc;  // an unread page's scale may be anything
-                }
-                split_parts<NP>(pr, pf[u][n]);
-            }
-        }
-#pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const Frag<bf16_t> vf = u == 0 ? codes_frag(vw[d].x, vw[d].y) : codes_frag(vw[d].z, vw[d].w);
-#pragma unroll
-                for (int n = 0; n < NR; ++n)
-#pragma unroll
-                    for (int p = 0; p < NP; ++p) o[d][n] = mma(vf, pf[u][n][p], o[d][n]);
-            }
-    }
+    x.clear();
+    const PagedKeys keys{a.k_cache, a.v_cache, a.k_scale, a.v_scale, a.block_table + (size_t)b * a.max_pages,
+                         a.n_pages, a.page, a.HK, hk, kl, a.scale_log2};
+    for (int kb = kb0 + wave; kb < kb1; kb += NW) x.attend(keys, kb, lane);
 
     // join the waves, 16 rows at a time
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
         if (r0 + 16 * n >= rows) break;
-        const float sum = group_add4(l[n]);
-        const float top = sum != sum ? -kNegInf : m[n];  // a NaN sum takes part whatever the other maxima are
+        const float sum = group_add4(x.l[n]);
+        const float top = sum != sum ? -kNegInf : x.m[n];  // a NaN sum takes part whatever the other maxima are
         __syncthreads();
         if (g == 0) {
             sml[wave][lr][0] = top;
             sml[wave][lr][1] = sum;
         }
 #pragma unroll
-        for (int d = 0; d < ND; ++d) *reinterpret_cast<floatx4*>(&so[wave][lr][16 * d + 4 * g]) = o[d][n];
+        for (int d = 0; d < ND; ++d) *reinterpret_cast<floatx4*>(&so[wave][lr][16 * d + 4 * g]) = x.o[d][n];
         __syncthreads();
         for (int i = threadIdx.x; i < 16 * D / 4; i += 64 * NW) {
             const int row = i / (D / 4), d = (i % (D / 4)) * 4, r = r0 + 16 * n + row;

@@ -29,6 +29,9 @@ EXPORTS = (
     "kda_chunk_bwd_workspace", "kda_chunk_bwd", "kda_chunk_bwd_grouped_workspace", "kda_chunk_bwd_grouped",
     "kda_rotary_freqs", "kda_rotary", "kda_attn_fwd_workspace", "kda_attn_fwd", "kda_attn_bwd_workspace",
     "kda_attn_bwd", "kda_cache_append", "kda_attn_step_workspace", "kda_attn_step",
+    "kda_cache_fork", "kda_cache_reserve", "kda_cache_free", "kda_cache_compact", "kda_cache_copy",
+    "kda_attn_shared_workspace", "kda_attn_shared", "kda_state_reorder",
+    "kda_beam_select_workspace", "kda_beam_select",
     "kda_status_string",
 )
 
@@ -110,6 +113,26 @@ def load() -> ctypes.CDLL:
     L.kda_attn_step_workspace.restype = S
     L.kda_attn_step.argtypes = [P] * 9 + [I] * 9 + [F, I, I, P, S, P]
     L.kda_attn_step.restype = I
+    L.kda_cache_fork.argtypes = [P] * 6 + [I] * 7 + [P]
+    L.kda_cache_fork.restype = I
+    L.kda_cache_reserve.argtypes = [P] * 7 + [I] * 5 + [P]
+    L.kda_cache_reserve.restype = I
+    L.kda_cache_free.argtypes = [P] * 4 + [I] * 4 + [P]
+    L.kda_cache_free.restype = I
+    L.kda_cache_compact.argtypes = [P] * 8 + [I] * 3 + [P]
+    L.kda_cache_compact.restype = I
+    L.kda_cache_copy.argtypes = [P] * 11 + [I] * 6 + [P]
+    L.kda_cache_copy.restype = I
+    L.kda_attn_shared_workspace.argtypes = [I] * 7
+    L.kda_attn_shared_workspace.restype = S
+    L.kda_attn_shared.argtypes = [P] * 11 + [I] * 10 + [F, I, I, P, S, P]
+    L.kda_attn_shared.restype = I
+    L.kda_state_reorder.argtypes = [P] * 3 + [I] * 3 + [S, P]
+    L.kda_state_reorder.restype = I
+    L.kda_beam_select_workspace.argtypes = [I] * 5
+    L.kda_beam_select_workspace.restype = S
+    L.kda_beam_select.argtypes = [P] * 6 + [I] * 7 + [P, S, P]
+    L.kda_beam_select.restype = I
     L.kda_status_string.argtypes = [I]
     L.kda_status_string.restype = ctypes.c_char_p
     _lib = L
@@ -680,3 +703,204 @@ def attn_step(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_len, new
             _ptr(cache_len), _ptr(new_len), _ptr(o), n_pages, max_pages, B, Tq, H, HK, D, page, ldq, D ** -0.5 if
             scale is None else scale, window, _dt(dt), *_ws_args(ws))
     return o
+
+
+# ---------------------------------------------------------------- one prompt, several continuations
+
+def _ints(name, shape, given, dev):
+    """The caller's int32 tensor of that shape, or a new one."""
+    if given is None:
+        return torch.empty(shape, dtype=torch.int32, device=dev)
+    _expect(name, given, shape, torch.int32, dev)
+    return given
+
+
+def _table(block_table, refs):
+    """(rows, pages of a row, pages of the cache, device) of a table and the cache's references."""
+    if block_table.dim() != 2 or refs.dim() != 1:
+        raise ValueError("block_table must be [B,max_pages] and refs [n_pages]")
+    dev = block_table.device
+    _expect("block_table", block_table, block_table.shape, torch.int32, dev)
+    _expect("refs", refs, refs.shape, torch.int32, dev)
+    B, width = block_table.shape
+    return B, _int32("block_table's pages", width), _int32("refs' pages", refs.shape[0]), dev
+
+
+def cache_fork(block_table, cache_len, parent, refs, *, page, keep=False, table_out=None, len_out=None):
+    """kda_cache_fork: R requests of K_in sequences (block_table [R*K_in,max_pages],
+    cache_len [R*K_in] int32) become R of K_out, row c of request r sharing the pages
+    of row parent[r,c] (parent [R,K_out] int32, an index within the request; one outside
+    makes an empty row).  refs [n_pages] int32 is updated: the old rows' references are
+    dropped unless `keep`.  Returns (table_out [R*K_out,max_pages], len_out [R*K_out])."""
+    B, width, n_pages, dev = _table(block_table, refs)
+    if parent.dim() != 2 or (parent.shape[0] == 0 and B > 0) or (parent.shape[0] > 0 and B % parent.shape[0] != 0):
+        raise ValueError(f"parent must be [R,K_out] with R a divisor of the table's {B} rows")
+    R, K_out = parent.shape
+    _int32("page", page)
+    _expect("cache_len", cache_len, (B,), torch.int32, dev)
+    _expect("parent", parent, (R, K_out), torch.int32, dev)
+    table_out, len_out = _ints("table_out", (R * K_out, width), table_out, dev), _ints("len_out", (R * K_out,), len_out, dev)
+    _launch("kda_cache_fork", dev, _ptr(block_table), _ptr(cache_len), _ptr(parent), _ptr(table_out), _ptr(len_out),
+            _ptr(refs), _int32("R", R), B // R if R else 0, K_out, width, n_pages, page, 1 if keep else 0)
+    return table_out, len_out
+
+
+def cache_reserve(block_table, cache_len, refs, new_len=None, *, T=1, page, src=None, dst=None, info=None):
+    """kda_cache_reserve: pages for new_len[b] (None: T; at most T) tokens behind
+    cache_len[b], before their cache_append; block_table and refs are updated in place.
+    Returns (src, dst, info): cache_copy's page to copy for each sequence and where to (-1:
+    none), and [entries that got no page, free pages left]."""
+    B, width, n_pages, dev = _table(block_table, refs)
+    _int32("T", T), _int32("page", page)
+    _expect("cache_len", cache_len, (B,), torch.int32, dev)
+    _expect("new_len", new_len, (B,), torch.int32, dev)
+    src, dst, info = _ints("src", (B,), src, dev), _ints("dst", (B,), dst, dev), _ints("info", (2,), info, dev)
+    _launch("kda_cache_reserve", dev, _ptr(block_table), _ptr(refs), _ptr(cache_len), _ptr(new_len), _ptr(src), _ptr(dst),
+            _ptr(info), B, T, width, n_pages, page)
+    return src, dst, info
+
+
+def cache_free(block_table, refs, keep_from=None, keep_to=None, *, page):
+    """kda_cache_free: gives back the pages of each sequence that hold none of its tokens
+    keep_from[b] .. keep_to[b]-1 (int32 [B]; None: 0): all of them without either.
+    block_table and refs are updated in place."""
+    B, width, n_pages, dev = _table(block_table, refs)
+    _int32("page", page)
+    _expect("keep_from", keep_from, (B,), torch.int32, dev)
+    _expect("keep_to", keep_to, (B,), torch.int32, dev)
+    _launch("kda_cache_free", dev, _ptr(block_table), _ptr(refs), _ptr(keep_from), _ptr(keep_to), B, width, n_pages, page)
+
+
+def cache_compact(block_table, refs, *, table_out=None, refs_out=None):
+    """kda_cache_compact: the used pages' new numbers, the first ones of the cache.
+    table_out / refs_out may be block_table / refs (in place).  Returns (table_out, refs_out,
+    remap [n_pages], src, dst [n_pages // 2], info): remap is a page's new number (-1: free),
+    info [copies, used pages].  cache_copy(..., src, dst, count=info) moves the data."""
+    B, width, n_pages, dev = _table(block_table, refs)
+    table_out, refs_out = _ints("table_out", (B, width), table_out, dev), _ints("refs_out", (n_pages,), refs_out, dev)
+    remap, info = _ints("remap", (n_pages,), None, dev), _ints("info", (2,), None, dev)
+    src, dst = _ints("src", (n_pages // 2,), None, dev), _ints("dst", (n_pages // 2,), None, dev)
+    _launch("kda_cache_compact", dev, _ptr(block_table), _ptr(refs), _ptr(table_out), _ptr(refs_out), _ptr(remap),
+            _ptr(src), _ptr(dst), _ptr(info), B, width, n_pages)
+    return table_out, refs_out, remap, src, dst, info
+
+
+def _cache_buffers(k_cache, v_cache, k_scale, v_scale, dev):
+    n_pages, HK, page, D = k_cache.shape
+    _expect("k_cache", k_cache, (n_pages, HK, page, D), torch.uint8, dev)
+    _expect("v_cache", v_cache, (n_pages, HK, D, page), torch.uint8, dev)
+    _expect("k_scale", k_scale, (n_pages, HK), torch.float32, dev)
+    _expect("v_scale", v_scale, (n_pages, HK), torch.float32, dev)
+    return n_pages, HK, page, D
+
+
+def cache_copy(k_cache, v_cache, k_scale, v_scale, src, dst, *, to=None, count=None):
+    """kda_cache_copy: page src[i] of the cache becomes page dst[i] (int32 [n]; -1: none) of
+    the cache `to` (its four buffers; None: the same cache), for the first count[0]
+    entries where count (int32) is given.  No page may be written twice, nor read by
+    the call that writes it."""
+    dev = k_cache.device
+    n_pages, HK, page, D = _cache_buffers(k_cache, v_cache, k_scale, v_scale, dev)
+    n_dst = n_pages
+    if to is not None:
+        n_dst = to[0].shape[0]
+        if _cache_buffers(*to, dev)[1:] != (HK, page, D):
+            raise ValueError("the caches' pages differ in shape")
+    kt, vt, kst, vst = (k_cache, v_cache, k_scale, v_scale) if to is None else to
+    _expect("src", src, (src.numel(),), torch.int32, dev)
+    _expect("dst", dst, (src.numel(),), torch.int32, dev)
+    if count is not None:
+        _expect("count", count, count.shape, torch.int32, dev)
+        if count.numel() < 1:
+            raise ValueError("count holds no number")
+    _launch("kda_cache_copy", dev, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(kt), _ptr(vt),
+            _ptr(kst), _ptr(vst), _ptr(src), _ptr(dst), _ptr(count), _int32("src", src.numel()), n_pages, n_dst, HK, D, page)
+
+
+def attn_shared_workspace_bytes(B, Tq, H, HK, D, n_groups, max_len) -> int:
+    return load().kda_attn_shared_workspace(B, Tq, H, HK, D, n_groups, max_len)
+
+
+def attn_shared(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_len, group_first, prefix_len, new_len=None, *,
+                scale=None, window=0, o=None, workspace=None):
+    """kda_attn_shared: attn_step where the sequences group_first[g] .. group_first[g+1]-1
+    (int32 [n_groups+1]) have their first prefix_len[g] tokens (int32 [n_groups]) in common:
+    their whole pages are read once a group, through its first sequence's row of block_table.
+    Returns o [B,Tq,H,D]."""
+    B, Tq, H, D = q.shape
+    _int32("window", window)
+    dev, dt = q.device, q.dtype
+    n_pages, HK, page, max_pages = _cache_shapes(k_cache, v_cache, k_scale, v_scale, block_table, cache_len, new_len,
+                                                 B, D, dev)
+    n_groups = prefix_len.shape[0]
+    _expect("prefix_len", prefix_len, (n_groups,), torch.int32, dev)
+    _expect("group_first", group_first, (n_groups + 1,), torch.int32, dev)
+    if o is None:
+        o = _like(q)
+    else:
+        _expect("o", o, (B, Tq, H, D), dt, dev)
+    qp, ldq = _rows("q", q)
+    ws = _workspace(attn_shared_workspace_bytes(B, Tq, H, HK, D, n_groups, max_pages * page), workspace, dev)
+    _launch("kda_attn_shared", dev, qp, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
+            _ptr(cache_len), _ptr(new_len), _ptr(group_first), _ptr(prefix_len), _ptr(o), n_groups, n_pages, max_pages, B, Tq,
+            H, HK, D, page, ldq, D ** -0.5 if scale is None else scale, window, _dt(dt), *_ws_args(ws))
+    return o
+
+
+def state_reorder(state, parent, *, out=None):
+    """kda_state_reorder: row c of request r of the result is row parent[r,c] of request
+    r of state [R*K_in, ...] (parent [R,K_out] int32, an index within the request; zeros for
+    one outside).  out=state reorders in place (K_in = K_out, at most 64).  Returns it."""
+    if parent.dim() != 2 or state.dim() < 1:
+        raise ValueError("parent must be [R,K_out] and state have rows")
+    R, K_out = parent.shape
+    dev, rows = state.device, state.shape[0]
+    if (R == 0 and rows > 0) or (R > 0 and rows % R != 0):
+        raise ValueError(f"state's {rows} rows are not those of {R} requests")
+    _expect("parent", parent, (R, K_out), torch.int32, dev)
+    shape = torch.Size((R * K_out, *state.shape[1:]))
+    if out is None:
+        out = torch.empty(shape, dtype=state.dtype, device=dev)
+    else:
+        _expect("out", out, shape, state.dtype, dev)
+    row_bytes = state.element_size()
+    for n in state.shape[1:]:
+        row_bytes *= n
+    _launch("kda_state_reorder", dev, _ptr(state), _ptr(out), _ptr(parent), _int32("R", R), rows // R if R else 0,
+            _int32("K_out", K_out), row_bytes)
+    return out
+
+
+def beam_select_workspace_bytes(R, K, V, M, dtype=torch.bfloat16) -> int:
+    return load().kda_beam_select_workspace(R, K, V, M, _dt(dtype))
+
+
+def beam_select(logits, scores=None, M=None, *, done=None, end=-1, scores_out=None, parent=None, token=None, workspace=None):
+    """kda_beam_select: the M (None: K) best continuations of each request over its K beams
+    and V tokens, by scores [R,K] fp32 (None: 0) + log-softmax of logits [R,K,V] (whose rows
+    may lie further apart than V).  Equal ones are in the order of (beam, token).  done [R,K]
+    uint8: finished beams, which continue with `end` at no cost.  Returns (scores [R,M]
+    fp32, parent [R,M], token [R,M] int32), -infinity, -1, -1 where there are fewer."""
+    if logits.dim() != 3:
+        raise ValueError("logits must be [R,K,V]")
+    R, K, V = logits.shape
+    M = K if M is None else _int32("M", M)
+    _int32("end", end)
+    dev, dt = logits.device, logits.dtype
+    if not logits.is_cuda:
+        raise ValueError("logits must be a device tensor")
+    sr, sk, sv = logits.stride()
+    ld = sk if K > 1 else sr if R > 1 else V
+    if logits.numel() and ((V > 1 and sv != 1) or ld < V or (R > 1 and K > 1 and sr != K * sk)):
+        raise ValueError("the rows of logits must be contiguous and lie one stride apart")
+    _expect("scores", scores, (R, K), torch.float32, dev)
+    _expect("done", done, (R, K), torch.uint8, dev)
+    if scores_out is None:
+        scores_out = torch.empty((R, M), dtype=torch.float32, device=dev)
+    else:
+        _expect("scores_out", scores_out, (R, M), torch.float32, dev)
+    parent, token = _ints("parent", (R, M), parent, dev), _ints("token", (R, M), token, dev)
+    ws = _workspace(beam_select_workspace_bytes(_int32("R", R), _int32("K", K), _int32("V", V), M, dt), workspace, dev)
+    _launch("kda_beam_select", dev, logits.data_ptr(), _ptr(scores), _ptr(done), _ptr(scores_out), _ptr(parent), _ptr(token),
+            R, K, V, M, _int32("the rows' stride", ld), end, _dt(dt), *_ws_args(ws))
+    return scores_out, parent, token

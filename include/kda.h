@@ -533,6 +533,143 @@ kda_status kda_attn_step(const void* q, const void* k_cache, const void* v_cache
                          int H, int HK, int D, int page, int ldq, float scale, int window, kda_dtype dt,
                          void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * One prompt continued several times (beams, parallel samples): sequences share the
+ * pages of what they have in common, attend over it once, and are reordered as a
+ * selection says.
+ *
+ * Pages.  refs [n_pages] int: how many table entries name a page, summed over every
+ * table (and other holder) of the cache; 0 is a free page.  A table entry outside
+ * 0 .. n_pages-1 names none; tables [B,max_pages], lengths and pages as for
+ * kda_cache_append.  The calls below keep refs in step with the tables that they
+ * are given.  One set of tables serves the caches of all layers: bookkeeping is one
+ * call, and its list of copies (src, dst: page numbers, -1 in entries without one) is
+ * given to kda_cache_copy for each layer.  Which page is taken, and who keeps a shared
+ * one, follows the order of (sequence, page), so results do not vary from run to run.
+ * Sizes: B * max_pages below 2^30, n_pages up to 2^30; page in {16, 32, 64, 128}. */
+
+/* Sequences that follow their parents: R requests of K_in sequences become R of K_out.
+ * Row c of request r gets the pages that hold tokens of row parent[r][c] (an index
+ * within the request; one outside 0 .. K_in-1 makes an empty row), -1 behind them,
+ * and its length.  The references of all of its entries are counted; those of the
+ * old rows are dropped unless `keep` (the prompt stays beside its samples).  Tokens
+ * are not copied: kda_cache_reserve gives every sequence a page of its own to write to.
+ *   table [R*K_in,max_pages], cache_len [R*K_in], parent [R,K_out] int;
+ *   table_out [R*K_out,max_pages], len_out [R*K_out] int; refs [n_pages], updated.
+ * K_in, K_out up to 1024.  Outputs may overlap no other buffer (KDA_ERR_SHAPE).
+ * Errors: KDA_ERR_SHAPE, KDA_ERR_NULL, KDA_ERR_ALIGN, KDA_ERR_HIP. */
+kda_status kda_cache_fork(const int* table, const int* cache_len, const int* parent, int* table_out,
+                          int* len_out, int* refs, int R, int K_in, int K_out, int max_pages,
+                          int n_pages, int page, int keep, hipStream_t stream);
+
+/* Room for new_len[b] (NULL: T) tokens behind the cache_len[b] of each sequence,
+ * before their kda_cache_append.  Of the pages that these tokens touch,
+ *   - one that is missing becomes the lowest free page (a page whose older tokens are
+ *     missing stays missing: appends drop its tokens);
+ *   - one that others hold too (refs > 1) is left to them for the lowest free page, into
+ *     which it has to be copied if it holds older tokens; where nobody outside the
+ *     call's sequences holds it, the last of them keeps it.
+ * A page that has a number and one reference is left as it is, so reserving again, or for
+ * more tokens, is safe.  Entries for which no page is free become -1 (a shared page is
+ * given up: this sequence's tokens in it are then missing).
+ *   table [B,max_pages], refs [n_pages]: updated;  cache_len, new_len [B] int;
+ *   src, dst [B] int: the page to copy for each sequence and where to;
+ *   info [2] int: entries that got no page, and free pages left.
+ * Errors as kda_cache_fork. */
+kda_status kda_cache_reserve(int* table, int* refs, const int* cache_len, const int* new_len,
+                             int* src, int* dst, int* info, int B, int T, int max_pages, int n_pages,
+                             int page, hipStream_t stream);
+
+/* Gives back the pages of each sequence that hold none of its tokens
+ * keep_from[b] .. keep_to[b]-1 (NULL: 0): all of them without either (the sequence
+ * ends), those behind accepted tokens (drafted ones are dropped), those that a
+ * window has passed.  Their entries become -1; cache_len is the caller's.
+ *   table [B,max_pages], refs [n_pages]: updated;  keep_from, keep_to [B] int.
+ * Errors as kda_cache_fork. */
+kda_status kda_cache_free(int* table, int* refs, const int* keep_from, const int* keep_to,
+                          int B, int max_pages, int n_pages, int page, hipStream_t stream);
+
+/* Moves the pages in use to the front of the cache, U of them: the i-th used page from
+ * U on goes to the i-th free page below U (both in ascending order), the others stay.
+ *   table [B,max_pages], refs [n_pages] -> table_out, refs_out (which may be table and
+ *   refs themselves);  remap [n_pages] int: a page's new number, -1 for a free one, for
+ *   tables that other holders have;  src, dst [n_pages / 2] int: the copies, -1 behind
+ *   the last;  info [2] int: their number (the `count` of kda_cache_copy), and U.
+ * Entries that name a free page become -1.  Errors as kda_cache_fork. */
+kda_status kda_cache_compact(const int* table, const int* refs, int* table_out, int* refs_out,
+                             int* remap, int* src, int* dst, int* info, int B, int max_pages,
+                             int n_pages, hipStream_t stream);
+
+/* Copies pages, codes and scales: page src[i] of one cache becomes page dst[i] of another
+ * (or of the same: all four pointers equal) for i < n, and i < count[0] if count is not
+ * NULL; entries that name no page are passed over.  No page may be written twice by a
+ * call, nor read by the call that writes it.
+ *   caches as for kda_cache_append, of n_src and n_dst pages;  src, dst [n], count [1] int.
+ * HK * page * D below 2^31.  Different caches may not overlap (KDA_ERR_SHAPE).  Errors as
+ * kda_cache_fork. */
+kda_status kda_cache_copy(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                          void* k_to, void* v_to, float* k_scale_to, float* v_scale_to,
+                          const int* src, const int* dst, const int* count, int n, int n_src, int n_dst,
+                          int HK, int D, int page, hipStream_t stream);
+
+/* kda_attn_step for groups of sequences that have a common prefix, which is read once a
+ * group instead of once a sequence: group g is the sequences group_first[g] ..
+ * group_first[g+1]-1, whose first prefix_len[g] tokens are the same.  Their whole pages
+ * are read through the row of the group's first sequence; the page in which a prefix
+ * ends, of which every sequence has a copy (whose codes move as its scale grows), and
+ * what follows through each sequence's own.  The result is that of kda_attn_step up to
+ * the order of its sums.  Everything else as there; a sequence of no group has no prefix,
+ * one whose length is below the prefix sees no further than its length.
+ *   group_first [n_groups+1] int, not descending (values outside 0 .. B are clamped);
+ *   prefix_len [n_groups] int (clamped to the table).
+ *   workspace  kda_attn_shared_workspace(B, Tq, H, HK, D, n_groups, max_pages * page)
+ *        bytes, 256-byte aligned: partial results of prefixes and of own keys.
+ * Sizes as there, and B * Tq * (H / HK) up to 2^29; below 2^24 workgroups (32 rows each
+ * for groups and sequences).  Errors as kda_attn_step. */
+size_t kda_attn_shared_workspace(int B, int Tq, int H, int HK, int D, int n_groups, int max_len);
+kda_status kda_attn_shared(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                           const float* v_scale, const int* block_table, const int* cache_len,
+                           const int* new_len, const int* group_first, const int* prefix_len, void* o,
+                           int n_groups, int n_pages, int max_pages, int B, int Tq, int H, int HK, int D,
+                           int page, int ldq, float scale, int window, kda_dtype dt,
+                           void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* States that follow their parents: row c of request r of `out` becomes row
+ * parent[r][c] (an index within the request) of request r of `state`, zeros if that is
+ * outside 0 .. K_in-1.  For the states [B,H,Dk,Dv] of kda_step and the windows
+ * [B,3,C] of kda_short_conv; any row of bytes.
+ *   state [R*K_in] rows, out [R*K_out] rows of row_bytes bytes (a multiple of 16), parent
+ *   [R,K_out] int.  out may be state itself where K_in = K_out <= 64: rows whose parent
+ *   they are themselves are then not touched.  No other overlap (KDA_ERR_SHAPE).
+ * Sizes: R * K up to 2^24, and below 2^24 pieces of 2 KB (in place, all rows of a request
+ * together) or 16 KB of a row.
+ * Errors: KDA_ERR_SHAPE, KDA_ERR_NULL, KDA_ERR_ALIGN (row_bytes too), KDA_ERR_HIP. */
+kda_status kda_state_reorder(const void* state, void* out, const int* parent, int R, int K_in, int K_out,
+                             size_t row_bytes, hipStream_t stream);
+
+/* Beam search's selection: over the K beams of a request and the V tokens,
+ *   s(b,w) = scores[b] + x_bw - ln sum_w' exp(x_bw'),
+ * the M largest, largest first, equal ones in the order of (b, w).
+ *   logits   [R,K,V] dtype dt, rows ld elements apart (0: V); any ld >= V.
+ *            Within a beam the order is that of the logits.
+ *   scores   [R,K] fp32, or NULL (zeros).  A beam whose score is not finite has no
+ *            continuation (the unused beams of a first step: -infinity).
+ *   done     [R,K] bytes or NULL: a finished beam (not 0) has one continuation, `end`
+ *            (a token, 0 .. V-1), with its score unchanged; its logits are not read.
+ *   scores_out [R,M] fp32, parent, token [R,M] int.  Where fewer than M continuations
+ *            have a score above -infinity the rest is -infinity, -1, -1.
+ * Logits of -infinity are no continuations; a beam with a NaN or +infinity has none.
+ * Continuations are compared in 64 bits (lse to about 1e-7) and their scores rounded
+ * once.  K, M up to 64, V up to 2^30, R * K below 2^18.
+ *   workspace  kda_beam_select_workspace bytes, 256-byte aligned.
+ * Outputs may overlap no other buffer.  Errors: KDA_ERR_DTYPE, KDA_ERR_SHAPE,
+ * KDA_ERR_NULL, KDA_ERR_ALIGN, KDA_ERR_WORKSPACE, KDA_ERR_HIP. */
+size_t kda_beam_select_workspace(int R, int K, int V, int M, kda_dtype dt);
+kda_status kda_beam_select(const void* logits, const float* scores, const unsigned char* done,
+                           float* scores_out, int* parent, int* token, int R, int K, int V, int M,
+                           int ld, int end, kda_dtype dt, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream);
+
 /* Static description of a status code (never NULL). */
 const char* kda_status_string(kda_status s);
 

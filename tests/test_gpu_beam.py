@@ -1,0 +1,217 @@
+"""GPU parity of the selection over beams and vocabulary (parents and tokens equal the
+oracle's, scores to fp32) and of states that follow their parents (byte for byte)."""
+
+import numpy as np
+import pytest
+import torch
+
+from gated_delta_rule_82_amd import kda
+from oracle import branch_oracle as ora
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+NEG = float("-inf")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    assert torch.cuda.is_available(), "GPU tests need a ROCm device"
+    kda.load()
+    yield
+    torch.cuda.synchronize()
+
+
+def logits_of(R, K, V, dtype, seed, std=3.0):
+    return (torch.randn(R, K, V, generator=torch.Generator().manual_seed(seed)) * std).to(dtype)
+
+
+def scores_of(R, K, seed):
+    return -10.0 * torch.rand(R, K, generator=torch.Generator().manual_seed(seed))
+
+
+def check(x, s, M, done=None, end=-1, given=None, tol=None):
+    """x, s, done on the host.  The score is rounded once (2^-24 of it), lse is off by at most 1e-6 (fp32
+    exponentials of 2^-22 each, sums of at most 2^9 of them a thread, each addition 2^-24: 2^-22 + 2^9 2^-24 is a
+    bound of 3e-5 that no sum of rounding errors of both signs comes near; 1e-6 holds for their root)."""
+    got = kda.beam_select(x.cuda() if given is None else given, None if s is None else s.cuda(), M,
+                          done=None if done is None else done.cuda(), end=end)
+    torch.cuda.synchronize()
+    want = ora.beam_select(x.double().numpy(), None if s is None else s.numpy(), M, None if done is None else done.numpy(), end)
+    assert np.array_equal(got[1].cpu().numpy(), want[1]) and np.array_equal(got[2].cpu().numpy(), want[2])
+    a, w = got[0].cpu().double().numpy(), want[0]
+    assert np.array_equal(np.isinf(a), np.isinf(w))
+    fin = np.isfinite(w)
+    assert np.all(np.abs(a[fin] - w[fin]) <= 1e-6 + 2.0 ** -23 * np.abs(w[fin])), np.abs(a[fin] - w[fin]).max()
+    return got
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("R,K,V,M", [(1, 1, 1, 1), (1, 1, 5, 7), (2, 3, 7, 6), (1, 4, 100, 8), (3, 2, 4095, 4), (2, 5, 4097, 5),
+                                     (1, 64, 1001, 64), (5, 8, 16384, 16), (1, 3, 70001, 64), (2, 2, 131072, 1), (64, 1, 3000, 2),
+                                     (1, 1, 400000, 10)])
+def test_select(dtype, R, K, V, M):
+    check(logits_of(R, K, V, dtype, V + K), scores_of(R, K, M), M)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V", [300, 20001])
+@pytest.mark.parametrize("M", [1, 3, 17, 64])
+def test_select_equal_values(dtype, V, M):
+    """One value everywhere, few values, two equal beams: the lowest (beam, token) first."""
+    check(torch.zeros(2, 3, V, dtype=dtype), torch.zeros(2, 3), M)
+    x = torch.zeros(1, 2, V, dtype=dtype)
+    x[:, :, V // 2:] = 1.0
+    check(x, None, M)
+    x = torch.randint(0, 3, (2, 4, V), generator=torch.Generator().manual_seed(V)).to(dtype)
+    x[:, 2] = x[:, 1]
+    check(x, torch.tensor([[-1.0, -0.5, -0.5, -9.0]] * 2), M)
+    x = torch.full((1, 2, V), 0.0, dtype=dtype)       # plus and minus zero are equal
+    x[:, :, ::2] = -0.0
+    check(x, None, M)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("M", [1, 8, 64])
+@pytest.mark.parametrize("order", ["rising", "falling", "blocks"])
+def test_select_ordered_rows(dtype, M, order):
+    """Rows in which one thread, or one end, holds everything that is large."""
+    V = 33000
+    x = torch.arange(V).float() / 64.0
+    if order == "falling":
+        x = x.flip(0)
+    if order == "blocks":     # every 2048th (1024th) block of 8 (4) elements lies far above the others
+        x = x + 3000.0 * ((torch.arange(V) // 8) % 256 == 7)
+    check(x.to(dtype).view(1, 1, V).repeat(1, 2, 1), torch.tensor([[-1.0, -2.5]]), M)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("fill", [NEG, "lowest"])
+@pytest.mark.parametrize("allowed", [0, 1, 5, 40])
+def test_select_masked(dtype, fill, allowed):
+    V, M = 20011, 8
+    x = torch.full((2, 3, V), torch.finfo(dtype).min if fill == "lowest" else fill, dtype=dtype)
+    g = torch.Generator().manual_seed(allowed)
+    for k in range(3):
+        at = torch.randperm(V, generator=g)[:allowed]
+        x[:, k, at] = torch.randn(allowed, generator=g).to(dtype)
+    check(x, scores_of(2, 3, 1), M)
+
+
+def test_select_values_that_are_no_numbers():
+    V, M = 9000, 6
+    x = logits_of(2, 6, V, F32, 1)
+    x[0, 0, 5], x[0, 1, 7000], x[0, 2, 3] = float("nan"), float("inf"), NEG
+    x[0, 3] = float("nan")
+    x[0, 4] = NEG
+    s = scores_of(2, 6, 2)
+    s[1, 0], s[1, 1], s[1, 2] = NEG, float("nan"), float("inf")
+    check(x, s, M)
+    check(torch.full((1, 2, V), float("nan")), None, M)
+    check(logits_of(1, 4, V, BF16, 3), torch.tensor([[0.0, NEG, NEG, NEG]]), 4)     # a first step
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_select_finished_beams(dtype):
+    R, K, V, M = 3, 4, 5003, 8
+    x, s = logits_of(R, K, V, dtype, 5), scores_of(R, K, 6)
+    done = torch.tensor([[0, 1, 0, 1], [1, 1, 1, 1], [0, 0, 0, 0]], dtype=torch.uint8)
+    x[0, 1] = float("nan")                 # not read
+    s[1, 2] = NEG
+    got = check(x, s, M, done, 2)
+    assert got[2][1].tolist() == [2, 2, 2] + [-1] * 5
+    check(x, s, M, done * 255, V - 1)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_select_rows_apart(dtype):
+    """A vocabulary padded to a longer row; what lies behind it may be anything.  Rows of odd length start
+    at every alignment."""
+    x = logits_of(2, 3, 5000, dtype, 7)
+    x[:, :, 4001:] = float("nan")
+    dev = x.cuda()
+    check(x[:, :, :4001].contiguous(), scores_of(2, 3, 8), 5, given=dev[:, :, :4001])
+    with pytest.raises(ValueError):
+        kda.beam_select(dev[:, :, ::2])
+    with pytest.raises(ValueError):
+        kda.beam_select(dev[:, :2])
+
+
+def test_select_from_extreme_logits():
+    """Logits far apart, and all large: lse neither overflows nor loses the others."""
+    x = logits_of(1, 3, 3000, F32, 9)
+    x[0, 0] += 1e4
+    x[0, 1] *= 30.0
+    x[0, 2, 17] = 3e38
+    check(x, scores_of(1, 3, 1), 5)
+
+
+def test_select_does_not_vary():
+    x, s = logits_of(4, 8, 50257, BF16, 11).cuda(), scores_of(4, 8, 12).cuda()
+    first = kda.beam_select(x, s, 16)
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(first, kda.beam_select(x, s, 16)))
+
+
+def test_select_refusals():
+    x = torch.zeros(2, 3, 50, device="cuda")
+    for bad in (dict(M=0), dict(M=65), dict(M=3, done=torch.zeros(2, 3, dtype=torch.uint8, device="cuda")),
+                dict(M=3, done=torch.zeros(2, 3, dtype=torch.uint8, device="cuda"), end=50)):
+        with pytest.raises(kda.KDAError):
+            kda.beam_select(x, **bad)
+    with pytest.raises(kda.KDAError):
+        kda.beam_select(torch.zeros(1, 65, 10, device="cuda"))
+    with pytest.raises(TypeError):
+        kda.beam_select(x.half())
+    with pytest.raises(TypeError):
+        kda.beam_select(x, done=torch.zeros(2, 3, device="cuda"))
+    with pytest.raises(ValueError):
+        kda.beam_select(x, torch.zeros(3, 2, device="cuda"))
+    with pytest.raises(ValueError):
+        kda.beam_select(x[0])
+
+
+@pytest.mark.parametrize("K", [1, 2, 4, 5, 8, 13, 16, 31, 32, 33, 64])
+@pytest.mark.parametrize("shape,dtype", [((8,), BF16), ((3, 5, 8), BF16), ((2, 16, 32), F32), ((7, 100, 4), F32)])
+def test_reorder_in_place(K, shape, dtype):
+    rng = np.random.default_rng(K)
+    R = 3
+    s = torch.randn(R * K, *shape, generator=torch.Generator().manual_seed(K)).to(dtype)
+    parent = rng.integers(-1, K + 1, (R, K))
+    parent[0] = rng.permutation(K)
+    if K > 1:
+        parent[1, :2] = [1, 0]
+    want = ora.state_reorder(s.float().numpy(), parent)
+    d, p = s.cuda(), torch.from_numpy(parent).to(torch.int32).cuda()
+    out = kda.state_reorder(d, p)
+    again = kda.state_reorder(d, p, out=d)
+    torch.cuda.synchronize()
+    assert again is d and np.array_equal(out.float().cpu().numpy(), want) and np.array_equal(d.float().cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("K_in,K_out", [(1, 8), (3, 1), (4, 70), (0, 2), (5, 0)])
+def test_reorder_to_other_rows(K_in, K_out):
+    rng = np.random.default_rng(K_out)
+    R = 2
+    s = torch.randn(R * K_in, 3, 5000, generator=torch.Generator().manual_seed(1))
+    parent = rng.integers(-1, K_in + 1, (R, K_out))
+    got = kda.state_reorder(s.cuda(), torch.from_numpy(parent).to(torch.int32).cuda())
+    torch.cuda.synchronize()
+    assert np.array_equal(got.cpu().numpy(), ora.state_reorder(s.numpy(), parent))
+
+
+def test_reorder_refusals():
+    s = torch.zeros(6, 16, device="cuda")
+    p = torch.zeros(2, 3, dtype=torch.int32, device="cuda")
+    with pytest.raises(kda.KDAError):
+        kda.state_reorder(torch.zeros(6, 3, device="cuda"), p)                      # 12 bytes a row
+    with pytest.raises(kda.KDAError):
+        kda.state_reorder(s[:4], p, out=s)                                          # overlaps, two rows become three
+    with pytest.raises(kda.KDAError):                                               # more rows than fit in place
+        kda.state_reorder(big := torch.zeros(65, 16, device="cuda"), torch.zeros(1, 65, dtype=torch.int32, device="cuda"), out=big)
+    with pytest.raises(ValueError):
+        kda.state_reorder(s[:5], p)
+    with pytest.raises(ValueError):
+        kda.state_reorder(s, p, out=torch.zeros(6, 15, device="cuda"))
+    with pytest.raises(TypeError):
+        kda.state_reorder(s, p.long())

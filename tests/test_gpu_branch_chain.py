@@ -1,0 +1,143 @@
+"""The operators together, as a beam search runs them over a small stack of one KDA layer and one layer
+of softmax attention: select, states and tables follow the parents, room for a token, the tail
+pages' copies, append, attention with the prompt in common.  At the end each beam's tokens are run
+again by themselves, from an empty state and cache and without sharing: the sums of their
+log-probabilities are the beams' scores."""
+
+import numpy as np
+import pytest
+import torch
+
+from gated_delta_rule_82_amd import kda
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    assert torch.cuda.is_available(), "GPU tests need a ROCm device"
+    kda.load()
+    yield
+    torch.cuda.synchronize()
+
+
+V, C, HK_, H, D, PAGE, WIDTH = 101, 64, 2, 4, 32, 16, 6
+
+
+class Stack:
+    """Weights of the two layers; all in fp32."""
+
+    def __init__(self, seed):
+        g = torch.Generator().manual_seed(seed)
+        w = lambda *n: torch.randn(*n, generator=g).cuda() * n[0] ** -0.5  # noqa: E731
+        self.embed = torch.randn(V, C, generator=g).cuda()
+        self.kda_in, self.beta_in, self.kda_out = w(C, 4 * 2 * 32), w(C, 2), w(2 * 32, C)
+        self.A_log = torch.zeros(2, device="cuda")
+        self.attn_in, self.attn_out, self.head = w(C, (H + 2 * HK_) * D), w(H * D, C), w(C, V) * 2
+        self.freqs, self.turn = kda.rotary_freqs(D)
+
+    def step(self, tokens, S, cache, table, lens, groups=None):
+        """Logits [n,V] of one more token of each sequence; S and the cache are updated."""
+        x = self.embed[tokens.long()]
+        n = x.shape[0]
+        q, k, v, z = (x @ self.kda_in).view(n, 4, 2, 32).unbind(1)
+        y = kda.step(*(t.contiguous() for t in (q, k, v, z)), (x @ self.beta_in).contiguous(), self.A_log, S)
+        x = x + y.reshape(n, -1) @ self.kda_out
+        p = (x @ self.attn_in).view(n, 1, H + 2 * HK_, D)
+        q, k = kda.rotary(p[:, :, :H], p[:, :, H:H + HK_], self.freqs, lens.view(n, 1), scale=self.turn)
+        kda.cache_append(k, p[:, :, H + HK_:], *cache, table, lens)
+        o = kda.attn_step(q, *cache, table, lens) if groups is None else kda.attn_shared(q, *cache, table, lens, *groups)
+        return (x + o.reshape(n, -1) @ self.attn_out) @ self.head
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("R,K", [(1, 4), (3, 3)])
+def test_beam_search(R, K):
+    net, B, steps, end = Stack(R), R * K, 14, 7
+    prompts = [[(13 * r + 5 * i) % V for i in range(n)] for r, n in zip(range(R), (21, 5, 32))]
+    n_pages = R * 2 + B * 3
+    cache, refs = kda.new_cache(n_pages, HK_, D, PAGE), torch.zeros(n_pages, dtype=torch.int32, device="cuda")
+    table, lens = torch.full((R, WIDTH), -1, dtype=torch.int32, device="cuda"), ints([0] * R)
+    S = torch.zeros(R, 2, 32, 32, device="cuda")
+    # the prompts, token by token (shorter ones wait, their states aside)
+    logits = torch.zeros(R, V, device="cuda")
+    for i in range(max(map(len, prompts))):
+        at = [r for r in range(R) if i < len(prompts[r])]
+        rows = torch.tensor(at, device="cuda")
+        t, n, s = table[rows].contiguous(), lens[rows].contiguous(), S[rows].contiguous()
+        kda.cache_reserve(t, n, refs, page=PAGE)
+        logits[rows] = net.step(ints([prompts[r][i] for r in at]), s, cache, t, n)
+        table[rows], S[rows], lens[rows] = t, s, n + 1
+    # one beam of each request continues at first
+    score, parent, token = kda.beam_select(logits.view(R, 1, V), None, K)
+    table, lens = kda.cache_fork(table, lens, parent, refs, page=PAGE)
+    S = kda.state_reorder(S, parent)
+    words = [[[int(w)] for w in row] for row in token.cpu()]
+    first, prefix = ints([K * r for r in range(R + 1)]), lens[::K].contiguous()
+    for _ in range(steps):
+        done = (token == end).to(torch.uint8)
+        src, dst, info = kda.cache_reserve(table, lens, refs, page=PAGE)
+        kda.cache_copy(*cache, src, dst)
+        logits = net.step(token.view(B), S, cache, table, lens, (first, prefix)).view(R, K, V)
+        lens = lens + 1
+        score, parent, token = kda.beam_select(logits, score, K, done=done, end=end)
+        table, lens = kda.cache_fork(table, lens, parent, refs, page=PAGE)
+        kda.state_reorder(S, parent, out=S)
+        p, w = parent.cpu().tolist(), token.cpu().tolist()
+        words = [[words[r][p[r][k]] + [w[r][k]] for k in range(K)] for r in range(R)]
+        assert info[0].item() == 0
+        held = table[table >= 0].cpu().numpy()
+        assert np.array_equal(refs.cpu().numpy(), np.bincount(held, minlength=n_pages))   # nothing lost, nothing held twice
+    assert len({tuple(x) for row in words for x in row}) == B
+    kda.cache_free(table, refs, page=PAGE)
+    torch.cuda.synchronize()
+    assert int(refs.abs().sum()) == 0
+
+    # each beam alone
+    for r in range(R):
+        for k in range(K):
+            alone = kda.new_cache(WIDTH, HK_, D, PAGE)
+            S1, t1 = torch.zeros(1, 2, 32, 32, device="cuda"), torch.arange(WIDTH, dtype=torch.int32, device="cuda").view(1, WIDTH)
+            total, ended = 0.0, False
+            seq = prompts[r] + words[r][k]
+            for i, w in enumerate(seq[:-1]):
+                x = net.step(ints([w]), S1, alone, t1, ints([i])).double().cpu()[0]
+                if i + 1 >= len(prompts[r]) and not ended:
+                    total += float(torch.log_softmax(x, 0)[seq[i + 1]])
+                    ended = seq[i + 1] == end
+            # what differs is the order of the attention's sums and the rounding of the matrix products around
+            # it (2^-24 of sums of at most 128 terms of size one, a few of them in a row): 1e-5 a logit, 15 steps
+            assert abs(total - float(score[r, k])) <= 15 * 2 * 1e-5 + 2.0 ** -22 * abs(total)
+
+
+def test_drafted_tokens_are_taken_back():
+    """Four drafted tokens of shared prompts, of which some are accepted: their pages go back, and the next
+    tokens find the cache as if the others had never been there."""
+    rng = np.random.default_rng(0)
+    K, T, n0 = 3, 4, 30
+    cache, refs = kda.new_cache(12, 2, 32, PAGE), torch.zeros(12, dtype=torch.int32, device="cuda")
+    g = torch.Generator().manual_seed(1)
+    r = lambda *n: torch.randn(*n, generator=g).cuda()  # noqa: E731
+    table, lens = torch.full((1, WIDTH), -1, dtype=torch.int32, device="cuda"), ints([0])
+    kda.cache_reserve(table, lens, refs, T=n0, page=PAGE)
+    kda.cache_append(r(1, n0, 2, 32), r(1, n0, 2, 32), *cache, table, lens)
+    table, lens = kda.cache_fork(table, ints([n0]), ints([[0] * K]), refs, page=PAGE)
+    groups = (ints([0, K]), ints([n0]))
+    for _ in range(5):
+        src, dst, info = kda.cache_reserve(table, lens, refs, T=T, page=PAGE)
+        kda.cache_copy(*cache, src, dst)
+        k, v, q = r(K, T, 2, 32), r(K, T, 2, 32), r(K, T, 4, 32)
+        kda.cache_append(k, v, *cache, table, lens)
+        a = kda.attn_shared(q, *cache, table, lens, *groups)
+        b = kda.attn_step(q, *cache, table, lens)
+        torch.cuda.synchronize()
+        assert info[0].item() == 0
+        # two sums of at most 64 terms of values below 8: 64 * 2^-24 * 8 and the scores' own rounding
+        assert float((a - b).abs().max()) <= 1e-4
+        lens = lens + ints(rng.integers(0, T + 1, K))
+        kda.cache_free(table, refs, None, lens, page=PAGE)
+        held = table[table >= 0].cpu().numpy()
+        assert np.array_equal(refs.cpu().numpy(), np.bincount(held, minlength=12))

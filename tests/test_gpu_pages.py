@@ -1,0 +1,341 @@
+"""GPU parity of the page operators: tables, references and lists equal the oracle's, copies
+are byte for byte, and what a captured loop of them leaves is what the eager one does."""
+
+import numpy as np
+import pytest
+import torch
+
+from gated_delta_rule_82_amd import kda
+from oracle import branch_oracle as ora
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    assert torch.cuda.is_available(), "GPU tests need a ROCm device"
+    kda.load()
+    yield
+    torch.cuda.synchronize()
+
+
+def ints(x):
+    return None if x is None else torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def host(t):
+    return t.cpu().numpy()
+
+
+def same(got, want, what):
+    got = host(got)
+    assert got.shape == np.shape(want) and np.array_equal(got, want), (what, got, want)
+
+
+def pages_of(rng, lens, width, n_pages, page):
+    """A table whose rows hold lens tokens in pages of their own, and its references."""
+    order, at = rng.permutation(n_pages), 0
+    table = np.full((len(lens), width), -1, np.int64)
+    refs = np.zeros(n_pages, np.int64)
+    for b, n in enumerate(lens):
+        k = -(-n // page)
+        table[b, :k] = order[at:at + k]
+        at += k
+    refs[table[table >= 0]] = 1
+    return table, refs
+
+
+@pytest.mark.parametrize("R,K_in,K_out,keep", [(1, 1, 4, True), (3, 4, 4, False), (2, 5, 3, False), (4, 2, 7, True), (1, 300, 200, False)])
+@pytest.mark.parametrize("page", [16, 128])
+def test_fork(R, K_in, K_out, keep, page):
+    rng = np.random.default_rng(R + K_in)
+    width = 6
+    lens = rng.integers(0, page * width + 1, R * K_in)
+    lens[0] = page * 2
+    table, refs = pages_of(rng, lens, width, R * K_in * width + 5, page)
+    table[-1, -1] = 1 << 30                      # entries that name no page
+    parent = rng.integers(-1, K_in + 1, (R, K_out))
+    want = ora.fork(table, lens, parent, refs, page, keep)
+    refs_d = ints(refs)
+    t, n = kda.cache_fork(ints(table), ints(lens), ints(parent), refs_d, page=page, keep=keep)
+    torch.cuda.synchronize()
+    for got, w, what in zip((t, n, refs_d), want, ("table", "len", "refs")):
+        same(got, w, what)
+
+
+def test_fork_of_lengths_that_are_no_lengths():
+    """Negative ones count as zero; past the table's end a row has all of its pages."""
+    table, refs = np.array([[0, 1], [2, 3], [4, 5]]), np.array([1] * 6)
+    lens, parent = [-5, 1000, 17], [[0, 1, 2, 1]]
+    refs_d = ints(refs)
+    t, n = kda.cache_fork(ints(table), ints(lens), ints(parent), refs_d, page=16)
+    torch.cuda.synchronize()
+    for got, w in zip((t, n, refs_d), ora.fork(table, lens, parent, refs, 16)):
+        same(got, w, "fork")
+
+
+def reserve(table, lens, refs, T, page, new_len=None):
+    t, r = ints(table), ints(refs)
+    src, dst, info = kda.cache_reserve(t, ints(lens), r, ints(new_len), T=T, page=page)
+    torch.cuda.synchronize()
+    want = ora.reserve(table, lens, refs, T, page, new_len)
+    for got, w, what in zip((t, r, src, dst, info), want, ("table", "refs", "src", "dst", "info")):
+        same(got, w, what)
+    return want
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("T", [0, 1, 16, 70])
+def test_reserve(page, T):
+    rng = np.random.default_rng(page + T)
+    width = 8
+    lens = [0, 1, page - 1, page, page + 1, 3 * page, page * width - 1, page * width, page * width + 3]
+    table, refs = pages_of(rng, np.minimum(lens, page * width), width, 60, page)
+    # shared rows: twice, three times, and with a holder outside the call
+    table, lens, refs = ora.fork(table, lens, [[0, 1, 2, 2, 2, 3, 4, 4, 5, 6, 7, 8, 1, 99]], refs, page)
+    refs[table[6, 0]] += 1
+    n_free = int((refs == 0).sum())
+    table, refs, _, _, info = reserve(table, lens, refs, T, page)
+    assert info[1] <= n_free
+    # reserving again, and for some sequences only
+    table, refs, src, dst, _ = reserve(table, lens, refs, T, page)
+    assert (src == -1).all()
+    reserve(table, lens, refs, 2 * T + 1, page, rng.integers(-1, 2 * T + 3, len(lens)))
+
+
+def test_reserve_runs_out_of_pages():
+    page, width = 16, 4
+    rng = np.random.default_rng(4)
+    table, refs = pages_of(rng, [20, 33, 5], width, 7, page)          # 2 + 3 + 1 of 7
+    table, lens, refs = ora.fork(table, [20, 33, 5], [[0, 0, 1, 1, 1, 2, 2]], refs, page)
+    _, refs, src, dst, info = reserve(table, lens, refs, 14, page)
+    assert info[0] > 0 and info[1] == 0
+    reserve(np.full((3, 2), -1), [0, 16, 40], np.ones(5, int), 1, page)          # none free at all
+    reserve(np.full((3, 2), -1), [0, 16, 40], np.zeros(0, int), 1, page)         # no pages
+    reserve(np.full((2, 0), -1), [0, 16], np.zeros(3, int), 1, page)             # no columns
+    reserve(np.full((0, 3), -1), [], np.zeros(3, int), 1, page)                  # no sequences
+
+
+def test_reserve_leaves_a_page_whose_tokens_are_missing():
+    table = np.array([[-1, -1, -1], [9, -1, -1], [1 << 30, 2, -1]])
+    reserve(table, [5, 5, 20], np.array([0, 0, 1, 0]), 20, 16)
+
+
+@pytest.mark.parametrize("n_pages", [1, 3, 4, 5, 4095, 4097, 30000])
+def test_reserve_walks_to_the_free_pages(n_pages):
+    """More free pages than a ring holds, and few of them at the end of a large cache."""
+    rng = np.random.default_rng(n_pages)
+    refs = np.zeros(n_pages, np.int64)
+    reserve(np.full((3, 4), -1), [0, 0, 0], refs, 50, 16)
+    refs[:] = rng.integers(1, 4, n_pages)
+    refs[max(0, n_pages - 7):] = 0
+    reserve(np.full((3, 4), -1), [0, 0, 0], refs, 50, 16)
+    reserve(np.full((2500, 2), -1), np.full(2500, 0), (rng.random(n_pages) < 0.7).astype(int), 17, 16)
+
+
+def test_reserve_with_many_holders():
+    """More claims of shared pages than one step of the workgroup takes, across its border too."""
+    rng = np.random.default_rng(8)
+    page, width = 16, 2
+    table, refs = pages_of(rng, [5, 20, 16, 31], width, 4000, page)
+    parent = rng.integers(0, 4, (1, 1000))
+    table, lens, refs = ora.fork(table, [5, 20, 16, 31], parent, refs, page)
+    more, _, refs = ora.fork(table[:500], lens[:500], rng.integers(0, 500, (1, 700)), refs, page, keep=True)
+    both, n = np.concatenate((table, more)), np.concatenate((lens, lens[:700]))
+    reserve(both, n, refs, 3, page)
+
+
+@pytest.mark.parametrize("page", [16, 64])
+def test_free(page):
+    rng = np.random.default_rng(page)
+    B, width = 9, 5
+    table, refs = pages_of(rng, [page * width] * B, width, B * width, page)
+    table[0, 1], table[3, 3] = -1, B * width + 1
+    lo = [0, 1, page - 1, page, page + 1, 2 * page, 1 << 30, -7, 3]
+    hi = [0, page * width, page, 2 * page, 5, 1 << 30, (1 << 31) - 1, 4 * page + 1, 3]
+    for f, t in ((None, None), (lo, None), (None, hi), (lo, hi)):
+        d, r = ints(table), ints(refs)
+        kda.cache_free(d, r, ints(f), ints(t), page=page)
+        torch.cuda.synchronize()
+        for got, w in zip((d, r), ora.free(table, refs, page, f, t)):
+            same(got, w, "free")
+
+
+@pytest.mark.parametrize("n_pages", [0, 1, 2, 7, 4096, 4099, 20001])
+@pytest.mark.parametrize("share", [0.0, 0.1, 0.5, 0.95, 1.0])
+def test_compact(n_pages, share):
+    rng = np.random.default_rng(n_pages + int(10 * share))
+    refs = (rng.random(n_pages) < share) * rng.integers(1, 5, n_pages)
+    table = rng.integers(-2, n_pages + 2, (5, 9))
+    want_t, want_r, remap, pairs = ora.compact(table, refs)
+    t, r, m, src, dst, info = kda.cache_compact(ints(table), ints(refs))
+    torch.cuda.synchronize()
+    same(t, want_t, "table"), same(r, want_r, "refs"), same(m, remap, "remap")
+    same(info, [len(pairs), int((refs != 0).sum())], "info")
+    fill = [(-1, -1)] * (n_pages // 2 - len(pairs))
+    same(src, np.array([p[0] for p in pairs + fill], int), "src"), same(dst, np.array([p[1] for p in pairs + fill], int), "dst")
+    t, r = ints(table), ints(refs)             # in place
+    kda.cache_compact(t, r, table_out=t, refs_out=r)
+    torch.cuda.synchronize()
+    same(t, want_t, "table in place"), same(r, want_r, "refs in place")
+
+
+def random_cache(n, HK, D, page, seed):
+    g = torch.Generator().manual_seed(seed)
+    c = kda.new_cache(n, HK, D, page)
+    for x in c[:2]:
+        x.copy_(torch.randint(0, 256, x.shape, generator=g, dtype=torch.uint8))
+    for x in c[2:]:
+        x.copy_(torch.randn(x.shape, generator=g))
+    return c
+
+
+@pytest.mark.parametrize("HK,D,page", [(1, 16, 16), (3, 32, 16), (2, 64, 64), (8, 128, 64), (5, 128, 128), (300, 16, 16)])
+def test_copy(HK, D, page):
+    n = 12
+    a, b = random_cache(n, HK, D, page, 1), random_cache(n + 2, HK, D, page, 2)
+    src, dst = [3, 11, -1, 5, n, 0, 1 << 30, 4, 9], [13, 0, 4, -1, 3, 7, 5, n + 2, 1]
+    for count in (None, 0, 2, 6, 100, -3):
+        to = [x.clone() for x in b]
+        kda.cache_copy(*a, ints(src), ints(dst), to=to, count=None if count is None else ints([count, 7]))
+        torch.cuda.synchronize()
+        want = [x.clone() for x in b]
+        for i, (s, d) in enumerate(zip(src, dst)):
+            if 0 <= s < n and 0 <= d < n + 2 and (count is None or i < count):
+                for x, y in zip(a, want):
+                    y[d] = x[s]
+        for got, w in zip(to, want):
+            assert torch.equal(got, w)
+    # within one cache
+    got, want = [x.clone() for x in a], [x.clone() for x in a]
+    kda.cache_copy(*got, ints([0, 1, 1]), ints([5, 6, 7]))
+    torch.cuda.synchronize()
+    for x in want:
+        x[5], x[6], x[7] = x[0].clone(), x[1].clone(), x[1].clone()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_copy_of_more_pages_than_workgroups():
+    n, HK, D, page = 5000, 2, 128, 64
+    a = random_cache(n, HK, D, page, 3)
+    b = [torch.zeros_like(x) for x in a]
+    order = torch.randperm(n, generator=torch.Generator().manual_seed(1)).to(torch.int32).cuda()
+    kda.cache_copy(*a, order, torch.arange(n, dtype=torch.int32, device="cuda"), to=b)
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, x[order.long()]) for x, y in zip(a, b))
+
+
+def test_compacted_cache_reads_the_same():
+    """Attention over scattered pages, and over the same ones moved to the front: the same bits."""
+    B, H, HK, D, page, width = 5, 4, 2, 32, 16, 6
+    rng = np.random.default_rng(2)
+    lens = [16, 90, 1, 47, 64]
+    table, refs = pages_of(rng, lens, width, 80, page)
+    c = kda.new_cache(80, HK, D, page)
+    k, v = (torch.randn(B, 90, HK, D, generator=torch.Generator().manual_seed(i)).cuda() for i in (1, 2))
+    t, r = ints(table), ints(refs)
+    kda.cache_append(k, v, *c, t, ints([0] * B), ints(lens))
+    q = torch.randn(B, 1, H, D, generator=torch.Generator().manual_seed(3)).cuda()
+    at = ints([n - 1 for n in lens])
+    want = kda.attn_step(q, *c, t, at)
+    t2, r2, _, src, dst, info = kda.cache_compact(t, r)
+    kda.cache_copy(*c, src, dst, count=info)
+    small = [x[:16].clone() for x in c]                     # 1 + 6 + 1 + 3 + 4 pages in use
+    got = kda.attn_step(q, *small, t2, at)
+    torch.cuda.synchronize()
+    assert info[1].item() == 15 and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_captured_and_replayed(side):
+    """Beams follow parents, get room and their tail pages' copies, in one graph of static buffers, as the
+    tables change from replay to replay; the same eagerly, and on a stream of its own."""
+    R, K, HK, D, page, width, n_pages = 2, 3, 2, 16, 16, 8, 60
+    start = np.array([[0, -1], [1, -1]])
+    table0 = np.full((2, width), -1)
+    table0[:, :1] = start[:, :1]
+    refs0 = np.zeros(n_pages, int)
+    refs0[:2] = 1
+
+    def buffers():
+        t = [ints(np.full((R * K, width), -1)) for _ in range(2)]
+        n = [ints([0] * R * K) for _ in range(2)]
+        refs = ints(refs0)
+        kda.cache_fork(ints(table0), ints([9, 12]), ints([[0] * K] * R), refs, page=page, table_out=t[0], len_out=n[0])
+        return t, n, refs, random_cache(n_pages, HK, D, page, 5)
+
+    parent = ints([[0] * K] * R)
+    T = 5
+
+    def step(t, n, refs, cache):
+        kda.cache_fork(t[0], n[0], parent, refs, page=page, table_out=t[1], len_out=n[1])
+        src, dst, info = kda.cache_reserve(t[1], n[1], refs, T=T, page=page)
+        kda.cache_copy(*cache, src, dst)
+        t[0].copy_(t[1])
+        torch.add(n[1], T, out=n[0])
+        return src, dst, info
+
+    g, e = buffers(), buffers()
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        warm = buffers()
+        step(*warm)
+    torch.cuda.current_stream().wait_stream(stream)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(*g)
+    rng = np.random.default_rng(0)
+    tables, lens, refs = *ora.fork(table0, [9, 12], [[0] * K] * R, refs0, page)[:2], ora.fork(table0, [9, 12], [[0] * K] * R, refs0, page)[2]
+    for i in range(12):
+        p = rng.integers(0, K, (R, K))
+        parent.copy_(torch.from_numpy(p))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        if side:
+            with torch.cuda.stream(stream):
+                eager = step(*e)
+        else:
+            eager = step(*e)
+        torch.cuda.synchronize()
+        tables, lens, refs = ora.fork(tables, lens, p, refs, page)
+        tables, refs, src, dst, info = ora.reserve(tables, lens, refs, T, page)
+        lens = lens + T
+        for x in (g, e):
+            same(x[0][0], tables, i), same(x[1][0], lens, i), same(x[2], refs, i)
+        for got, ea, w in zip(out, eager, (src, dst, info)):
+            same(got, w, i), same(ea, w, i)
+        assert all(torch.equal(x, y) for x, y in zip(g[3], e[3]))
+
+
+def test_refusals():
+    t, n, refs = ints([[0, 1], [2, 3]]), ints([5, 20]), ints([1] * 4)
+    with pytest.raises(kda.KDAError):
+        kda.cache_fork(t, n, ints([[0, 1]]), refs, page=24)
+    with pytest.raises(kda.KDAError):
+        kda.cache_fork(t, n, ints([[0, 1]]), refs, page=16, table_out=t)
+    with pytest.raises(ValueError):
+        kda.cache_fork(t, n, ints([[0], [0], [0]]), refs, page=16)
+    with pytest.raises(TypeError):
+        kda.cache_fork(t, n, ints([[0, 1]]).long(), refs, page=16)
+    with pytest.raises(ValueError):
+        kda.cache_fork(t, n[:1], ints([[0, 1]]), refs, page=16)
+    with pytest.raises(kda.KDAError):
+        kda.cache_reserve(t, n, refs, T=-1, page=16)
+    with pytest.raises(ValueError):
+        kda.cache_reserve(t, n, refs, ints([1]), page=16)
+    with pytest.raises(ValueError):
+        kda.cache_free(t.t(), refs, page=16)            # rows that are not contiguous
+    with pytest.raises(TypeError):
+        kda.cache_free(t, refs.float(), page=16)
+    c, other = kda.new_cache(4, 2, 16, 16), kda.new_cache(4, 2, 32, 16)
+    with pytest.raises(ValueError):
+        kda.cache_copy(*c, ints([0]), ints([1]), to=other)
+    with pytest.raises(ValueError):
+        kda.cache_copy(*c, ints([0]), ints([1, 2]))
+    with pytest.raises(ValueError):
+        kda.cache_copy(*c, ints([0]), ints([1]), count=ints([]))
+    with pytest.raises(kda.KDAError):                   # one buffer of two caches
+        kda.cache_copy(*c, ints([0]), ints([1]), to=(c[0], *kda.new_cache(4, 2, 16, 16)[1:]))
