@@ -59,31 +59,36 @@ struct AttnSharedArgs {
     const int* block_table; const int* cache_len; const int* new_len; const int* group_first; const int* prefix_len;
     void* o; float* part_o; float* part_ml;
     int n_groups, n_pages, max_pages, B, Tq, H, HK, G, page, window;
-    int row_blocks;                 // 16-row blocks of a workgroup's rows
+    int wide, own_blocks;           // SharedPlan
     int tiles, nprefix, nown;       // tiles of all groups' rows (at most); parts of a prefix and of a sequence's own keys
     int prefix_blocks;              // HK * tiles * nprefix
     size_t ldq;
     float scale_log2;
-    FastDiv divG;
+    FastDiv divG, divT;
 };
 // How the rows and keys are cut, from what the host knows: tables of max_len tokens.
 struct SharedPlan {
-    int row_blocks, tiles, nprefix, nown;
+    int wide;               // groups of 32 rows of a workgroup on a prefix; 0: own_blocks of 16 there too
+    int own_blocks;         // 16-row blocks of a workgroup on own keys
+    int tiles, nprefix, nown;
     long long blocks;
 };
-inline SharedPlan shared_plan(int B, int Tq, int HK, int G, int n_groups, int max_len) {
+inline SharedPlan shared_plan(int elem_bytes, int B, int Tq, int HK, int G, int D, int n_groups, int max_len) {
     SharedPlan p;
     const long long each = (long long)Tq * G, rows = each * B, average = n_groups > 0 ? rows / n_groups : rows;
-    p.row_blocks = average <= 16 ? 1 : 2;
-    const int br = 16 * p.row_blocks;
+    p.wide = elem_bytes == 4 || D < 32 || average <= 16 ? 0 : average <= 64 ? 2 : 4;
+    p.own_blocks = (p.wide ? each : average) <= 16 ? 1 : 2;
+    const int br = p.wide ? 32 * p.wide : 16 * p.own_blocks, bo = 16 * p.own_blocks;
     p.tiles = n_groups > 0 ? (int)(rows / br + n_groups) : 0;
-    const long long own = (long long)B * HK * ((each + br - 1) / br), most = max_len / 256;
+    const long long own = (long long)B * HK * ((each + bo - 1) / bo), most = max_len / 256;
     const auto parts = [most](long long wgs, long long want, int limit) {
         long long n = wgs > 0 ? want / wgs : 1;
         n = n < most ? n : most;
         return n < 1 ? 1 : n > limit ? limit : (int)n;
     };
-    p.nprefix = parts((long long)p.tiles * HK, 1024, kMaxSplits / 2);
+    // tiles that are there, if the groups are about as large as each other
+    const long long tiles = (rows + br - 1) / br > n_groups ? (rows + br - 1) / br : n_groups;
+    p.nprefix = parts(tiles * HK, p.wide ? 256 : 512, kMaxSplits / 2);
     p.nown = parts(own, 512, kMaxSplits / 2);
     p.blocks = (long long)HK * p.tiles * p.nprefix + own * p.nown;
     return p;

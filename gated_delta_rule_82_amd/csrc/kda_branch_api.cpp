@@ -135,18 +135,23 @@ kda_status kda_cache_copy(const void* k_cache, const void* v_cache, const float*
     return status_of(kda::launch_cache_copy(a, stream));
 }
 
-static bool shared_sizes_ok(int B, int Tq, int H, int HK, int n_groups, int max_len) {
+static bool shared_sizes_ok(int B, int Tq, int H, int HK, int D, int n_groups, int max_len) {
     if (n_groups < 0 || n_groups > (1 << 24) || !step_sizes_ok(B, Tq, H, HK, max_len)) return false;
     // packed rows of all sequences, and the workgroups of one launch
     if (H == 0) return true;
     return (unsigned long long)B * Tq * (H / HK) <= (1ull << 29) &&
-           kda::shared_plan(B, Tq, HK, H / HK, n_groups, max_len).blocks < (1ll << 24);
+           kda::shared_plan(4, B, Tq, HK, H / HK, D, n_groups, max_len).blocks < (1ll << 23) &&
+           kda::shared_plan(2, B, Tq, HK, H / HK, D, n_groups, max_len).blocks < (1ll << 23);
 }
 
 size_t kda_attn_shared_workspace(int B, int Tq, int H, int HK, int D, int n_groups, int max_len) {
-    if (!dim_ok(D) || !shared_sizes_ok(B, Tq, H, HK, n_groups, max_len) || B == 0 || H == 0 || Tq == 0) return 0;
-    const kda::SharedPlan p = kda::shared_plan(B, Tq, HK, H / HK, n_groups, max_len);
-    return split_bytes(p.nprefix + p.nown, (size_t)B * Tq * H, D);
+    if (!dim_ok(D) || !shared_sizes_ok(B, Tq, H, HK, D, n_groups, max_len) || B == 0 || H == 0 || Tq == 0) return 0;
+    int parts = 0;      // as many as either type needs
+    for (int e = 2; e <= 4; e += 2) {
+        const kda::SharedPlan p = kda::shared_plan(e, B, Tq, HK, H / HK, D, n_groups, max_len);
+        if (p.nprefix + p.nown > parts) parts = p.nprefix + p.nown;
+    }
+    return split_bytes(parts, (size_t)B * Tq * H, D);
 }
 
 kda_status kda_attn_shared(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -158,7 +163,7 @@ kda_status kda_attn_shared(const void* q, const void* k_cache, const void* v_cac
     if (!dtype_ok(dt)) return KDA_ERR_DTYPE;
     if (HK < 0 || !cache_sizes_ok(n_pages, max_pages, B, Tq, HK, D, page) || window < 0) return KDA_ERR_SHAPE;
     const int max_len = max_pages * page;
-    if (!shared_sizes_ok(B, Tq, H, HK, n_groups, max_len)) return KDA_ERR_SHAPE;
+    if (!shared_sizes_ok(B, Tq, H, HK, D, n_groups, max_len)) return KDA_ERR_SHAPE;
     if (!scale_ok(scale)) return KDA_ERR_SCALE;
     kda::AttnSharedArgs a{};
     KDA_TRY(stride(ldq, INT_MAX, H, D, dt, &a.ldq));
@@ -178,16 +183,17 @@ kda_status kda_attn_shared(const void* q, const void* k_cache, const void* v_cac
                        ints(prefix_len, n_groups), bytes_of(workspace, want)};
     const Rows ro = rows_of(o, nq, (size_t)H * D, H, D, dt);
     if (overlaps_any(ro, in, 11) || overlaps_any(in[10], in, 10)) return KDA_ERR_SHAPE;
-    const kda::SharedPlan p = kda::shared_plan(B, Tq, HK, H / HK, n_groups, max_len);
+    const kda::SharedPlan p = kda::shared_plan(elem_bytes(dt), B, Tq, HK, H / HK, D, n_groups, max_len);
     a.q = q; a.k_cache = (const uint8_t*)k_cache; a.v_cache = (const uint8_t*)v_cache; a.k_scale = k_scale; a.v_scale = v_scale;
     a.block_table = block_table; a.cache_len = cache_len; a.new_len = new_len; a.group_first = group_first;
     a.prefix_len = prefix_len; a.o = o;
     a.n_groups = n_groups; a.n_pages = n_pages; a.max_pages = n_pages > 0 ? max_pages : 0;
     a.B = B; a.Tq = Tq; a.H = H; a.HK = HK; a.G = H / HK; a.page = page; a.window = window;
-    a.row_blocks = p.row_blocks; a.tiles = p.tiles; a.nprefix = p.nprefix; a.nown = p.nown;
+    a.wide = p.wide; a.own_blocks = p.own_blocks; a.tiles = p.tiles; a.nprefix = p.nprefix; a.nown = p.nown;
     a.prefix_blocks = HK * p.tiles * p.nprefix;
     a.scale_log2 = (float)(scale * kLog2eD);
     a.divG = kda::fast_div((uint32_t)a.G);
+    a.divT = kda::fast_div((uint32_t)Tq);
     const size_t parts = (size_t)p.nprefix + p.nown;
     a.part_o = reinterpret_cast<float*>(workspace);
     a.part_ml = a.part_o + round256(parts * nq * H * D * 4) / 4;

@@ -49,8 +49,8 @@ hipError_t launch_cache_copy(const CopyArgs& a, hipStream_t) {
 hipError_t launch_attn_shared(int, int, const AttnSharedArgs& a, hipStream_t) {
     ++g_launches;
     expect((long long)a.max_pages * a.page <= (1 << 29) && a.nprefix >= 1 && a.nown >= 1 && a.nprefix + a.nown <= kMaxSplits, "shared sizes");
-    const u64 each = (u64)a.Tq * a.G, own = (u64)a.B * a.HK * a.nown * ((each + 16 * a.row_blocks - 1) / (16 * a.row_blocks));
-    expect(a.prefix_blocks >= 0 && a.prefix_blocks + own < (1ull << 24) && (u64)a.B * each <= (1ull << 29), "shared grid");
+    const u64 each = (u64)a.Tq * a.G, own = (u64)a.B * a.HK * a.nown * ((each + 16 * a.own_blocks - 1) / (16 * a.own_blocks));
+    expect(a.prefix_blocks >= 0 && a.prefix_blocks + own < (1ull << 23) && (u64)a.B * each <= (1ull << 29), "shared grid");
     expect(a.part_o && a.part_ml, "shared partials");
     return hipSuccess;
 }

@@ -157,6 +157,21 @@ def test_missing_pages():
     check(o, want, 64 * 1e-5, "missing pages")    # values below 64; a row's bound is below 1e-5 of them
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("N", [2, 12, 40])
+def test_scales_that_are_no_powers_of_two(dtype, N):
+    """A cache that somebody else filled: a code stands for itself times any scale."""
+    x = Batch([N], [200], [3, 40], 2, 64, 16, 1, dtype, seed=N)
+    c = x.cache
+    g = torch.Generator().manual_seed(N)
+    for dev, o in ((c.dev[2], c.K), (c.dev[3], c.V)):
+        f = 1.0 + torch.rand(dev.shape, generator=g).cuda()
+        f[torch.rand(dev.shape, generator=g).cuda() < 0.5] = 1.0
+        dev.mul_(f)
+        o.scale[:] = np64(dev)
+    run(x, queries(N, 1, 8, 64, dtype))
+
+
 def test_groups_that_are_none():
     """No groups, groups outside the batch: the decode step."""
     x = Batch([4], [50], [20, 3], 2, 32, 16, 1, F32)
