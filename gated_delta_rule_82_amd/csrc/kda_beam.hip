@@ -14,8 +14,13 @@ namespace kda {
 namespace {
 
 constexpr int kSegments = 8;      // of a part: each thread keeps the maximum of what it read of each
-constexpr int kUnroll = 8;        // 16-byte loads of a thread in flight; a segment is a multiple of them
+constexpr int kJoinThreads = 512;
+constexpr int kUnroll = 4;        // 16-byte loads of a thread in flight; a segment is a multiple of them
 constexpr int kFound = 1024;      // candidates of a part that are ranked
+
+// e^d of a difference d <= 0 in a sum that has a term of 1: the rounding of d log2 e is off
+// by |d| 2^-24 of the term, at most 2^-25 of the sum.
+__device__ __forceinline__ float exp_term(float d) { return exp2_fast(d * kLog2e); }
 
 // Order of values as that of unsigned integers; -0 is +0.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -33,35 +38,38 @@ __device__ __forceinline__ double key_value(uint64_t k) {
     return __longlong_as_double((long long)(k & 0x8000000000000000ull ? k ^ 0x8000000000000000ull : ~k));
 }
 
-// The largest t such that at least `most` of a wave's 4 x 64 keys are >= t (0 if fewer are).
-__device__ __forceinline__ uint32_t threshold(const uint32_t (&key)[4], int most) {
+// A t such that at least `most` of a wave's 2 x 64 keys are >= t (0 if fewer are): the largest
+// one of 20 bits, for a float sign, exponent and 11 bits, because each bit costs a round of
+// scalar work that nothing hides.
+__device__ __forceinline__ uint32_t threshold(uint32_t key0, uint32_t key1, int most) {
     uint32_t t = 0;
-    for (int bit = 31; bit >= 0; --bit) {
+    for (int bit = 31; bit >= 12; --bit) {
         const uint32_t c = t | 1u << bit;
-        int n = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) n += __popcll(__ballot(key[i] >= c));
-        if (n >= most) t = c;
+        if (__popcll(__ballot(key0 >= c)) + __popcll(__ballot(key1 >= c)) >= most) t = c;
     }
     return t;
 }
 
+// 16 bytes of a row whose elements are aligned as such only.
 template <typename T> struct Vec {
     static constexpr int N = 16 / (int)sizeof(T);
-    float x[N];
-    // from a row whose elements are aligned as such only; those at or past n are -infinity
+    struct __attribute__((packed, aligned(sizeof(T)))) Raw { uint32_t w[4]; } raw;
+    __device__ __forceinline__ void load(const T* p) { raw = *reinterpret_cast<const Raw*>(p); }
+    // elements [at, at + N) of n; those at or past n are -infinity
     __device__ __forceinline__ void load(const T* row, int at, int n) {
-        struct __attribute__((packed, aligned(sizeof(T)))) Raw { uint32_t w[4]; };
         if (at + N <= n) {
-            const Raw r = *reinterpret_cast<const Raw*>(row + at);
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                x[i] = sizeof(T) == 4 ? __uint_as_float(r.w[i % 4])
-                                      : __uint_as_float(i & 1 ? r.w[(i / 2) % 4] & 0xffff0000u : r.w[(i / 2) % 4] << 16);
+            load(row + at);
         } else {
 #pragma unroll
-            for (int i = 0; i < N; ++i) x[i] = at + i < n ? to_f<T>(row[at + i]) : kNegInf;
+            for (int i = 0; i < N; ++i) {
+                const float x = at + i < n ? to_f<T>(row[at + i]) : kNegInf;
+                if (sizeof(T) == 4) raw.w[i % 4] = __float_as_uint(x);
+                else raw.w[(i / 2) % 4] = i & 1 ? raw.w[(i / 2) % 4] | (__float_as_uint(x) & 0xffff0000u) : __float_as_uint(x) >> 16;
+            }
         }
+    }
+    __device__ __forceinline__ float operator[](int i) const {
+        return __uint_as_float(sizeof(T) == 4 ? raw.w[i % 4] : i & 1 ? raw.w[(i / 2) % 4] & 0xffff0000u : raw.w[(i / 2) % 4] << 16);
     }
 };
 
@@ -72,10 +80,15 @@ __device__ __forceinline__ bool beam_lives(const SelectArgs& a, int row) {
 }  // namespace
 
 // One part of one beam's row.  Each thread keeps the maximum and the sum of exponentials
-// of what it reads, and the maxima of its segments.  The M-th largest of the threads'
-// maxima bounds the M first from below; only segments that reach it are read again (a
+// of what it reads, and the maxima of its segments.  The M-th largest of the maxima of
+// pairs of threads bounds the M first from below; only segments that reach it are read again (a
 // few of 2048, from the cache nearby) and what reaches it there, usually little more
 // than M values, is ranked by counting.
+// Bound by reading the logits: 512 rows of 131072 bf16 (134 MB) take 34 us, 4.0 TB/s over all
+// and 26 us at the rate of a copy; the rest is the start and the selection, which all
+// parts do at the same time.  An exponential with its argument's rounding carried along
+// costs twice the instructions of one difference and took 41 us, groups of eight loads
+// a register too many for four workgroups a CU (48 us).  4 rows of 32000 fp32: 6.7 us.
 template <typename T>
 __global__ __launch_bounds__(kSelThreads) void kda_select_part_kernel(const SelectArgs a) {
     constexpr int N = Vec<T>::N, STEP = kSelThreads * N;
@@ -88,57 +101,82 @@ __global__ __launch_bounds__(kSelThreads) void kda_select_part_kernel(const Sele
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int row = blockIdx.x / a.nsplit, split = blockIdx.x % a.nsplit;
-    if ((a.done && a.done[row]) || !beam_lives(a, row)) return;    // the join does not ask for it
     const int per = select_part(a.V, a.nsplit, N), lo = min((long long)split * per, (long long)a.V), n = min(per, a.V - lo);
     const T* x = reinterpret_cast<const T*>(a.logits) + (size_t)row * a.ld + lo;
-    // loads of a segment
+    // loads of a segment, groups of loads
     const int loads = (n + STEP - 1) / STEP, per_seg = max(1, (loads + kSegments * kUnroll - 1) / (kSegments * kUnroll)) * kUnroll;
+    const int groups = (loads + kUnroll - 1) / kUnroll;
+    const bool skip = (a.done && a.done[row]) || !beam_lives(a, row);
 
-    float m = kNegInf, l = 0.f;
-    for (int s = 0; s < kSegments; ++s) {
-        float best = kNegInf;
-        for (int i = s * per_seg; i < min((s + 1) * per_seg, loads); i += kUnroll) {
-            Vec<T> v[kUnroll];
+    // A group is loaded while the one before is summed.  Behind the last whole 16 bytes a
+    // thread takes the row's last ones instead and drops those that are not its own.
+    float m = kNegInf, l = 0.f, best = kNegInf;
+    auto fetch = [&](Vec<T> (&v)[kUnroll], int g) {
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) v[u].load(x, ((i + u) * kSelThreads + tid) * N, n);
-            float y = kNegInf;
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-                for (int e = 0; e < N; ++e) y = fmaxf(y, v[u].x[e]);
-            best = fmaxf(best, y);
-            const float now = fmaxf(m, y), mu = now == kNegInf ? 0.f : now;
-            l *= exp_carried(m - mu);
-            m = now;
-            float part = 0.f;
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-                for (int e = 0; e < N; ++e) part += exp_carried(v[u].x[e] - mu);
-            l += part;
+        for (int u = 0; u < kUnroll; ++u) {
+            const int at = ((g * kUnroll + u) * kSelThreads + tid) * N;
+            if (n >= N) v[u].load(x + min(at, n - N));
+            else v[u].load(x, at, n);
         }
-        seg[s][tid] = best;
+    };
+    auto reduce = [&](const Vec<T> (&v)[kUnroll], int g) {
+        const bool whole = (g + 1) * kUnroll * STEP <= n || n < N;
+        auto value = [&](int u, int e) {
+            const int at = ((g * kUnroll + u) * kSelThreads + tid) * N;
+            return whole || min(at, n - N) + e >= at ? v[u][e] : kNegInf;
+        };
+        auto both = [&](auto value) {
+            float y[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+                for (int e = 0; e < N; ++e) y[e % 4] = fmaxf(y[e % 4], value(u, e));
+            const float z = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+            best = fmaxf(best, z);
+            const float now = fmaxf(m, z), mu = now == kNegInf ? 0.f : now;
+            l *= exp_term(m - mu);
+            m = now;
+            float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+                for (int e = 0; e < N; ++e) part[e % 4] += exp_term(value(u, e) - mu);
+            l += (part[0] + part[1]) + (part[2] + part[3]);
+        };
+        if (whole) both([&](int u, int e) { return v[u][e]; });
+        else both(value);
+        if ((g + 1) * kUnroll % per_seg == 0 || g + 1 == groups) {
+            seg[g * kUnroll / per_seg][tid] = best;
+            best = kNegInf;
+        }
+    };
+    Vec<T> v0[kUnroll], v1[kUnroll];
+    fetch(v0, 0);
+    if (skip) return;    // the join does not ask for it
+    for (int g = 0; g < groups; g += 2) {
+        if (g + 1 < groups) fetch(v1, g + 1);
+        reduce(v0, g);
+        if (g + 1 < groups) {
+            if (g + 2 < groups) fetch(v0, g + 2);
+            reduce(v1, g + 1);
+        }
     }
+    const int segments = (groups * kUnroll + per_seg - 1) / per_seg;
     top[tid] = m;
     if (tid == 0) n_todo = n_found = n_above = 0;
     __syncthreads();
 
-    uint32_t key[4];
-    float all = kNegInf;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float y = top[i * 64 + lane];
-        key[i] = order_key(y);
-        all = fmaxf(all, y);
-    }
+    // maxima of pairs of threads
+    const float top0 = fmaxf(top[lane], top[lane + 64]), top1 = fmaxf(top[lane + 128], top[lane + 192]);
+    float all = fmaxf(top0, top1);
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor(all, o, 64));
-    double sum = (double)l * (double)exp_carried(m - (all == kNegInf ? 0.f : all));
+    double sum = (double)l * (double)exp_term(m - (all == kNegInf ? 0.f : all));
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
     if (lane == 0) sums[wave] = sum;
     // candidates reach t; -infinity is none
-    uint32_t t = max(threshold(key, a.M), order_key(kNegInf) + 1);
+    uint32_t t = max(threshold(order_key(top0), order_key(top1), a.M), order_key(kNegInf) + 1);
 
     auto collect = [&](uint32_t least, int* counter) {   // of the segments in `todo`
         for (int i = tid; i < n_todo * per_seg; i += kSelThreads) {
@@ -148,14 +186,14 @@ __global__ __launch_bounds__(kSelThreads) void kda_select_part_kernel(const Sele
             v.load(x, at, n);
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                const uint32_t k = order_key(v.x[e]);
-                if (k < least || v.x[e] != v.x[e]) continue;
+                const uint32_t k = order_key(v[e]);
+                if (k < least || v[e] != v[e]) continue;
                 const int p = atomicAdd(counter, 1);
                 if (p < kFound) found[p] = (uint64_t)k << 32 | (uint32_t)~(uint32_t)(at + e);
             }
         }
     };
-    for (int s = 0; s < kSegments; ++s)
+    for (int s = 0; s < segments; ++s)
         if (order_key(seg[s][tid]) >= t) todo[atomicAdd(&n_todo, 1)] = (uint16_t)(s * kSelThreads + tid);
     __syncthreads();
     collect(t, &n_found);
@@ -179,7 +217,7 @@ __global__ __launch_bounds__(kSelThreads) void kda_select_part_kernel(const Sele
                     Vec<T> v;
                     v.load(x, at, n);
 #pragma unroll
-                    for (int e = 0; e < N; ++e) mine += v.x[e] == v.x[e] && order_key(v.x[e]) >= c ? 1 : 0;
+                    for (int e = 0; e < N; ++e) mine += v[e] == v[e] && order_key(v[e]) >= c ? 1 : 0;
                 }
 #pragma unroll
                 for (int o = 32; o > 0; o >>= 1) mine += __shfl_xor(mine, o, 64);
@@ -205,7 +243,7 @@ __global__ __launch_bounds__(kSelThreads) void kda_select_part_kernel(const Sele
             if (at < n) {
                 v.load(x, at, n);
 #pragma unroll
-                for (int e = 0; e < N; ++e) mine += order_key(v.x[e]) == t ? 1 : 0;
+                for (int e = 0; e < N; ++e) mine += order_key(v[e]) == t ? 1 : 0;
             }
             int y = mine;
 #pragma unroll
@@ -225,7 +263,7 @@ __global__ __launch_bounds__(kSelThreads) void kda_select_part_kernel(const Sele
             if (mine > 0) {
 #pragma unroll
                 for (int e = 0; e < N; ++e)
-                    if (order_key(v.x[e]) == t) {
+                    if (order_key(v[e]) == t) {
                         if (before < a.M) found[before] = (uint64_t)t << 32 | (uint32_t)~(uint32_t)(at + e);
                         ++before;
                     }
@@ -239,6 +277,7 @@ __global__ __launch_bounds__(kSelThreads) void kda_select_part_kernel(const Sele
     for (int i = tid; i < held; i += kSelThreads) {
         const uint64_t k = found[i];
         int rank = 0;
+#pragma unroll 8
         for (int j = 0; j < held; ++j) rank += found[j] > k ? 1 : 0;
         if (rank < a.M) {
             a.part_x[part * a.M + rank] = key_value((uint32_t)(k >> 32));
@@ -255,84 +294,89 @@ __global__ __launch_bounds__(kSelThreads) void kda_select_part_kernel(const Sele
 }
 
 // One workgroup a request: each beam's lse from its parts, then its parts' candidates
-// as scores in 64 bits, thinned by the M-th largest of the threads' maxima (of the
-// upper halves of their keys) and ranked by counting.
-__global__ __launch_bounds__(kSelThreads) void kda_select_join_kernel(const SelectArgs a) {
+// as scores in 64 bits, thinned by the M-th largest of the maxima of 128 sets (of the
+// upper halves of their keys) and ranked by counting.  A wave has a beam: what a beam
+// that lives no longer, or one at its end, has in the parts is whatever was there before.
+// Bound by waits one after the other: 64 requests of 8 beams, 2 parts and 16 candidates
+// take 5 us, 64 beams of 64 candidates 15.  Sets by thread were sets by rank, of which
+// a few held all the best: a thousand candidates to rank instead of a hundred.
+__global__ __launch_bounds__(kJoinThreads) void kda_select_join_kernel(const SelectArgs a) {
     __shared__ uint64_t key[kSelectHeld];
-    __shared__ uint64_t id[kSelectHeld];        // beam << 32 | token
-    __shared__ uint16_t list[kSelectHeld];
-    __shared__ uint32_t top[kSelThreads];
-    __shared__ double lse[kSelectMost], score[kSelectMost];
+    __shared__ uint32_t token[kSelectHeld];
+    __shared__ uint64_t list_key[kSelectHeld], list_id[kSelectHeld];    // beam << 32 | token
+    __shared__ uint32_t top[128];
     __shared__ int n_list;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = blockIdx.x;
-    for (int k = wave; k < a.K; k += kSelThreads / 64) {
+    const int per = a.nsplit * a.M;
+    if (tid == 0) n_list = 0;
+    if (tid < 128) top[tid] = 0;
+    __syncthreads();
+    for (int k = wave; k < a.K; k += kJoinThreads / 64) {
         const int row = r * a.K + k;
-        const bool lives = beam_lives(a, row), done = a.done && a.done[row];
-        double z = 0.0, y = lives && a.scores ? (double)a.scores[row] : 0.0;
+        const size_t part = (size_t)row * a.nsplit;
+        // independent of each other: one wait for all
+        const bool mine = lane < a.nsplit;
+        const double m0 = mine ? a.stat[2 * (part + lane)] : 0.0, l0 = mine ? a.stat[2 * (part + lane) + 1] : 0.0;
+        const float score0 = a.scores ? a.scores[row] : 0.f;
+        const bool done = a.done && a.done[row], lives = score0 - score0 == 0.f;
+        int w0 = -1;
+        float x0 = 0.f;
+        if (lane < per) {
+            w0 = a.part_w[part * a.M + lane];
+            x0 = a.part_x[part * a.M + lane];
+        }
+        double lse = 0.0;
         if (lives && !done) {
-            const size_t part = (size_t)row * a.nsplit + lane;
-            const bool mine = lane < a.nsplit;
-            const float m = mine ? (float)a.stat[2 * part] : kNegInf;
-            const double l = mine ? a.stat[2 * part + 1] : 0.0;
+            const float m = mine ? (float)m0 : kNegInf;
             float all = m;
 #pragma unroll
             for (int o = 32; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor(all, o, 64));
-            double sum = l == 0.0 ? 0.0 : l * exp((double)m - (double)all);
+            double sum = !mine || l0 == 0.0 ? 0.0 : l0 * exp((double)m - (double)all);
 #pragma unroll
             for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
-            z = (double)all + log(sum);
+            lse = (double)all + log(sum);
         }
-        if (lane == 0) {
-            lse[k] = z;
-            score[k] = y;
-        }
-    }
-    if (tid == 0) n_list = 0;
-    __syncthreads();
-    const int per = a.nsplit * a.M, held = a.K * per;
-    uint32_t most = 0;
-    for (int i = tid; i < held; i += kSelThreads) {
-        const int k = i / per, row = r * a.K + k;
-        const bool lives = beam_lives(a, row), done = a.done && a.done[row];
-        uint64_t y = 0, w = 0;
-        if (lives) {
-            double s = -__builtin_inf();
-            if (done) {
-                if (i % per == 0) {
-                    s = score[k];
-                    w = (uint32_t)a.end;
+        for (int i = lane; i < per; i += 64) {
+            uint64_t y = 0;
+            uint32_t w = 0;
+            if (lives) {
+                double s = -__builtin_inf();
+                if (done) {
+                    if (i == 0) {
+                        s = (double)score0;
+                        w = (uint32_t)a.end;
+                    }
+                } else {
+                    const int next = i < 64 ? w0 : a.part_w[part * a.M + i];
+                    if (next >= 0) {
+                        s = (double)score0 + ((double)(i < 64 ? x0 : a.part_x[part * a.M + i]) - lse);
+                        w = (uint32_t)next;
+                    }
                 }
-            } else {
-                const size_t at = (size_t)r * held + i;
-                const int token = a.part_w[at];
-                if (token >= 0) {
-                    s = score[k] + ((double)a.part_x[at] - lse[k]);
-                    w = (uint32_t)token;
-                }
+                if (s - s == 0.0) y = order_key(s);   // what is not finite is no continuation
             }
-            if (s - s == 0.0) y = order_key(s);   // what is not finite is no continuation
+            key[k * per + i] = y;
+            token[k * per + i] = w;
+            // one of 128 sets, not by the rank in the part
+            if (y) atomicMax(&top[((uint32_t)(k * per + i) * 0x9e3779b1u) >> 25], (uint32_t)(y >> 32));
         }
-        key[i] = y;
-        id[i] = (uint64_t)k << 32 | w;
-        most = max(most, (uint32_t)(y >> 32));
     }
-    top[tid] = most;
+    const int held = a.K * per;
     __syncthreads();
-    uint32_t mine[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) mine[i] = top[i * 64 + lane];
-    const uint32_t t = max(threshold(mine, a.M), 1u);   // the key of no finite number is below 2^32
-    for (int i = tid; i < held; i += kSelThreads)
-        if ((uint32_t)(key[i] >> 32) >= t) list[atomicAdd(&n_list, 1)] = (uint16_t)i;
+    const uint32_t t = max(threshold(top[lane], top[lane + 64], a.M), 1u);   // the key of no finite number is below 2^32
+    for (int i = tid; i < held; i += kJoinThreads)
+        if ((uint32_t)(key[i] >> 32) >= t) {
+            const int p = atomicAdd(&n_list, 1);
+            list_key[p] = key[i];
+            list_id[p] = (uint64_t)(i / per) << 32 | token[i];
+        }
     __syncthreads();
     const int n = n_list;
-    for (int i = tid; i < n; i += kSelThreads) {
-        const uint64_t y = key[list[i]], w = id[list[i]];
+    for (int i = tid; i < n; i += kJoinThreads) {
+        const uint64_t y = list_key[i], w = list_id[i];
         int rank = 0;
-        for (int j = 0; j < n; ++j) {
-            const uint64_t yj = key[list[j]];
-            rank += yj > y || (yj == y && id[list[j]] < w) ? 1 : 0;
-        }
+#pragma unroll 8
+        for (int j = 0; j < n; ++j) rank += (int)(list_key[j] > y) | ((int)(list_key[j] == y) & (int)(list_id[j] < w));
         if (rank < a.M) {
             const size_t at = (size_t)r * a.M + rank;
             a.scores_out[at] = (float)key_value(y);
@@ -340,7 +384,7 @@ __global__ __launch_bounds__(kSelThreads) void kda_select_join_kernel(const Sele
             a.token[at] = (int)(uint32_t)w;
         }
     }
-    for (int i = n + tid; i < a.M; i += kSelThreads) {
+    for (int i = n + tid; i < a.M; i += kJoinThreads) {
         const size_t at = (size_t)r * a.M + i;
         a.scores_out[at] = kNegInf;
         a.parent[at] = a.token[at] = -1;
@@ -351,7 +395,7 @@ template <typename T> static hipError_t launch_select_t(const SelectArgs& a, hip
     hipLaunchKernelGGL((kda_select_part_kernel<T>), dim3((unsigned)a.R * a.K * a.nsplit), dim3(kSelThreads), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kda_select_join_kernel, dim3((unsigned)a.R), dim3(kSelThreads), 0, s, a);
+    hipLaunchKernelGGL(kda_select_join_kernel, dim3((unsigned)a.R), dim3(kJoinThreads), 0, s, a);
     return hipGetLastError();
 }
 hipError_t launch_beam_select(int dt, const SelectArgs& a, hipStream_t s) {

@@ -112,7 +112,9 @@ constexpr int select_part(int V, int n, int per_load) {
     const int step = kSelThreads * per_load, per = (V + n - 1) / n;
     return (per + step - 1) / step * step;
 }
-// Parts of a row: about 1024 workgroups, at least 4096 elements each, and no more
+// Parts of a row: about 1024 workgroups (512 rows of 131072 bf16 take 54 us in 512, 43 in 1024,
+// 45 in 2048), at least 4096 elements each (32 rows of 65536 fp32 take 12 us, 15 with
+// twice as many parts of 2048), and no more
 // candidates than the join holds (a wave joins a beam's parts).
 inline int select_splits(int elem_bytes, int R, int K, int V, int M) {
     const long long rows = (long long)R * K;
