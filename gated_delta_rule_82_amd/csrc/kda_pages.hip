@@ -48,6 +48,11 @@ __device__ __forceinline__ int prefix_sum(int x, int* waves, int& total) {
     return before + y - x;
 }
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ void store_once(void* p, const uint4& x) {
+    __builtin_nontemporal_store(u32x4{x.x, x.y, x.z, x.w}, reinterpret_cast<u32x4*>(p));
+}
+
 // Four references from index i (a multiple of 4); those past the end count as in use.
 __device__ __forceinline__ int4 four_refs(const int* refs, int i, int n) {
     if (i + 4 <= n) return *reinterpret_cast<const int4*>(refs + i);
@@ -110,16 +115,22 @@ hipError_t launch_cache_free(const FreeArgs& a, hipStream_t s) {
 // need a page, how many before them do (a prefix sum), and which holders of a shared
 // page leave it (all but the last where nobody else holds it: holder k of those in
 // order leaves while refs - k > 1).  Free pages come in order from a walk over the
-// references, as many as are needed, through a ring in LDS.  256 sequences of one new
-// token, 2432 pages: see the table of cases; a walk over 65 536 pages adds 5 us.
+// references, as many as are needed, through a ring in LDS.  Bound by loads that wait for
+// each other (lengths, entries, references) and barriers: 4 sequences take 5 us; 256 of
+// one new token that all leave a shared page take 11, of which finding their order among
+// 256 holders is 4 (one compared at a time 6).
 __global__ __launch_bounds__(kBookThreads) void kda_cache_reserve_kernel(const ReserveArgs a) {
     constexpr int RING = 8192, STEP = 4 * kBookThreads;   // a step adds up to 4096 to fewer than 1024 left
     __shared__ int ring[RING];
-    __shared__ int claims[kBookThreads];
+    __shared__ __align__(16) int claims[kBookThreads];   // whole groups of 16
     __shared__ int waves[kBookWaves];
     const int tid = threadIdx.x;
     const unsigned items = (unsigned)a.B * a.touched;
+    const int page_log2 = 31 - __clz(a.page);
     int cursor = 0, lacking = 0;         // the same in every thread
+    // What the next step of the walk reads, ahead of it: no page becomes free here, and those
+    // handed out lie before the walk.
+    int4 ahead = four_refs(a.refs, 4 * tid, a.n_pages);
     unsigned head = 0, tail = 0;
     for (unsigned base = 0; base < items; base += kBookThreads) {
         const unsigned item = base + tid;
@@ -128,11 +139,11 @@ __global__ __launch_bounds__(kBookThreads) void kda_cache_reserve_kernel(const R
         int e = -1, held = 0;
         size_t at = 0;
         if (item < items) {
-            const long long before = len_of(a.cache_len, b), fresh = fresh_of(a.new_len, b, a.T), j = before / a.page + jj;
-            if (fresh > 0 && j < a.max_pages && j * a.page < before + fresh) {
+            const long long before = len_of(a.cache_len, b), fresh = fresh_of(a.new_len, b, a.T), j = (before >> page_log2) + jj;
+            if (fresh > 0 && j < a.max_pages && j << page_log2 < before + fresh) {
                 at = (size_t)b * a.max_pages + j;
                 e = a.table[at];
-                older = jj == 0 && before % a.page != 0;
+                older = jj == 0 && (before & (a.page - 1)) != 0;
                 const bool has = e >= 0 && e < a.n_pages;
                 if (has) held = load_refs(a.refs + e);
                 claim = has && held > 1;
@@ -146,7 +157,17 @@ __global__ __launch_bounds__(kBookThreads) void kda_cache_reserve_kernel(const R
             __syncthreads();
             if (claim) {
                 int k = 0;
-                for (int i = 0; i < rank; ++i) k += claims[i] == e;
+                for (int i = 0; i < rank; i += 16) {
+                    int4 c[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) c[u] = *reinterpret_cast<const int4*>(claims + i + 4 * u);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int left = rank - i - 4 * u;
+                        k += (int)(left > 0 & c[u].x == e) + (int)(left > 1 & c[u].y == e) + (int)(left > 2 & c[u].z == e) +
+                             (int)(left > 3 & c[u].w == e);
+                    }
+                }
                 claim = held - k > 1;
                 need = claim;
             }
@@ -155,7 +176,8 @@ __global__ __launch_bounds__(kBookThreads) void kda_cache_reserve_kernel(const R
         const int order = prefix_sum(need ? 1 : 0, waves, wanted);
         while ((int)(tail - head) < wanted && cursor < a.n_pages) {
             const int p = cursor + 4 * tid;
-            const int4 r = four_refs(a.refs, p, a.n_pages);
+            const int4 r = ahead;
+            ahead = four_refs(a.refs, p + STEP, a.n_pages);
             int found;
             unsigned to = tail + prefix_sum((r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0), waves, found);
             if (r.x == 0) ring[to++ % RING] = p;
@@ -181,12 +203,17 @@ __global__ __launch_bounds__(kBookThreads) void kda_cache_reserve_kernel(const R
         }
         head += have;
         lacking += wanted - have;
-        __threadfence();
-        __syncthreads();
+        if (items - base > kBookThreads) {
+            // the next entries read these references: all are at the second-level cache then (a
+            // fence for other workgroups too would write all of it back, 4 us)
+            wait_vmcnt<0>();
+            __syncthreads();
+        }
     }
     // free pages left: those in the ring and those behind the walk
-    int left = 0;
-    for (int p = cursor + 4 * tid; p < a.n_pages; p += STEP) {
+    int left = (ahead.x == 0) + (ahead.y == 0) + (ahead.z == 0) + (ahead.w == 0);
+    for (int p = cursor + 4 * tid; p < a.n_pages - STEP; ) {
+        p += STEP;
         const int4 r = four_refs(a.refs, p, a.n_pages);
         left += (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
     }
@@ -282,7 +309,10 @@ hipError_t launch_cache_compact(const CompactArgs& a, hipStream_t s) {
 }
 
 // A page's K, all heads, is one piece of memory, its V another.  A workgroup takes
-// pieces of up to 16 KB, four loads a thread in flight.
+// pieces of up to 16 KB, four loads a thread in flight.  512 pages of 64 tokens, 8 heads and
+// D = 128 (134 MB read and written): 25 us, 5.4 TB/s, with stores that leave the caches at once;
+// ordinary ones 38, loads of that kind as well 28; pieces of 8 KB 39, of 32 KB 50 (both with
+// ordinary stores).
 __global__ __launch_bounds__(256) void kda_cache_copy_kernel(const CopyArgs a, unsigned chunks) {
     constexpr unsigned U = 4, CHUNK = 256 * 16 * U;
     const int n = a.count ? min(max(a.count[0], 0), a.n) : a.n;
@@ -302,7 +332,7 @@ __global__ __launch_bounds__(256) void kda_cache_copy_kernel(const CopyArgs a, u
 #pragma unroll
         for (unsigned i = 0; i < U; ++i) {
             const unsigned at = c * CHUNK + i * 4096 + threadIdx.x * 16;
-            if (at < a.bytes) *reinterpret_cast<uint4*>(q + at) = x[i];
+            if (at < a.bytes) store_once(q + at, x[i]);
         }
         if (c == 0) {
             const float* s = (part ? a.vs : a.ks) + (size_t)from * a.HK;

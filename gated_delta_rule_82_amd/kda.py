@@ -754,7 +754,9 @@ def cache_reserve(block_table, cache_len, refs, new_len=None, *, T=1, page, src=
     _int32("T", T), _int32("page", page)
     _expect("cache_len", cache_len, (B,), torch.int32, dev)
     _expect("new_len", new_len, (B,), torch.int32, dev)
-    src, dst, info = _ints("src", (B,), src, dev), _ints("dst", (B,), dst, dev), _ints("info", (2,), info, dev)
+    src = _like(cache_len) if src is None else _ints("src", (B,), src, dev)
+    dst = _like(cache_len) if dst is None else _ints("dst", (B,), dst, dev)
+    info = _ints("info", (2,), info, dev)
     _launch("kda_cache_reserve", dev, _ptr(block_table), _ptr(refs), _ptr(cache_len), _ptr(new_len), _ptr(src), _ptr(dst),
             _ptr(info), B, T, width, n_pages, page)
     return src, dst, info
@@ -899,7 +901,8 @@ def beam_select(logits, scores=None, M=None, *, done=None, end=-1, scores_out=No
         scores_out = torch.empty((R, M), dtype=torch.float32, device=dev)
     else:
         _expect("scores_out", scores_out, (R, M), torch.float32, dev)
-    parent, token = _ints("parent", (R, M), parent, dev), _ints("token", (R, M), token, dev)
+    parent = _ints("parent", (R, M), parent, dev)
+    token = _like(parent) if token is None else _ints("token", (R, M), token, dev)
     ws = _workspace(beam_select_workspace_bytes(_int32("R", R), _int32("K", K), _int32("V", V), M, dt), workspace, dev)
     _launch("kda_beam_select", dev, logits.data_ptr(), _ptr(scores), _ptr(done), _ptr(scores_out), _ptr(parent), _ptr(token),
             R, K, V, M, _int32("the rows' stride", ld), end, _dt(dt), *_ws_args(ws))
