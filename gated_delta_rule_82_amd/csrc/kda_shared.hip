@@ -483,10 +483,40 @@ __global__ __launch_bounds__(512, 2) void kda_attn_shared_wide_kernel(const Attn
     }
     if (!work_of<BR, 16 * NR, 2>(a, lane, w)) return;
     const int rg = wave % RW, kg = wave / RW, wr0 = 32 * RB * rg;
-    for (int i = threadIdx.x; i < BR * D / 8; i += 512) {
-        const int r = i / (D / 8), gr = i % (D / 8);
-        *reinterpret_cast<uint4*>(queries + query_place<D>(r, gr)) = *reinterpret_cast<const uint4*>(row_of<T>(a, w, w.r0 + r, D).q + 8 * gr);
+    const int shift = 31 - __clz(a.page);
+    const int* table = a.block_table + (size_t)w.first * a.max_pages;
+    // steps of this part: of the prefix, or of what a window leaves of it
+    int s0 = 0, s1 = (w.prefix + 127) / 128, from, to;
+    auto share = [&]() {
+        s0 = __builtin_amdgcn_readfirstlane(s0);
+        s1 = __builtin_amdgcn_readfirstlane(s1);
+        const int per = s1 > s0 ? (s1 - s0 + w.parts - 1) / w.parts : 0;
+        from = min(s1, s0 + w.part * per);
+        to = min(s1, from + per);
+    };
+    share();
+    auto page_of = [&](int c0, int i) {
+        const int key = (c0 * kStepPieces + i) * 16;
+        return key < w.prefix && i < (min(to, c0 + kChunk) - c0) * kStepPieces ? table[key >> shift] : -1;
+    };
+    auto piece_of = [&](int pg, float k, float v) {
+        return pg >= 0 && pg < a.n_pages ? Piece{(uint32_t)pg * a.HK + w.hk, power(k), power(v), k / power(k), v / power(v)}
+                                         : Piece{Piece::kNoPage, 1.f, 1.f, 1.f, 1.f};
+    };
+    auto scale_of = [&](const float* scale, int pg) { return pg >= 0 && pg < a.n_pages ? scale[(uint32_t)pg * a.HK + w.hk] : 1.f; };
+    // Page numbers, queries, scales and lengths are each other's next loads or independent: they
+    // are on their way together before anything waits.  With a window the steps are not known yet.
+    int first_page = -1;
+    if (!a.window) first_page = page_of(from, threadIdx.x);
+    constexpr int NQ = (BR * D / 8 + 511) / 512;
+    u32x4 first_q[NQ];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+        const int at = i * 512 + threadIdx.x;
+        first_q[i] = u32x4{0u, 0u, 0u, 0u};
+        if (at < BR * D / 8) first_q[i] = *reinterpret_cast<const u32x4*>(row_of<T>(a, w, w.r0 + at / (D / 8), D).q + 8 * (at % (D / 8)));
     }
+    const float first_k = scale_of(a.k_scale, first_page), first_v = scale_of(a.v_scale, first_page);
     WideRows<D, RB> x;
     // keys that some row sees, and that all of this wave's do
     int lo = INT_MAX, hi = 0, all_lo = 0, all_hi = INT_MAX;
@@ -519,9 +549,11 @@ __global__ __launch_bounds__(512, 2) void kda_attn_shared_wide_kernel(const Attn
     }
     all_lo = __builtin_amdgcn_readfirstlane(all_lo);
     all_hi = __builtin_amdgcn_readfirstlane(all_hi);
-    // steps of this part: of the prefix, or of what a window leaves of it; page numbers are
-    // looked up before the lengths are there where there is none
-    int s0 = 0, s1 = (w.prefix + 127) / 128;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+        const int at = i * 512 + threadIdx.x;
+        if (at < BR * D / 8) *reinterpret_cast<u32x4*>(queries + query_place<D>(at / (D / 8), at % (D / 8))) = first_q[i];
+    }
     if (a.window) {
         __syncthreads();
 #pragma unroll
@@ -531,12 +563,8 @@ __global__ __launch_bounds__(512, 2) void kda_attn_shared_wide_kernel(const Attn
         }
         s0 = min(lo, w.prefix) / 128;
         s1 = (hi + 127) / 128;
+        share();
     }
-    s0 = __builtin_amdgcn_readfirstlane(s0);
-    s1 = __builtin_amdgcn_readfirstlane(s1);
-    const int per = s1 > s0 ? (s1 - s0 + w.parts - 1) / w.parts : 0;
-    const int from = min(s1, s0 + w.part * per), to = min(s1, from + per);
-    const int shift = 31 - __clz(a.page);
     // what this wave copies of a step: 16 keys of K; of V as much, as rows of 64 keys (a
     // quarter of the channels) or of 16
     const bool rows64 = a.page >= 64;
@@ -553,21 +581,18 @@ __global__ __launch_bounds__(512, 2) void kda_attn_shared_wide_kernel(const Attn
     const int vkey = 2 * kg + h, r32 = lane & 31;
     const uint32_t v_place = rows64 ? (vkey >> 2) * 4 * S::kPiece + r32 * 64 + ((vkey ^ (r32 >> 2)) & 3) * 16 : vkey * S::kPiece + r32 * 16;
     const uint32_t v_step = rows64 ? 32 * 64 : 32 * 16;
-    const int* table = a.block_table + (size_t)w.first * a.max_pages;
     const int page_log2 = shift + (D == 128 ? 7 : D == 64 ? 6 : 5);      // bytes of a page and head
     for (int c0 = from; c0 < to; c0 += kChunk) {
         const int c1 = min(to, c0 + kChunk);
         __syncthreads();
-        for (int i = threadIdx.x; i < (c1 - c0) * kStepPieces; i += 512) {
-            const int key = (c0 * kStepPieces + i) * 16;
-            Piece p{Piece::kNoPage, 1.f, 1.f, 1.f, 1.f};
-            if (key < w.prefix) {
-                const int pg = table[key >> shift];
-                if (pg >= 0 && pg < a.n_pages) {
-                    p.row = (uint32_t)pg * a.HK + w.hk;
-                    const float k = a.k_scale[p.row], v = a.v_scale[p.row];
-                    p = Piece{p.row, power(k), power(v), k / power(k), v / power(v)};
-                }
+        {
+            const int i = threadIdx.x;
+            Piece p;
+            if (c0 == from && !a.window) {
+                p = piece_of(first_page, first_k, first_v);
+            } else {
+                const int pg = page_of(c0, i);
+                p = piece_of(pg, scale_of(a.k_scale, pg), scale_of(a.v_scale, pg));
             }
             // plain steps: all pages there, scales powers of two
             const uint64_t fine = __ballot(p.there() && p.k_rest == 1.f && p.v_rest == 1.f);
