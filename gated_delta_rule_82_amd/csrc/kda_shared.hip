@@ -77,6 +77,15 @@ __device__ __forceinline__ bool group_of_tile(const AttnSharedArgs& a, int& tile
     return false;
 }
 
+// The number of a workgroup among those of the prefixes (common) or of own keys.  Half of the
+// latter go first and half last: what they read does not fit the memory's rate if all do so
+// at once, and the products of prefixes leave most of it idle.
+__device__ __forceinline__ int block_of(const AttnSharedArgs& a, bool& common) {
+    const int bid = blockIdx.x, early = ((int)gridDim.x - a.prefix_blocks) / 2;
+    common = bid >= early && bid < early + a.prefix_blocks;
+    return common ? bid - early : bid < early ? bid : bid - a.prefix_blocks;
+}
+
 // What a workgroup of BR rows computes.
 struct Work {
     int first, rows, r0;        // first sequence, rows of the group or sequence, first row here
@@ -86,8 +95,7 @@ struct Work {
 template <int BR_COMMON, int BR_OWN, int TEAMS = 1>
 __device__ __forceinline__ bool work_of(const AttnSharedArgs& a, int lane, Work& w, int team = 0) {
     const int each = a.Tq * a.G;
-    int bid = blockIdx.x;
-    w.common = bid < a.prefix_blocks;
+    int bid = block_of(a, w.common);
     if (w.common) {
         w.hk = bid % a.HK;
         bid /= a.HK;
@@ -104,7 +112,7 @@ __device__ __forceinline__ bool work_of(const AttnSharedArgs& a, int lane, Work&
         w.r0 = tile * BR_COMMON;
         return true;
     }
-    bid = (bid - a.prefix_blocks) * TEAMS + team;
+    bid = bid * TEAMS + team;
     const int nbh = a.B * a.HK, bh = bid % nbh;
     bid /= nbh;
     w.hk = bh % a.HK;
@@ -474,7 +482,9 @@ __global__ __launch_bounds__(512, 2) void kda_attn_shared_wide_kernel(const Attn
     __shared__ int2 bounds[BR];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
     Work w;
-    if (blockIdx.x >= (unsigned)a.prefix_blocks) {
+    bool common;
+    block_of(a, common);
+    if (!common) {
         const int team = wave / 4;
         const bool work = work_of<BR, 16 * NR, 2>(a, lane, w, team);
         narrow_rows<T, D, NR, 4>(a, w, work, reinterpret_cast<float(*)[16][D + 4]>(sm + team * kTeam),
