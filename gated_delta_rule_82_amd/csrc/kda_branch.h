@@ -66,30 +66,50 @@ struct AttnSharedArgs {
     float scale_log2;
     FastDiv divG, divT;
 };
-// How the rows and keys are cut, from what the host knows: tables of max_len tokens.
+// How a call is divided: tiles of 64 or 128 rows of a group (bf16, D >= 32) over steps of
+// 128 keys copied into LDS, or of 16 or 32 rows whose keys four waves read for
+// themselves.  A wide tile reads and converts each key for more rows, but fills a
+// compute unit alone and pays its start and end once a workgroup: its workgroups have to
+// have enough steps.  In us, 32-row / 64-row / 128-row tiles, 8 key/value heads, D = 128:
+//   8 groups of 32 rows on 4096 keys     29   36   42     8 of 32 on 16384     63   73   89
+//   4 groups of 64 rows on 4096 keys     26   33   36     8 of 64 on 4096      46   43   48
+//   8 groups of 64 rows on 16384 keys    96   83   96     1 of 256 on 4096     24   32   37
+//   1 group of 128 rows on 32768 keys    50   47   48     1 of 256 on 32768    83   74   65
+// where the 64-row tiles' workgroups have 8, 32, 4, 8, 32, 4, 16 and 32 steps each.  Each part of a
+// prefix is written and read again once, so there are only as many as give every
+// compute unit a workgroup (8 groups of 32 rows on 4096 keys: 29 us with 4 parts, 35 with 8); for
+// 32-row tiles twice as many where each keeps 1024 keys (on 16384 keys: 65 us with 4, 61 with 8).
 struct SharedPlan {
-    int wide;               // groups of 32 rows of a workgroup on a prefix; 0: own_blocks of 16 there too
-    int own_blocks;         // 16-row blocks of a workgroup on own keys
+    int wide;           // 0, or blocks of 32 rows of a tile: 2, 4
+    int own_blocks;     // blocks of 16 rows of a sequence's own keys (of a tile too, if not wide)
     int tiles, nprefix, nown;
-    long long blocks;
+    long long blocks;   // workgroups, at most
 };
 inline SharedPlan shared_plan(int elem_bytes, int B, int Tq, int HK, int G, int D, int n_groups, int max_len) {
     SharedPlan p;
     const long long each = (long long)Tq * G, rows = each * B, average = n_groups > 0 ? rows / n_groups : rows;
-    p.wide = elem_bytes == 4 || D < 32 || average <= 16 ? 0 : average <= 64 ? 2 : 4;
+    // tiles that are there, if the groups are about as large as each other
+    const auto tiles_of = [rows, n_groups](int br) { const long long n = (rows + br - 1) / br; return n > n_groups ? n : n_groups; };
+    const auto steps = [&](int br) {    // of a workgroup, where there are 256
+        const long long n = tiles_of(br) * HK;
+        return (n < 65536 ? n : 65536) * (max_len / 128) / 256;
+    };
+    const bool can = elem_bytes == 2 && D >= 32;
+    p.wide = can && average > 64 && steps(128) >= 12 ? 4 : can && average > 32 && steps(64) >= 8 ? 2 : 0;
     p.own_blocks = (p.wide ? each : average) <= 16 ? 1 : 2;
     const int br = p.wide ? 32 * p.wide : 16 * p.own_blocks, bo = 16 * p.own_blocks;
     p.tiles = n_groups > 0 ? (int)(rows / br + n_groups) : 0;
-    const long long own = (long long)B * HK * ((each + bo - 1) / bo), most = max_len / 256;
-    const auto parts = [most](long long wgs, long long want, int limit) {
+    const long long own = (long long)B * HK * ((each + bo - 1) / bo);
+    const auto parts = [max_len](long long wgs, int want, int keys) {
         long long n = wgs > 0 ? want / wgs : 1;
-        n = n < most ? n : most;
-        return n < 1 ? 1 : n > limit ? limit : (int)n;
+        n = n < max_len / keys ? n : max_len / keys;
+        return n < 1 ? 1 : n > kMaxSplits / 2 ? kMaxSplits / 2 : (int)n;
     };
-    // tiles that are there, if the groups are about as large as each other
-    const long long tiles = (rows + br - 1) / br > n_groups ? (rows + br - 1) / br : n_groups;
-    p.nprefix = parts(tiles * HK, p.wide ? 256 : 512, kMaxSplits / 2);
-    p.nown = parts(own, 512, kMaxSplits / 2);
+    const long long wgs = tiles_of(br) * HK;
+    p.nprefix = parts(wgs, 256, 256);
+    const int more = parts(wgs, 512, 1024);
+    if (!p.wide && p.own_blocks == 2 && more > p.nprefix) p.nprefix = more;
+    p.nown = parts(own, 512, 256);
     p.blocks = (long long)HK * p.tiles * p.nprefix + own * p.nown;
     return p;
 }
