@@ -136,7 +136,7 @@ kda_status kda_cache_copy(const void* k_cache, const void* v_cache, const float*
 }
 
 static bool shared_sizes_ok(int B, int Tq, int H, int HK, int D, int n_groups, int max_len) {
-    if (n_groups < 0 || n_groups > (1 << 24) || !step_sizes_ok(B, Tq, H, HK, max_len)) return false;
+    if (n_groups < 0 || n_groups > (1 << 16) || !step_sizes_ok(B, Tq, H, HK, max_len)) return false;
     // packed rows of all sequences, and the workgroups of one launch
     if (H == 0) return true;
     return (unsigned long long)B * Tq * (H / HK) <= (1ull << 29) &&

@@ -36,43 +36,59 @@ __device__ __forceinline__ Group from_lane(const Group& x, int i) {
     return Group{__builtin_amdgcn_readlane(x.first, i), __builtin_amdgcn_readlane(x.last, i), __builtin_amdgcn_readlane(x.prefix, i)};
 }
 
-// The group of sequence b (one of no tokens where there is none).  A wave looks at 64 groups
-// at a time.
+// The group of sequence b (one of no tokens where there is none): the last that begins at or
+// before it.  A wave looks at the first sequences of 64 groups at a time, evenly apart
+// until they are next to each other.
 __device__ __forceinline__ bool group_of(const AttnSharedArgs& a, int b, int lane, Group& found) {
-    for (int g0 = 0; g0 < a.n_groups; g0 += 64) {
-        Group x{0, 0, 0};
-        if (g0 + lane < a.n_groups) x = group_at(a, g0 + lane);
-        const uint64_t who = __ballot(x.first <= b && b < x.last);
-        if (who) {
-            found = from_lane(x, __builtin_ctzll(who));
-            return true;
+    int lo = 0, hi = a.n_groups;        // groups before lo begin at or before b, those from hi on behind it
+    while (lo < hi) {
+        const int apart = (hi - lo + 63) / 64, g = lo + lane * apart;
+        const int before = __popcll(__ballot(g < hi && min(max(a.group_first[g < hi ? g : lo], 0), a.B) <= b));
+        if (before == 0) hi = lo;
+        else {
+            const int last = lo + (before - 1) * apart;
+            hi = min(hi, last + apart);
+            lo = last + 1;
         }
     }
     found = Group{b, b + 1, 0};
-    return false;
+    if (lo == 0) return false;
+    const Group x = group_at(a, lo - 1);
+    if (b < x.first || b >= x.last) return false;
+    found = x;
+    return true;
 }
 
 // The group whose rows are in tile number `tile` of all groups' tiles, and the tile's
-// number within it.
+// number within it.  Four times 64 groups are on their way together.
 __device__ __forceinline__ bool group_of_tile(const AttnSharedArgs& a, int& tile, int rows_per_tile, int lane, Group& found) {
-    for (int g0 = 0; g0 < a.n_groups; g0 += 64) {
-        Group x{0, 0, 0};
-        if (g0 + lane < a.n_groups) x = group_at(a, g0 + lane);
-        const int n = (int)(((long long)(x.last - x.first) * a.Tq * a.G + rows_per_tile - 1) / rows_per_tile);
-        int y = n;
+    for (int g0 = 0; g0 < a.n_groups; g0 += 256) {
+        Group x[4];
 #pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int z = __shfl_up(y, o, 64);
-            if (lane >= o) y += z;
+        for (int i = 0; i < 4; ++i) {
+            const int g = g0 + 64 * i + lane;
+            x[i] = Group{0, 0, 0};
+            if (g < a.n_groups) x[i] = group_at(a, g);
         }
-        const uint64_t who = __ballot(tile < y);
-        if (who) {
-            const int i = __builtin_ctzll(who);
-            tile -= __builtin_amdgcn_readlane(y, i) - __builtin_amdgcn_readlane(n, i);
-            found = from_lane(x, i);
-            return true;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (g0 + 64 * i >= a.n_groups) break;
+            const int n = (int)(((long long)(x[i].last - x[i].first) * a.Tq * a.G + rows_per_tile - 1) / rows_per_tile);
+            int y = n;
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const int z = __shfl_up(y, o, 64);
+                if (lane >= o) y += z;
+            }
+            const uint64_t who = __ballot(tile < y);
+            if (who) {
+                const int j = __builtin_ctzll(who);
+                tile -= __builtin_amdgcn_readlane(y, j) - __builtin_amdgcn_readlane(n, j);
+                found = from_lane(x[i], j);
+                return true;
+            }
+            tile -= __builtin_amdgcn_readlane(y, 63);
         }
-        tile -= __builtin_amdgcn_readlane(y, 63);
     }
     return false;
 }

@@ -624,7 +624,7 @@ kda_status kda_cache_copy(const void* k_cache, const void* v_cache, const float*
  *   prefix_len [n_groups] int (clamped to the table).
  *   workspace  kda_attn_shared_workspace(B, Tq, H, HK, D, n_groups, max_pages * page)
  *        bytes, 256-byte aligned: partial results of prefixes and of own keys.
- * Sizes as there, and B * Tq * (H / HK) up to 2^29; below 2^23 workgroups (about 16 rows
+ * Sizes as there, and n_groups up to 2^16, B * Tq * (H / HK) up to 2^29; below 2^23 workgroups (about 16 rows
  * each, for groups and sequences, times the parts that fill the card).  Errors as kda_attn_step. */
 size_t kda_attn_shared_workspace(int B, int Tq, int H, int HK, int D, int n_groups, int max_len);
 kda_status kda_attn_shared(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -655,7 +655,7 @@ kda_status kda_state_reorder(const void* state, void* out, const int* parent, in
  *   scores   [R,K] fp32, or NULL (zeros).  A beam whose score is not finite has no
  *            continuation (the unused beams of a first step: -infinity).
  *   done     [R,K] bytes or NULL: a finished beam (not 0) has one continuation, `end`
- *            (a token, 0 .. V-1), with its score unchanged; its logits are not read.
+ *            (a token, 0 .. V-1), with its score unchanged, whatever its logits are.
  *   scores_out [R,M] fp32, parent, token [R,M] int.  Where fewer than M continuations
  *            have a score above -infinity the rest is -infinity, -1, -1.
  * Logits of -infinity are no continuations; a beam with a NaN or +infinity has none.

@@ -54,6 +54,51 @@ def test_select(dtype, R, K, V, M):
     check(logits_of(R, K, V, dtype, V + K), scores_of(R, K, M), M)
 
 
+@pytest.mark.parametrize("dtype,V", [(F32, 40001), (F32, 70000), (BF16, 100003), (BF16, 140000)])
+def test_select_of_one_part_a_row(dtype, V):
+    """As many beams and picks as there may be: a row is one part, read in several groups a segment."""
+    x, s = logits_of(1, 64, V, dtype, V), scores_of(1, 64, 1)
+    check(x, s, 64)
+    x[:, ::2] = x[:, :1, :1]                # equal values, the first V first of all
+    x[:, 1::2, V - 9:] = x.max() + 1        # and at the end of a row
+    check(x, s, 64)
+
+
+def test_select_and_reorder_captured_and_replayed():
+    """Logits, scores and finished beams change between replays of one graph; the state follows in place."""
+    R, K, V = 3, 4, 5003
+    x, s = logits_of(R, K, V, BF16, 1).cuda(), scores_of(R, K, 1).cuda()
+    done = torch.zeros(R, K, dtype=torch.uint8, device="cuda")
+    state = torch.zeros(R * K, 4, 8, device="cuda")
+
+    def step():
+        out = kda.beam_select(x, s, K, done=done, end=2)
+        kda.state_reorder(state, out[1], out=state)
+        return out
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for i in range(5):
+        hx, hs = logits_of(R, K, V, BF16, 10 + i), scores_of(R, K, 20 + i)
+        hd = torch.zeros(R, K, dtype=torch.uint8)
+        hd[i % R, i % K] = 1
+        before = torch.randn(R * K, 4, 8)
+        x.copy_(hx), s.copy_(hs), done.copy_(hd), state.copy_(before)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        eager = check(hx, hs, K, hd, 2)
+        assert all(torch.equal(a, b) for a, b in zip(got, eager))
+        assert np.array_equal(state.cpu().numpy(), ora.state_reorder(before.numpy(), got[1].cpu().numpy()))
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("V", [300, 20001])
 @pytest.mark.parametrize("M", [1, 3, 17, 64])

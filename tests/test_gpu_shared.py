@@ -189,6 +189,13 @@ def test_many_groups():
     run(x, queries(x.B, 1, 2, 16, BF16))
 
 
+@pytest.mark.parametrize("at", [0, 255, 256, 4095, 4999])
+def test_a_group_far_down(at):
+    """Empty groups before and behind the one that there is."""
+    x = Batch([0] * at + [5] + [0] * (4999 - at), [16] * at + [100] + [16] * (4999 - at), [20, 3], 2, 32, 16, 1, BF16, before=1)
+    run(x, queries(7, 1, 4, 32, BF16))
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_packed_queries(dtype):
     """The queries of a packed projection, read where they lie; a workspace of the caller's."""
@@ -267,3 +274,5 @@ def test_refusals():
         kda.attn_shared(q, *x.cache.dev, x.table, lens, first, prefix, workspace=torch.empty(1 << 20, dtype=torch.uint8))
     with pytest.raises(kda.KDAError):
         kda.attn_shared(q, *x.cache.dev, x.table, lens, first, prefix, o=q)
+    with pytest.raises(kda.KDAError):          # more groups than are looked through
+        kda.attn_shared(q, *x.cache.dev, x.table, lens, ints([0] * ((1 << 16) + 2)), ints([0] * ((1 << 16) + 1)))
