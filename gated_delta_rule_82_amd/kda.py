@@ -648,12 +648,27 @@ def new_cache(n_pages, HK, D, page=64, device="cuda"):
             torch.empty((n_pages, HK), dtype=torch.float32, device=device))
 
 
-def _cache_shapes(k_cache, v_cache, k_scale, v_scale, block_table, cache_len, new_len, B, D, dev):
-    n_pages, HK, page = k_cache.shape[:3]
+def _cache_fits(k_cache, v_cache, k_scale, v_scale, n_pages, HK, page, D, dev):
+    """Whether the four buffers are a cache of that size on `dev`: one test, since each of these calls' latency
+    is mostly that of looking at its arguments."""
+    return (k_cache.dtype is torch.uint8 and v_cache.dtype is torch.uint8 and k_scale.dtype is torch.float32
+            and v_scale.dtype is torch.float32 and k_cache.shape == (n_pages, HK, page, D)
+            and v_cache.shape == (n_pages, HK, D, page) and k_scale.shape == v_scale.shape == (n_pages, HK)
+            and k_cache.device == v_cache.device == k_scale.device == v_scale.device == dev)
+
+
+def _expect_cache(k_cache, v_cache, k_scale, v_scale, n_pages, HK, page, D, dev):
+    if _cache_fits(k_cache, v_cache, k_scale, v_scale, n_pages, HK, page, D, dev):
+        return
     _expect("k_cache", k_cache, (n_pages, HK, page, D), torch.uint8, dev)
     _expect("v_cache", v_cache, (n_pages, HK, D, page), torch.uint8, dev)
     _expect("k_scale", k_scale, (n_pages, HK), torch.float32, dev)
     _expect("v_scale", v_scale, (n_pages, HK), torch.float32, dev)
+
+
+def _cache_shapes(k_cache, v_cache, k_scale, v_scale, block_table, cache_len, new_len, B, D, dev):
+    n_pages, HK, page = k_cache.shape[:3]
+    _expect_cache(k_cache, v_cache, k_scale, v_scale, n_pages, HK, page, D, dev)
     _expect("block_table", block_table, (B, block_table.shape[-1]), torch.int32, dev)
     _expect("cache_len", cache_len, (B,), torch.int32, dev)
     _expect("new_len", new_len, (B,), torch.int32, dev)
@@ -720,8 +735,9 @@ def _table(block_table, refs):
     if block_table.dim() != 2 or refs.dim() != 1:
         raise ValueError("block_table must be [B,max_pages] and refs [n_pages]")
     dev = block_table.device
-    _expect("block_table", block_table, block_table.shape, torch.int32, dev)
-    _expect("refs", refs, refs.shape, torch.int32, dev)
+    if block_table.dtype is not torch.int32 or refs.dtype is not torch.int32 or refs.device != dev:
+        _expect("block_table", block_table, block_table.shape, torch.int32, dev)
+        _expect("refs", refs, refs.shape, torch.int32, dev)
     B, width = block_table.shape
     return B, _int32("block_table's pages", width), _int32("refs' pages", refs.shape[0]), dev
 
@@ -779,9 +795,10 @@ def cache_compact(block_table, refs, *, table_out=None, refs_out=None):
     remap [n_pages], src, dst [n_pages // 2], info): remap is a page's new number (-1: free),
     info [copies, used pages].  cache_copy(..., src, dst, count=info) moves the data."""
     B, width, n_pages, dev = _table(block_table, refs)
-    table_out, refs_out = _ints("table_out", (B, width), table_out, dev), _ints("refs_out", (n_pages,), refs_out, dev)
-    remap, info = _ints("remap", (n_pages,), None, dev), _ints("info", (2,), None, dev)
-    src, dst = _ints("src", (n_pages // 2,), None, dev), _ints("dst", (n_pages // 2,), None, dev)
+    table_out = _like(block_table) if table_out is None else _ints("table_out", (B, width), table_out, dev)
+    refs_out = _like(refs) if refs_out is None else _ints("refs_out", (n_pages,), refs_out, dev)
+    remap, info, src = _like(refs), _ints("info", (2,), None, dev), _ints("src", (n_pages // 2,), None, dev)
+    dst = _like(src)
     _launch("kda_cache_compact", dev, _ptr(block_table), _ptr(refs), _ptr(table_out), _ptr(refs_out), _ptr(remap),
             _ptr(src), _ptr(dst), _ptr(info), B, width, n_pages)
     return table_out, refs_out, remap, src, dst, info
@@ -789,10 +806,7 @@ def cache_compact(block_table, refs, *, table_out=None, refs_out=None):
 
 def _cache_buffers(k_cache, v_cache, k_scale, v_scale, dev):
     n_pages, HK, page, D = k_cache.shape
-    _expect("k_cache", k_cache, (n_pages, HK, page, D), torch.uint8, dev)
-    _expect("v_cache", v_cache, (n_pages, HK, D, page), torch.uint8, dev)
-    _expect("k_scale", k_scale, (n_pages, HK), torch.float32, dev)
-    _expect("v_scale", v_scale, (n_pages, HK), torch.float32, dev)
+    _expect_cache(k_cache, v_cache, k_scale, v_scale, n_pages, HK, page, D, dev)
     return n_pages, HK, page, D
 
 
