@@ -178,9 +178,13 @@ __device__ __forceinline__ size_t part_at(const AttnSharedArgs& a, const Work& w
     const int each = a.Tq * a.G, s = (int)fdiv(fdiv((uint32_t)r, a.divG), a.divT);
     return (((size_t)(w.common ? w.part : a.nprefix + w.part) * a.B + w.first + s) * a.HK + w.hk) * each + (r - s * each);
 }
-__device__ __forceinline__ void leave_sum(const AttnSharedArgs& a, const Work& w, int r, size_t at, float m, float total) {
+// Whether it belongs to a token that there is.
+__device__ __forceinline__ bool row_lives(const AttnSharedArgs& a, const Work& w, int r) {
     const int tau = (int)fdiv((uint32_t)r, a.divG), s = (int)fdiv((uint32_t)tau, a.divT);
-    const bool live = tau - s * a.Tq < seq_len(a.new_len, w.first + s, a.Tq);
+    return tau - s * a.Tq < seq_len(a.new_len, w.first + s, a.Tq);
+}
+__device__ __forceinline__ size_t place_of(const uint2& x) { return (size_t)(x.y & ~(1u << 31)) << 32 | x.x; }
+__device__ __forceinline__ void leave_sum(const AttnSharedArgs& a, bool live, size_t at, float m, float total) {
     *reinterpret_cast<float2*>(a.part_ml + 2 * at) = live ? make_float2(m, total) : make_float2(kNegInf, 0.f);
 }
 
@@ -227,14 +231,14 @@ __device__ __forceinline__ void narrow_rows(const AttnSharedArgs& a, const Work&
     for (int n = 0; n < NR; ++n) {
         const float sum = group_add4(x.l[n]);
         const float top = sum != sum ? -kNegInf : x.m[n];  // a NaN sum takes part whatever the other maxima are
-        __syncthreads();
+        lds_barrier();
         if (g == 0) {
             sml[wave][lr][0] = top;
             sml[wave][lr][1] = sum;
         }
 #pragma unroll
         for (int d = 0; d < ND; ++d) *reinterpret_cast<floatx4*>(&so[wave][lr][16 * d + 4 * g]) = x.o[d][n];
-        __syncthreads();
+        lds_barrier();
         for (int i = threadIdx.x % (64 * NW); i < 16 * D / 4; i += 64 * NW) {
             const int row = i / (D / 4), d = (i % (D / 4)) * 4, r = w.r0 + 16 * n + row;
             if (!work || r >= w.rows) continue;
@@ -254,7 +258,7 @@ __device__ __forceinline__ void narrow_rows(const AttnSharedArgs& a, const Work&
             }
             const size_t at = part_at(a, w, r);
             *reinterpret_cast<floatx4*>(a.part_o + at * D + d) = y;
-            if (d == 0) leave_sum(a, w, r, at, mm, total);
+            if (d == 0) leave_sum(a, row_lives(a, w, r), at, mm, total);
         }
     }
 }
@@ -499,6 +503,7 @@ __global__ __launch_bounds__(512, 2) void kda_attn_shared_wide_kernel(const Attn
     __shared__ float sml[NW][32][2];
     __shared__ int range[NW][2];
     __shared__ int2 bounds[BR];
+    __shared__ uint2 place[BR];                     // of a row's part, and whether the row is there
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
     Work w;
     bool common;
@@ -553,6 +558,11 @@ __global__ __launch_bounds__(512, 2) void kda_attn_shared_wide_kernel(const Attn
     for (int n = 0; n < RB; ++n) {
         const Row<T> row = row_of<T>(a, w, w.r0 + wr0 + 32 * n + (lane & 31), D);
         if (kg == 0 && h == 0) bounds[wr0 + 32 * n + lane] = make_int2(row.lo, row.hi);
+        if (kg == 1 && h == 0) {
+            const int r = min(w.r0 + wr0 + 32 * n + lane, w.rows - 1);
+            const size_t at = part_at(a, w, r);
+            place[wr0 + 32 * n + lane] = make_uint2((uint32_t)at, (uint32_t)(at >> 32) | (row_lives(a, w, r) ? 1u << 31 : 0u));
+        }
         x.m[n] = kNegInf;
         x.l[n] = 0.f;
 #pragma unroll
@@ -728,50 +738,59 @@ __global__ __launch_bounds__(512, 2) void kda_attn_shared_wide_kernel(const Attn
         lds_barrier();
         if (!late) lds_barrier();
     }
-    // join the waves of each row group, 32 rows at a time: each wave's sums weighted, then added
+    // join the waves of each row group, 32 rows at a time: each wave's sums weighted, then added;
+    // barriers that do not wait for the parts' way to memory
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));   // nothing of it is kept through the loop, where it would be spilled
+    const int er = tid & 31, eh = tid >> 5 & 1;
     float(*buf)[32][D + 4] = reinterpret_cast<float(*)[32][D + 4]>(sm);
 #pragma unroll
     for (int n = 0; n < RB; ++n) {
         const float sum = pair_add(x.l[n]);
-        __syncthreads();
-        if (h == 0) {
-            sml[wave][lane][0] = sum != sum ? -kNegInf : x.m[n];  // a NaN sum takes part whatever the other maxima are
-            sml[wave][lane][1] = sum;
+        lds_barrier();
+        if (eh == 0) {
+            sml[wave][er][0] = sum != sum ? -kNegInf : x.m[n];  // a NaN sum takes part whatever the other maxima are
+            sml[wave][er][1] = sum;
         }
-        __syncthreads();
-        float mm = kNegInf;
+        lds_barrier();
+        float top[KW], total[KW], mm = kNegInf;
 #pragma unroll
-        for (int v = 0; v < KW; ++v) mm = fmaxf(mm, sml[v * RW + rg][r32][0]);
-        const float f = exp2_fast(sml[wave][r32][0] - (mm == kNegInf ? 0.f : mm));
+        for (int v = 0; v < KW; ++v) {
+            top[v] = sml[v * RW + rg][er][0];
+            total[v] = sml[v * RW + rg][er][1];
+            mm = fmaxf(mm, top[v]);
+        }
+        const float mu = mm == kNegInf ? 0.f : mm, f = exp2_fast(sml[wave][er][0] - mu);
+        if (kg == 0 && eh == 0 && w.r0 + wr0 + 32 * n + er < w.rows) {
+            float l = 0.f;
+#pragma unroll
+            for (int v = 0; v < KW; ++v) {
+                const float e = exp2_fast(top[v] - mu);
+                if (e != 0.f) l = fmaf(e, total[v], l);
+            }
+            const uint2 there = place[wr0 + 32 * n + er];
+            leave_sum(a, there.y >> 31, place_of(there), mm, l);
+        }
+        const bool all = __all(f != 0.f);           // a wave that saw nothing of a row takes no part in it
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 floatx4 y = {x.o[n][d][4 * e], x.o[n][d][4 * e + 1], x.o[n][d][4 * e + 2], x.o[n][d][4 * e + 3]};
-                *reinterpret_cast<floatx4*>(&buf[wave][r32][32 * d + 8 * e + 4 * h]) = f == 0.f ? floatx4{0.f, 0.f, 0.f, 0.f} : y * f;
+                y *= f;
+                if (!all) y = f == 0.f ? floatx4{0.f, 0.f, 0.f, 0.f} : y;
+                *reinterpret_cast<floatx4*>(&buf[wave][er][32 * d + 8 * e + 4 * eh]) = y;
             }
-        __syncthreads();
+        lds_barrier();
 #pragma unroll
-        for (int i = threadIdx.x; i < RW * 32 * (D / 4); i += 64 * NW) {
-            const int g = i / (8 * D), at32 = i / (D / 4) % 32, ch = i % (D / 4) * 4, row = w.r0 + 32 * (RB * g + n) + at32;
+        for (int k = 0; k < RW * 32 * (D / 4) / (64 * NW); ++k) {
+            const int i = k * (64 * NW) + tid;
+            const int g = i / (8 * D), at32 = i / (D / 4) % 32, ch = i % (D / 4) * 4, local = 32 * (RB * g + n) + at32, row = w.r0 + local;
             if (row >= w.rows) continue;
             floatx4 y = *reinterpret_cast<const floatx4*>(&buf[g][at32][ch]);
 #pragma unroll
             for (int v = 1; v < KW; ++v) y += *reinterpret_cast<const floatx4*>(&buf[v * RW + g][at32][ch]);
-            const size_t at = part_at(a, w, row);
-            *reinterpret_cast<floatx4*>(a.part_o + at * D + ch) = y;
-            if (ch == 0) {
-                float top = kNegInf, total = 0.f;
-#pragma unroll
-                for (int v = 0; v < KW; ++v) top = fmaxf(top, sml[v * RW + g][at32][0]);
-                const float mu = top == kNegInf ? 0.f : top;
-#pragma unroll
-                for (int v = 0; v < KW; ++v) {
-                    const float e = exp2_fast(sml[v * RW + g][at32][0] - mu);
-                    if (e != 0.f) total = fmaf(e, sml[v * RW + g][at32][1], total);
-                }
-                leave_sum(a, w, row, at, top, total);
-            }
+            *reinterpret_cast<floatx4*>(a.part_o + place_of(place[local]) * D + ch) = y;
         }
     }
 }
