@@ -37,26 +37,25 @@ __device__ __forceinline__ Group from_lane(const Group& x, int i) {
 }
 
 // The group of sequence b (one of no tokens where there is none): the last that begins at or
-// before it.  A wave looks at the first sequences of 64 groups at a time, evenly apart
-// until they are next to each other.
+// before it.  A wave looks at 64 groups at a time, evenly apart until they are next to
+// each other.
 __device__ __forceinline__ bool group_of(const AttnSharedArgs& a, int b, int lane, Group& found) {
+    found = Group{0, 0, 0};
     int lo = 0, hi = a.n_groups;        // groups before lo begin at or before b, those from hi on behind it
     while (lo < hi) {
         const int apart = (hi - lo + 63) / 64, g = lo + lane * apart;
-        const int before = __popcll(__ballot(g < hi && min(max(a.group_first[g < hi ? g : lo], 0), a.B) <= b));
-        if (before == 0) hi = lo;
-        else {
-            const int last = lo + (before - 1) * apart;
-            hi = min(hi, last + apart);
-            lo = last + 1;
-        }
+        Group x{0, 0, 0};
+        if (g < hi) x = group_at(a, g);
+        const int before = __popcll(__ballot(g < hi && x.first <= b));
+        if (before == 0) break;
+        found = from_lane(x, before - 1);
+        const int last = lo + (before - 1) * apart;
+        hi = min(hi, last + apart);
+        lo = last + 1;
     }
+    if (b >= found.first && b < found.last) return true;
     found = Group{b, b + 1, 0};
-    if (lo == 0) return false;
-    const Group x = group_at(a, lo - 1);
-    if (b < x.first || b >= x.last) return false;
-    found = x;
-    return true;
+    return false;
 }
 
 // The group whose rows are in tile number `tile` of all groups' tiles, and the tile's
@@ -107,6 +106,7 @@ struct Work {
     int first, rows, r0;        // first sequence, rows of the group or sequence, first row here
     int hk, prefix, part, parts;
     bool common;                // keys of the prefix, for a group's rows
+    int len;                    // tokens before the new ones, of own keys' sequence
 };
 template <int BR_COMMON, int BR_OWN, int TEAMS = 1>
 __device__ __forceinline__ bool work_of(const AttnSharedArgs& a, int lane, Work& w, int team = 0) {
@@ -138,6 +138,7 @@ __device__ __forceinline__ bool work_of(const AttnSharedArgs& a, int lane, Work&
     w.rows = each;
     w.r0 = bid / a.nown * BR_OWN;
     if (w.r0 >= w.rows) return false;                   // a team without work
+    w.len = a.cache_len[w.first];                        // on its way while the group is looked for
     Group x;
     const bool member = group_of(a, w.first, lane, x);
     w.prefix = x.prefix;
@@ -162,7 +163,7 @@ __device__ __forceinline__ Row<T> row_of(const AttnSharedArgs& a, const Work& w,
     x.t = tau - s * a.Tq;
     x.b = w.first + s;
     const int ql = seq_len(a.new_len, x.b, a.Tq), cap = a.max_pages * a.page;
-    const long long before = max(a.cache_len[x.b], 0), at = before + x.t;
+    const long long before = max(w.common ? a.cache_len[x.b] : w.len, 0), at = before + x.t;
     const int kl = (int)min(before + ql, (long long)cap);
     const int from = a.window ? (int)min((long long)cap, max(at - a.window + 1, 0ll)) : 0, to = (int)min(at, (long long)kl - 1);
     x.lo = w.common ? from : max(from, w.prefix);
