@@ -485,9 +485,9 @@ __global__ __launch_bounds__(64 * kSharedWaves) void kda_attn_shared_kernel(cons
 // Bound by issue: a step of 128 keys for 128 rows of D = 128 is 64 products (2048 cycles of a
 // SIMD) beside as many cycles of conversions, exponentials and sums that the products of
 // the other wave hide in part only; it takes about 5000.  64 sequences of 4 heads on 32768
-// common keys (8 key/value heads, 512 own keys each): 71 us, of which the steps are 34 (the
-// products alone would be 25 at the rate of a large product), own keys 11; 7 more for the
-// join.  On 32-row tiles 96 us in all.
+// common keys (8 key/value heads, 512 own keys each): 69 us with the join, of which the steps
+// are 34 (the products alone would be 25 at the rate of a large product) and own keys 11.
+// On 32-row tiles 96 us.
 template <int D, int RB, int NR>
 __global__ __launch_bounds__(512, 2) void kda_attn_shared_wide_kernel(const AttnSharedArgs a) {
     typedef bf16_t T;

@@ -141,3 +141,46 @@ def test_drafted_tokens_are_taken_back():
         kda.cache_free(table, refs, None, lens, page=PAGE)
         held = table[table >= 0].cpu().numpy()
         assert np.array_equal(refs.cpu().numpy(), np.bincount(held, minlength=12))
+
+
+def test_two_streams_at_once():
+    """Calls of two streams, each with tensors of its own, give what they give alone."""
+    def work(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        rand = lambda *n: torch.randint(0, 100, n, generator=g, device="cuda", dtype=torch.uint8)  # noqa: E731
+        n_pages, HK, D, page, B = 300, 2, 64, 16, 40
+        cache = [rand(n_pages, HK, page, D), rand(n_pages, HK, D, page), torch.ones(n_pages, HK, device="cuda"),
+                 torch.ones(n_pages, HK, device="cuda")]
+        table = torch.full((B, 1 << 14), -1, dtype=torch.int32, device="cuda")     # room for the wide tiles too
+        table[:, :6] = torch.arange(6, device="cuda")
+        table[:, 6] = 6 + torch.arange(B, device="cuda")
+        lens, refs = ints([100] * B), torch.zeros(n_pages, dtype=torch.int32, device="cuda")
+        refs[:6], refs[6:6 + B] = B, 1
+        q = torch.randn(B, 1, 8, D, generator=g, device="cuda").bfloat16()
+        logits = torch.randn(4, 10, 20000, generator=g, device="cuda").bfloat16()
+        scores = -torch.rand(4, 10, generator=g, device="cuda")
+        first, prefix = ints([0, B]), ints([96])
+
+        def run():
+            o = kda.attn_shared(q, *cache, table, lens, first, prefix)
+            best = kda.beam_select(logits, scores, 10)
+            r = refs.clone()
+            kids, n = kda.cache_fork(table[:, :8].contiguous(), lens, best[1].contiguous(), r, page=page)
+            src, dst, info = kda.cache_reserve(kids, n, r, page=page)
+            copied = [x.clone() for x in cache]
+            kda.cache_copy(*copied, src, dst)
+            return [o, *best, kids, n, r, src, dst, info, *copied]
+        return run
+
+    runs = [work(1), work(2)]
+    want = [r() for r in runs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in runs]
+    got = [None, None]
+    for _ in range(5):
+        for i, (r, s) in enumerate(zip(runs, streams)):
+            with torch.cuda.stream(s):
+                got[i] = r()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
