@@ -348,7 +348,7 @@ __global__ __launch_bounds__(64 * kStepWaves) void kda_attn_step_kernel(const At
     x.clear();
     const PagedKeys keys{a.k_cache, a.v_cache, a.k_scale, a.v_scale, a.block_table + (size_t)b * a.max_pages,
                          a.n_pages, a.page, a.HK, hk, kl, a.scale_log2};
-    for (int kb = kb0 + wave; kb < kb1; kb += NW) x.attend(keys, kb, lane);
+    x.attend(keys, kb0 + wave, kb1, NW, lane);
 
     // join the waves, 16 rows at a time
 #pragma unroll

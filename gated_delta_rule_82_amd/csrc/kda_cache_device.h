@@ -56,6 +56,21 @@ struct PagedKeys {
     int n_pages, page, HK, hk;
     int kl;                     // cached tokens
     float scale_log2;
+
+    __device__ __forceinline__ int page_log2() const { return 31 - __builtin_clz(page); }
+    // 16-key pieces of a lane's V keys (piece g of block kb) and of its K rows (piece lr / 4);
+    // those past the last token repeat the last one
+    __device__ __forceinline__ int2 pieces(int kb, int lane) const {
+        const int last = (kl - 1) >> 4, first = kb * (kStepKeys / 16);
+        return make_int2(min(first + (lane >> 4), last), min(first + ((lane & 15) >> 2), last));
+    }
+    // their table entries, asked for a block ahead: one wait less a block (the decode step over 4096
+    // tokens 220 -> 216 us, one group's 32-row tiles on 4001 common keys 28 -> 27)
+    __device__ __forceinline__ int2 entries(int kb, int lane) const {
+        const int2 p = pieces(kb, lane);
+        const int shift = page_log2() - 4;
+        return make_int2(table[p.x >> shift], table[p.y >> shift]);
+    }
 };
 
 // A wave's 16 NR packed rows and what they have gathered.  It takes blocks of 64 keys: lane
@@ -100,22 +115,20 @@ template <typename T, int D, int NR> struct CacheRows {
         }
     }
 
-    // Keys 64 kb .. 64 kb + 63 below the length.
-    __device__ __forceinline__ void attend(const PagedKeys& c, int kb, int lane) {
+    // Keys 64 kb .. 64 kb + 63 below the length, in the pages of these entries.
+    __device__ __forceinline__ void attend(const PagedKeys& c, int kb, int2 entries, int lane) {
         const int g = lane >> 4, lr = lane & 15;
         const int k0 = kb * kStepKeys, kl = c.kl;
-        // pages of the lane's V keys (sub-block g) and of its K rows (sub-block
-        // lr / 4); sub-blocks past the last token repeat the last one
-        const int last = (kl - 1) >> 4;
-        const int subv = min((k0 >> 4) + g, last), subk = min((k0 >> 4) + (lr >> 2), last);
-        int pv = c.table[subv * 16 / c.page], pk = c.table[subk * 16 / c.page];
+        const int2 piece = c.pieces(kb, lane);
+        const int shift = c.page_log2(), subv = piece.x, subk = piece.y;
+        int pv = entries.x, pk = entries.y;
         const bool seen = pv >= 0 && pv < c.n_pages;         // a missing page is masked and reads page 0
         pv = seen ? pv : 0;
         pk = pk >= 0 && pk < c.n_pages ? pk : 0;
         const size_t sv = (size_t)pv * c.HK + c.hk, sk = (size_t)pk * c.HK + c.hk;
         const float ksc = c.k_scale[sv] * c.scale_log2, vsc = c.v_scale[sv];
-        const uint8_t* kp = c.k_cache + sk * (size_t)c.page * D + (size_t)(subk * 16 % c.page + (lr & 3)) * D + g * (D / 4);
-        const uint8_t* vp = c.v_cache + sv * (size_t)c.page * D + (size_t)lr * c.page + subv * 16 % c.page;
+        const uint8_t* kp = c.k_cache + (sk << shift) * D + (size_t)((subk * 16 & (c.page - 1)) + (lr & 3)) * D + g * (D / 4);
+        const uint8_t* vp = c.v_cache + (sv << shift) * D + ((size_t)lr << shift) + (subv * 16 & (c.page - 1));
         uint32_t kw[4][KW];
         uint4 vw[ND];
 #pragma unroll
@@ -133,7 +146,7 @@ template <typename T, int D, int NR> struct CacheRows {
             }
         }
 #pragma unroll
-        for (int d = 0; d < ND; ++d) vw[d] = *reinterpret_cast<const uint4*>(vp + (size_t)(16 * d) * c.page);
+        for (int d = 0; d < ND; ++d) vw[d] = *reinterpret_cast<const uint4*>(vp + ((size_t)(16 * d) << shift));
         const int key0 = k0 + 16 * g, valid = seen ? kl - key0 : 0;  // this group's keys below the length
         if (!__all(valid >= 16)) {  // bytes past the last token may be anything, NaN codes among them
 #pragma unroll
@@ -195,6 +208,17 @@ template <typename T, int D, int NR> struct CacheRows {
 #pragma unroll
                     for (int p = 0; p < NP; ++p) o[d][n] = mma(vf, pf[u][n][p], o[d][n]);
             }
+    }
+
+    // Blocks first, first + by, .. below end.
+    __device__ __forceinline__ void attend(const PagedKeys& c, int first, int end, int by, int lane) {
+        if (first >= end) return;
+        int2 now = c.entries(first, lane);
+        for (int kb = first; kb < end; kb += by) {
+            const int2 next = c.entries(min(kb + by, end - 1), lane);
+            attend(c, kb, now, lane);
+            now = next;
+        }
     }
 };
 

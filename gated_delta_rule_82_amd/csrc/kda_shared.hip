@@ -226,7 +226,7 @@ __device__ __forceinline__ void narrow_rows(const AttnSharedArgs& a, const Work&
         kb0 = min(kb1, kb0 + w.part * per);
         kb1 = min(kb1, kb0 + per);
         const PagedKeys keys = keys_of(a, w, hi);
-        for (int kb = kb0 + wave; kb < kb1; kb += NW) x.attend(keys, kb, lane);
+        x.attend(keys, kb0 + wave, kb1, NW, lane);
     }
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
