@@ -65,7 +65,8 @@ struct PagedKeys {
         return make_int2(min(first + (lane >> 4), last), min(first + ((lane & 15) >> 2), last));
     }
     // their table entries, asked for a block ahead: one wait less a block (the decode step over 4096
-    // tokens 220 -> 216 us, one group's 32-row tiles on 4001 common keys 28 -> 27)
+    // tokens 220 -> 216 us, eight groups' 32-row tiles on 4001 common keys 28 -> 27; codes a block
+    // ahead as well take registers that more waves need: 42)
     __device__ __forceinline__ int2 entries(int kb, int lane) const {
         const int2 p = pieces(kb, lane);
         const int shift = page_log2() - 4;
