@@ -71,14 +71,16 @@ struct AttnSharedArgs {
 // themselves.  A wide tile reads and converts each key for more rows, but fills a
 // compute unit alone and pays its start and end once a workgroup: its workgroups have to
 // have enough steps.  In us, 32-row / 64-row / 128-row tiles, 8 key/value heads, D = 128:
-//   8 groups of 32 rows on 4096 keys     29   36   42     8 of 32 on 16384     63   73   89
-//   4 groups of 64 rows on 4096 keys     26   33   36     8 of 64 on 4096      46   43   48
-//   8 groups of 64 rows on 16384 keys    96   83   96     1 of 256 on 4096     24   32   37
-//   1 group of 128 rows on 32768 keys    50   47   48     1 of 256 on 32768    83   74   65
+//   8 groups of 32 rows on 4096 keys     26   35   41     8 of 32 on 16384     59   72   88
+//   4 groups of 64 rows on 4096 keys     24   31   33     8 of 64 on 4096      45   43   47
+//   8 groups of 64 rows on 16384 keys    88   85   96     1 of 256 on 4096     24   30   34
+//   1 group of 128 rows on 32768 keys    48   48   46     1 of 256 on 32768    76   74   63
 // where the 64-row tiles' workgroups have 8, 32, 4, 8, 32, 4, 16 and 32 steps each.  Each part of a
 // prefix is written and read again once, so there are only as many as give every
-// compute unit a workgroup (8 groups of 32 rows on 4096 keys: 29 us with 4 parts, 35 with 8); for
-// 32-row tiles twice as many where each keeps 1024 keys (on 16384 keys: 65 us with 4, 61 with 8).
+// compute unit a workgroup (8 groups of 32 rows on 4096 keys: 25 us with 4 parts, 31 with 8; on
+// 16384 keys 57 and 59); 32-row tiles that would have one or two get twice as many where each
+// keeps 1024 keys (32 groups on 4096 keys: 94 us with 1, 84 with 2; 16 on 16384: 156 with 2,
+// 126 with 4).
 struct SharedPlan {
     int wide;           // 0, or blocks of 32 rows of a tile: 2, 4
     int own_blocks;     // blocks of 16 rows of a sequence's own keys (of a tile too, if not wide)
@@ -108,7 +110,7 @@ inline SharedPlan shared_plan(int elem_bytes, int B, int Tq, int HK, int G, int 
     const long long wgs = tiles_of(br) * HK;
     p.nprefix = parts(wgs, 256, 256);
     const int more = parts(wgs, 512, 1024);
-    if (!p.wide && p.own_blocks == 2 && more > p.nprefix) p.nprefix = more;
+    if (!p.wide && p.own_blocks == 2 && p.nprefix <= 2 && more > p.nprefix) p.nprefix = more;
     p.nown = parts(own, 512, 256);
     p.blocks = (long long)HK * p.tiles * p.nprefix + own * p.nown;
     return p;
