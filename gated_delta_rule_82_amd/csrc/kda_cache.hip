@@ -298,7 +298,7 @@ constexpr int kStepWaves = 4;
 // turn and are joined in LDS; splits of a long cache are joined by kda_attn_join_kernel.  Nothing of the
 // cache is staged: every byte is used by one wave, and loads straight into the operands
 // leave the LDS and barriers out of the stream.  Bound by the bytes: 256 sequences of up
-// to 4096 tokens, 8 heads of 128 channels (1.21 GB), 32 query heads 218 us, 5.5 TB/s; one
+// to 4096 tokens, 8 heads of 128 channels (1.21 GB), 32 query heads 216 us, 5.6 TB/s; one
 // sequence of 65 536, four new tokens (134 MB) 27 us and 5.5 for the join of 128 parts.
 template <typename T, int D, int NR>
 __global__ __launch_bounds__(64 * kStepWaves) void kda_attn_step_kernel(const AttnStepArgs a) {

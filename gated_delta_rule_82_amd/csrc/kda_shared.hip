@@ -463,7 +463,7 @@ template <int D, int RB> struct WideRows {
 
 // fp32, D = 16, and groups of few rows: bound by memory and, in few parts, by the latency of
 // what four waves have in flight.  Eight groups of 8 sequences of 4 heads on 4001 common keys
-// (8 key/value heads, 200 own keys each; 83 MB): 28 us with the join, 2 more with eight waves
+// (8 key/value heads, 200 own keys each; 83 MB): 26 us with the join, 2 more with eight waves
 // a workgroup.
 template <typename T, int D, int NR>
 __global__ __launch_bounds__(64 * kSharedWaves) void kda_attn_shared_kernel(const AttnSharedArgs a) {
