@@ -65,8 +65,9 @@ kda_status kda_cache_reserve(int* table, int* refs, const int* cache_len, const 
                              int* src, int* dst, int* info, int B, int T, int max_pages, int n_pages,
                              int page, hipStream_t stream) {
     if (!page_ok(page) || T < 0 || !table_ok(B, max_pages, n_pages)) return KDA_ERR_SHAPE;
-    const int touched = kda::pages_touched(T, page);
-    if ((long long)B * touched >= (1ll << 30)) return KDA_ERR_SHAPE;
+    const int pages = kda::pages_touched(T, page), width = max_pages > 0 ? max_pages : 1;
+    if ((long long)B * pages >= (1ll << 30)) return KDA_ERR_SHAPE;
+    const int touched = pages < width ? pages : width;      // entries of a row that there are
     KDA_TRY(need(info));
     if (B > 0) {
         KDA_TRY(need(cache_len)); KDA_TRY(maybe(new_len)); KDA_TRY(need(src)); KDA_TRY(need(dst));

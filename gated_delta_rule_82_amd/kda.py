@@ -725,7 +725,7 @@ def attn_step(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_len, new
 def _ints(name, shape, given, dev):
     """The caller's int32 tensor of that shape, or a new one."""
     if given is None:
-        return torch.empty(shape, dtype=torch.int32, device=dev)
+        return torch.empty(shape if len(shape) > 1 else shape[0], dtype=torch.int32, device=dev)   # quicker without a tuple
     _expect(name, given, shape, torch.int32, dev)
     return given
 
@@ -915,7 +915,7 @@ def beam_select(logits, scores=None, M=None, *, done=None, end=-1, scores_out=No
         scores_out = torch.empty((R, M), dtype=torch.float32, device=dev)
     else:
         _expect("scores_out", scores_out, (R, M), torch.float32, dev)
-    parent = _ints("parent", (R, M), parent, dev)
+    parent = torch.empty_like(scores_out, dtype=torch.int32) if parent is None else _ints("parent", (R, M), parent, dev)
     token = _like(parent) if token is None else _ints("token", (R, M), token, dev)
     ws = _workspace(beam_select_workspace_bytes(_int32("R", R), _int32("K", K), _int32("V", V), M, dt), workspace, dev)
     _launch("kda_beam_select", dev, logits.data_ptr(), _ptr(scores), _ptr(done), _ptr(scores_out), _ptr(parent), _ptr(token),

@@ -116,6 +116,13 @@ def test_reserve_runs_out_of_pages():
     reserve(np.full((0, 3), -1), [], np.zeros(3, int), 1, page)                  # no sequences
 
 
+def test_reserve_for_more_tokens_than_a_row_holds():
+    """All entries behind the length, however many tokens are meant to come."""
+    for T in (100, 1 << 20, (1 << 31) - 1):
+        reserve(np.full((3, 4), -1), [0, 20, 70], np.zeros(20, int), T, 16)
+        reserve(np.full((3, 4), -1), [0, 20, 70], np.zeros(20, int), T, 16, [T, 3, 0])
+
+
 def test_reserve_leaves_a_page_whose_tokens_are_missing():
     table = np.array([[-1, -1, -1], [9, -1, -1], [1 << 30, 2, -1]])
     reserve(table, [5, 5, 20], np.array([0, 0, 1, 0]), 20, 16)
