@@ -93,8 +93,10 @@ __device__ __forceinline__ bool group_of_tile(const AttnSharedArgs& a, int& tile
 }
 
 // The number of a workgroup among those of the prefixes (common) or of own keys.  Half of the
-// latter go first and half last: what they read does not fit the memory's rate if all do so
-// at once, and the products of prefixes leave most of it idle.
+// latter go first and half last: all at once they are bound by memory, which the products
+// of prefixes leave idle for the most part.  With all of them behind the prefixes, 64 sequences
+// of 512 own keys on 32768 common ones took 78 us instead of 76, eight groups of eight 36
+// instead of 34.
 __device__ __forceinline__ int block_of(const AttnSharedArgs& a, bool& common) {
     const int bid = blockIdx.x, early = ((int)gridDim.x - a.prefix_blocks) / 2;
     common = bid >= early && bid < early + a.prefix_blocks;
