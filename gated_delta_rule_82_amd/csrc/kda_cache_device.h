@@ -47,6 +47,24 @@ __device__ __forceinline__ uint4 keep_bytes(uint4 v, int n) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Codes that are NaN become zeros; whether there were any.
+__device__ __forceinline__ bool drop_nan_codes(uint4& v) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w}, any = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t nan = ((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;    // 0x7f and 0xff only carry
+        w[i] &= ~(nan | (nan - (nan >> 7)));
+        any |= nan;
+    }
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+    return any != 0;
+}
+
+// NaN where bit i is set.
+__device__ __forceinline__ float nan_if(float x, uint32_t bits, int i) {
+    return __uint_as_float(__float_as_uint(x) | ((uint32_t)((int32_t)(bits << (31 - i)) >> 31) & 0x7fc00000u));
+}
+
 constexpr int kStepKeys = 64;   // keys of a wave's block: 16 for each lane group
 
 // The pages of one sequence and one key/value head.
@@ -87,10 +105,12 @@ template <typename T, int D, int NR> struct CacheRows {
     Frag<bf16_t> qf[NR][NS][NP];
     float m[NR], l[NR];
     floatx4 o[ND][NR];
+    uint32_t nans[NR];                         // this lane's elements of o (bit 4 d + e) that met a NaN code of v
 
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
+            nans[n] = 0u;
             m[n] = kNegInf;
             l[n] = 0.f;
 #pragma unroll
@@ -152,6 +172,21 @@ template <typename T, int D, int NR> struct CacheRows {
         if (!__all(valid >= 16)) {  // bytes past the last token may be anything, NaN codes among them
 #pragma unroll
             for (int d = 0; d < ND; ++d) vw[d] = keep_bytes(vw[d], valid);
+        }
+        // Zero times a NaN code is NaN too: where a row sees none of these keys, NaN codes are left out and noted for
+        // the rows that see some.
+        bool every = true;
+#pragma unroll
+        for (int n = 0; n < NR; ++n) every = every && lo[n] < k0 + kStepKeys && hi[n] >= k0;
+        if (!__all(every)) {
+            uint32_t mine = 0;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+                const uint64_t who = __ballot(drop_nan_codes(vw[d])), pair = who | who >> 32;
+                mine |= ((uint32_t)(pair | pair >> 16) >> (4 * g) & 15u) << (4 * d);
+            }
+#pragma unroll
+            for (int n = 0; n < NR; ++n) nans[n] |= lo[n] < k0 + kStepKeys && hi[n] >= k0 ? mine : 0u;
         }
 
         floatx4 st[4][NR];
@@ -220,6 +255,12 @@ template <typename T, int D, int NR> struct CacheRows {
             attend(c, kb, now, lane);
             now = next;
         }
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+            if (__any(nans[n] != 0)) {
+#pragma unroll
+                for (int i = 0; i < 4 * ND; ++i) o[i / 4][n][i % 4] = nan_if(o[i / 4][n][i % 4], nans[n], i);
+            }
     }
 };
 

@@ -339,7 +339,7 @@ template <int D, int RB> struct WideRows {
     template <bool VALUES, bool SCORES, typename Between>
     __device__ __forceinline__ void products(const unsigned char* v_codes, uint32_t v_place, uint32_t v_step, const Piece* v_pieces,
                                              int v_plain, int v_first, int end, const unsigned char* k_codes, const Piece* k_pieces,
-                                             const unsigned char* queries, int b, int lane, Between between) {
+                                             const unsigned char* queries, int b, const int2* bounds, uint32_t* nans, int lane, Between between) {
         const int h = lane >> 5, r = lane & 31, krow = 8 * (r >> 4) + 4 * ((r >> 3) & 1) + (r & 3), kp = 2 * b + ((r >> 2) & 1), vp = 2 * b + h;
         float v_scale = 1.f, k_scale = 1.f;
         // a granule's place is an exclusive or away from the first one's: two values are kept,
@@ -375,6 +375,15 @@ template <int D, int RB> struct WideRows {
                 if (!v_plain) {     // bytes past the end may be anything, NaN codes among them
                     asm volatile("" : "+v"(valid));
                     x = keep_bytes(x, valid);
+                    // left out for rows that see none of these keys, and noted for those that see some
+                    const uint64_t who = __ballot(drop_nan_codes(x));
+                    if (who != 0 && lane < 32) {
+#pragma unroll
+                        for (int n = 0; n < RB; ++n) {
+                            const int2 row = bounds[32 * n + lane];
+                            if (row.x < v_first + 32 && row.y >= v_first) atomicOr(nans + (32 * n + lane) * ND + k, (uint32_t)(who | who >> 32));
+                        }
+                    }
                 }
                 const Frag<bf16_t> v0 = scaled_frag(x.x, x.y, v_scale), v1 = scaled_frag(x.z, x.w, v_scale);
 #pragma unroll
@@ -490,8 +499,10 @@ __global__ __launch_bounds__(64 * kSharedWaves) void kda_attn_shared_kernel(cons
 // common keys (8 key/value heads, 512 own keys each): 69 us with the join, of which the steps
 // are 34 (the products alone would be 25 at the rate of a large product) and own keys 11.
 // On 32-row tiles 96 us.
+// Two workgroups a compute unit where the LDS holds them (tiles of 64 rows, D = 32, and D = 64 with few own rows, which
+// have 128 registers a lane then): 8 groups of 64 rows on 16384 keys, D = 64, 52 us instead of 60.
 template <int D, int RB, int NR>
-__global__ __launch_bounds__(512, 2) void kda_attn_shared_wide_kernel(const AttnSharedArgs a) {
+__global__ __launch_bounds__(512, RB == 1 && D * NR <= 64 ? 4 : 2) void kda_attn_shared_wide_kernel(const AttnSharedArgs a) {
     typedef bf16_t T;
     typedef StepCodes<D> S;
     constexpr int NW = 8, RW = 2, ND = D / 32, KW = NW / RW, NC = 2 * S::kCopies, BR = 32 * RB * RW, kChunk = kChunkPieces / kStepPieces;
@@ -506,6 +517,7 @@ __global__ __launch_bounds__(512, 2) void kda_attn_shared_wide_kernel(const Attn
     __shared__ float sml[NW][32][2];
     __shared__ int range[NW][2];
     __shared__ int2 bounds[BR];
+    __shared__ uint32_t nans[BR][ND];               // channels of a row that met a NaN code of v
     __shared__ uint2 place[BR];                     // of a row's part, and whether the row is there
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
     Work w;
@@ -560,7 +572,11 @@ __global__ __launch_bounds__(512, 2) void kda_attn_shared_wide_kernel(const Attn
 #pragma unroll
     for (int n = 0; n < RB; ++n) {
         const Row<T> row = row_of<T>(a, w, w.r0 + wr0 + 32 * n + (lane & 31), D);
-        if (kg == 0 && h == 0) bounds[wr0 + 32 * n + lane] = make_int2(row.lo, row.hi);
+        if (kg == 0 && h == 0) {
+            bounds[wr0 + 32 * n + lane] = make_int2(row.lo, row.hi);
+#pragma unroll
+            for (int d = 0; d < ND; ++d) nans[wr0 + 32 * n + lane][d] = 0u;
+        }
         if (kg == 1 && h == 0) {
             const int r = min(w.r0 + wr0 + 32 * n + lane, w.rows - 1);
             const size_t at = part_at(a, w, r);
@@ -695,7 +711,7 @@ __global__ __launch_bounds__(512, 2) void kda_attn_shared_wide_kernel(const Attn
                 __builtin_amdgcn_s_setprio(2);
                 x.template products<decltype(values)::value, decltype(scores)::value>(
                     sm + (3 + (place == 0 ? 2 : place - 1)) * kSide, v_place, v_step, now - kStepPieces, fine0, (s - 1) * 128 + 32 * kg, hi,
-                    sm + place * kSide, now, mine, kg, lane, between);
+                    sm + place * kSide, now, mine, kg, bounds + wr0, &nans[wr0][0], lane, between);
                 __builtin_amdgcn_s_setprio(0);
             } else {
 #pragma unroll
@@ -793,6 +809,9 @@ __global__ __launch_bounds__(512, 2) void kda_attn_shared_wide_kernel(const Attn
             floatx4 y = *reinterpret_cast<const floatx4*>(&buf[g][at32][ch]);
 #pragma unroll
             for (int v = 1; v < KW; ++v) y += *reinterpret_cast<const floatx4*>(&buf[v * RW + g][at32][ch]);
+            const uint32_t bad = nans[local][ch / 32] >> (ch % 32);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = nan_if(y[e], bad, e);
             *reinterpret_cast<floatx4*>(a.part_o + place_of(place[local]) * D + ch) = y;
         }
     }
