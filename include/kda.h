@@ -618,8 +618,11 @@ kda_status kda_cache_copy(const void* k_cache, const void* v_cache, const float*
  * are read through the row of the group's first sequence; the page in which a prefix
  * ends, of which every sequence has a copy (whose codes move as its scale grows), and
  * what follows through each sequence's own.  The result is that of kda_attn_step up to
- * the order of its sums.  Everything else as there; a sequence of no group has no prefix,
- * one whose length is below the prefix sees no further than its length.
+ * the order of its sums and, in bf16, the rounding of probabilities: where groups have
+ * more than 32 rows they may be relative to a maximum that lies a factor 2 below the row's,
+ * and are then divided by the sum of the rounded ones.  Everything else as there; a
+ * sequence of no group has no prefix, one whose length is below the prefix sees no
+ * further than its length.
  *   group_first [n_groups+1] int, not descending (values outside 0 .. B are clamped);
  *   prefix_len [n_groups] int (clamped to the table).
  *   workspace  kda_attn_shared_workspace(B, Tq, H, HK, D, n_groups, max_pages * page)
