@@ -17,9 +17,12 @@ constexpr int kSegments = 8;      // of a part: each thread keeps the maximum of
 constexpr int kJoinThreads = 512;
 constexpr int kUnroll = 4;        // 16-byte loads of a thread in flight; a segment is a multiple of them
 constexpr int kFound = 1024;      // candidates of a part that are ranked
+// A thread's sum of exponentials is relative to a value that its logits exceed by no more than this: sums of rows that
+// rise slowly are not multiplied by a rounded factor for every group of loads.
+constexpr float kRefSlack = 4.f;
 
-// e^d of a difference d <= 0 in a sum that has a term of 1: the rounding of d log2 e is off
-// by |d| 2^-24 of the term, at most 2^-25 of the sum.
+// e^d for differences |d| of a few units: off by 2^-23 of itself (the instruction) and 1.3 |d| 2^-24 (the rounding of
+// d log2 e, and kLog2e's own).
 __device__ __forceinline__ float exp_term(float d) { return exp2_fast(d * kLog2e); }
 
 // Order of values as that of unsigned integers; -0 is +0.
@@ -83,7 +86,9 @@ __device__ __forceinline__ bool beam_lives(const SelectArgs& a, int row) {
 // of what it reads, and the maxima of its segments.  The M-th largest of the maxima of
 // pairs of threads bounds the M first from below; only segments that reach it are read again (a
 // few of 2048, from the cache nearby) and what reaches it there, usually little more
-// than M values, is ranked by counting.
+// than M values, is ranked by counting.  Sums are relative to a maximum of the thread's own, in 64
+// bits beyond a group of loads: errors of equal terms do not cancel (one large logit above 2^20 equal
+// ones: up to 9e-6 off with fp32 sums and one factor for all threads' terms, 3e-7 at most now).
 // Bound by reading the logits: 512 rows of 131072 bf16 (134 MB) take 34 us, 4.0 TB/s over all
 // and 26 us at the rate of a copy; the rest is the start and the selection, which all
 // parts do at the same time.  An exponential with its argument's rounding carried along
@@ -110,7 +115,8 @@ __global__ __launch_bounds__(kSelThreads) void kda_select_part_kernel(const Sele
 
     // A group is loaded while the one before is summed.  Behind the last whole 16 bytes a
     // thread takes the row's last ones instead and drops those that are not its own.
-    float m = kNegInf, l = 0.f, best = kNegInf;
+    float m = kNegInf, ref = kNegInf, best = kNegInf;
+    double l = 0.0;                 // sum of e^(x - ref)
     auto fetch = [&](Vec<T> (&v)[kUnroll], int g) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
@@ -133,15 +139,21 @@ __global__ __launch_bounds__(kSelThreads) void kda_select_part_kernel(const Sele
                 for (int e = 0; e < N; ++e) y[e % 4] = fmaxf(y[e % 4], value(u, e));
             const float z = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
             best = fmaxf(best, z);
-            const float now = fmaxf(m, z), mu = now == kNegInf ? 0.f : now;
-            l *= exp_term(m - mu);
-            m = now;
-            float part[4] = {0.f, 0.f, 0.f, 0.f};
+            m = fmaxf(m, z);
+            if (z > ref + kRefSlack) {
+                l *= (double)exp_term(ref - z);
+                ref = z;
+            }
+            const float mu = ref == kNegInf ? 0.f : ref;
+            // pairs, pairs of pairs and so on: at most five roundings meet a term
+            float part[kUnroll * N];
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u)
+            for (int i = 0; i < kUnroll * N; ++i) part[i] = exp_term(value(i / N, i % N) - mu);
 #pragma unroll
-                for (int e = 0; e < N; ++e) part[e % 4] += exp_term(value(u, e) - mu);
-            l += (part[0] + part[1]) + (part[2] + part[3]);
+            for (int w = 1; w < kUnroll * N; w *= 2)
+#pragma unroll
+                for (int i = 0; i < kUnroll * N; i += 2 * w) part[i] += part[i + w];
+            l += (double)part[0];
         };
         if (whole) both([&](int u, int e) { return v[u][e]; });
         else both(value);
@@ -171,7 +183,7 @@ __global__ __launch_bounds__(kSelThreads) void kda_select_part_kernel(const Sele
     float all = fmaxf(top0, top1);
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor(all, o, 64));
-    double sum = (double)l * (double)exp_term(m - (all == kNegInf ? 0.f : all));
+    double sum = l == 0.0 ? 0.0 : l * exp((double)ref - (double)all);
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
     if (lane == 0) sums[wave] = sum;
