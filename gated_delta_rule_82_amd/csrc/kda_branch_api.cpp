@@ -138,9 +138,10 @@ kda_status kda_cache_copy(const void* k_cache, const void* v_cache, const float*
 
 static bool shared_sizes_ok(int B, int Tq, int H, int HK, int D, int n_groups, int max_len) {
     if (n_groups < 0 || n_groups > (1 << 16) || !step_sizes_ok(B, Tq, H, HK, max_len)) return false;
-    // packed rows of all sequences, and the workgroups of one launch
+    // packed rows of all sequences, the workgroups of one launch, and the threads of the join behind it (four
+    // channels each where there are few parts; with many there are few rows)
     if (H == 0) return true;
-    return (unsigned long long)B * Tq * (H / HK) <= (1ull << 29) &&
+    return (unsigned long long)B * Tq * H * (D / 4) + 255 < (1ull << 32) && (unsigned long long)B * Tq * (H / HK) <= (1ull << 29) &&
            kda::shared_plan(4, B, Tq, HK, H / HK, D, n_groups, max_len).blocks < (1ll << 23) &&
            kda::shared_plan(2, B, Tq, HK, H / HK, D, n_groups, max_len).blocks < (1ll << 23);
 }

@@ -627,8 +627,9 @@ kda_status kda_cache_copy(const void* k_cache, const void* v_cache, const float*
  *   prefix_len [n_groups] int (clamped to the table).
  *   workspace  kda_attn_shared_workspace(B, Tq, H, HK, D, n_groups, max_pages * page)
  *        bytes, 256-byte aligned: partial results of prefixes and of own keys.
- * Sizes as there, and n_groups up to 2^16, B * Tq * (H / HK) up to 2^29; below 2^23 workgroups (about 16 rows
- * each, for groups and sequences, times the parts that fill the card).  Errors as kda_attn_step. */
+ * Sizes as there, and n_groups up to 2^16, B * Tq * (H / HK) up to 2^29, B * Tq * H * D below 2^34;
+ * below 2^23 workgroups (about 16 rows each, for groups and sequences, times the parts that fill the card).
+ * Errors as kda_attn_step. */
 size_t kda_attn_shared_workspace(int B, int Tq, int H, int HK, int D, int n_groups, int max_len);
 kda_status kda_attn_shared(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
                            const float* v_scale, const int* block_table, const int* cache_len,
