@@ -45,7 +45,7 @@ kda_status kda_cache_fork(const int* table, const int* cache_len, const int* par
     if (!page_ok(page) || R < 0 || K_in < 0 || K_in > 1024 || K_out < 0 || K_out > 1024 ||
         !table_ok((long long)R * K_in, max_pages, n_pages) || !table_ok((long long)R * K_out, max_pages, n_pages))
         return KDA_ERR_SHAPE;
-    if (R == 0 || (K_in == 0 && K_out == 0)) return KDA_OK;
+    if (R == 0 || (K_out == 0 && (K_in == 0 || max_pages == 0))) return KDA_OK;    // no entry and no length to write
     const unsigned long long n_in = (unsigned long long)R * K_in, n_out = (unsigned long long)R * K_out;
     if (n_in > 0) KDA_TRY(need(cache_len));
     if (n_out > 0) { KDA_TRY(need(parent)); KDA_TRY(need(len_out)); }
