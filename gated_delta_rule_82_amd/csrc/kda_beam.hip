@@ -314,8 +314,11 @@ __global__ __launch_bounds__(kSelThreads) void kda_select_part_kernel(const Sele
 // a few held all the best: a thousand candidates to rank instead of a hundred.
 __global__ __launch_bounds__(kJoinThreads) void kda_select_join_kernel(const SelectArgs a) {
     __shared__ uint64_t key[kSelectHeld];
-    __shared__ uint32_t token[kSelectHeld];
-    __shared__ uint64_t list_key[kSelectHeld], list_id[kSelectHeld];    // beam << 32 | token
+    __shared__ uint32_t token[kSelectHeld], logit[kSelectHeld];         // logit: the largest first
+    // Order of equal scores: beam, then logit (a score rounds away what logits near zero differ by), then
+    // candidate, which is by token where logits are equal: 6, 32 and 12 bits.
+    __shared__ uint64_t list_key[kSelectHeld], list_id[kSelectHeld];
+    static_assert(kSelectHeld == 1 << 12 && kSelectMost == 1 << 6, "bits of list_id");
     __shared__ uint32_t top[128];
     __shared__ int n_list;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = blockIdx.x;
@@ -350,7 +353,7 @@ __global__ __launch_bounds__(kJoinThreads) void kda_select_join_kernel(const Sel
         }
         for (int i = lane; i < per; i += 64) {
             uint64_t y = 0;
-            uint32_t w = 0;
+            uint32_t w = 0, x = 0;
             if (lives) {
                 double s = -__builtin_inf();
                 if (done) {
@@ -361,14 +364,17 @@ __global__ __launch_bounds__(kJoinThreads) void kda_select_join_kernel(const Sel
                 } else {
                     const int next = i < 64 ? w0 : a.part_w[part * a.M + i];
                     if (next >= 0) {
-                        s = (double)score0 + ((double)(i < 64 ? x0 : a.part_x[part * a.M + i]) - lse);
+                        const float value = i < 64 ? x0 : a.part_x[part * a.M + i];
+                        s = (double)score0 + ((double)value - lse);
                         w = (uint32_t)next;
+                        x = ~order_key(value);
                     }
                 }
                 if (s - s == 0.0) y = order_key(s);   // what is not finite is no continuation
             }
             key[k * per + i] = y;
             token[k * per + i] = w;
+            logit[k * per + i] = x;
             // one of 128 sets, not by the rank in the part
             if (y) atomicMax(&top[((uint32_t)(k * per + i) * 0x9e3779b1u) >> 25], (uint32_t)(y >> 32));
         }
@@ -380,7 +386,7 @@ __global__ __launch_bounds__(kJoinThreads) void kda_select_join_kernel(const Sel
         if ((uint32_t)(key[i] >> 32) >= t) {
             const int p = atomicAdd(&n_list, 1);
             list_key[p] = key[i];
-            list_id[p] = (uint64_t)(i / per) << 32 | token[i];
+            list_id[p] = (uint64_t)(i / per) << 44 | (uint64_t)logit[i] << 12 | (uint32_t)i;
         }
     __syncthreads();
     const int n = n_list;
@@ -392,8 +398,8 @@ __global__ __launch_bounds__(kJoinThreads) void kda_select_join_kernel(const Sel
         if (rank < a.M) {
             const size_t at = (size_t)r * a.M + rank;
             a.scores_out[at] = (float)key_value(y);
-            a.parent[at] = (int)(w >> 32);
-            a.token[at] = (int)(uint32_t)w;
+            a.parent[at] = (int)(w >> 44);
+            a.token[at] = (int)token[w & (kSelectHeld - 1)];
         }
     }
     for (int i = n + tid; i < a.M; i += kJoinThreads) {

@@ -149,13 +149,13 @@ def beam_select(logits, scores, M, done=None, end=-1):
     R, K, V = logits.shape
     out, parent, token = np.full((R, M), -np.inf), np.full((R, M), -1, np.int32), np.full((R, M), -1, np.int32)
     for r in range(R):
-        s, b, w = [], [], []
+        s, b, w, l = [], [], [], []
         for k in range(K):
             score = 0.0 if scores is None else float(scores[r, k])
             if not np.isfinite(score):
                 continue
             if done is not None and done[r, k]:
-                s.append(np.array([score])), b.append(np.array([k])), w.append(np.array([end]))
+                s.append(np.array([score])), b.append(np.array([k])), w.append(np.array([end])), l.append(np.zeros(1))
                 continue
             x = logits[r, k]
             if np.isnan(x).any() or np.isposinf(x).any():
@@ -165,11 +165,11 @@ def beam_select(logits, scores, M, done=None, end=-1):
                 continue
             top = x.max()
             y = score + (x[at] - (top + np.log(np.exp(x[at] - top).sum())))
-            s.append(y), b.append(np.full(len(at), k)), w.append(at)
+            s.append(y), b.append(np.full(len(at), k)), w.append(at), l.append(x[at])
         if not s:
             continue
-        s, b, w = np.concatenate(s), np.concatenate(b), np.concatenate(w)
-        order = np.argsort(-s, kind="stable")[:M]
+        s, b, w, l = np.concatenate(s), np.concatenate(b), np.concatenate(w), np.concatenate(l)
+        order = np.lexsort((w, -l, b, -s))[:M]      # a beam's logits decide where rounded scores do not
         n = len(order)
         out[r, :n], parent[r, :n], token[r, :n] = s[order], b[order], w[order]
     return out, parent, token

@@ -1,4 +1,5 @@
-"""The selection's log-sum-exp where errors of equal terms add up."""
+"""The selection where scores meet the end of their precision: errors of equal terms that add up in lse, logits
+whose scores are equal in 64 bits, scores past fp32's range."""
 
 import math
 
@@ -72,3 +73,20 @@ def test_a_row_that_rises_slowly(V, rise):
     top = float(x[0, 0, -1].double())
     assert int(token[0, 0]) == V - 1
     assert abs(float(s[0, 0]) - (float(torch.tensor(lse).double()) - lse + top)) <= 2e-6 + 2.0 ** -24 * top
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V", [300, 20001])
+@pytest.mark.parametrize("M", [1, 2, 3, 5, 20])
+def test_logits_whose_scores_are_equal(dtype, V, M):
+    """Logits so small that 64 bits do not tell their scores apart: within a beam in the order of the logits, whatever
+    the number of picks."""
+    x = torch.zeros(1, 2, V, dtype=dtype)
+    x[0, :, V - 9], x[0, :, 50], x[0, :, 0] = 2e-20, 1e-20, -1e-20
+    s, parent, token = kda.beam_select(x.cuda(), torch.tensor([[0.0, -1.0]], device="cuda"), M)
+    torch.cuda.synchronize()
+    want = [V - 9, 50] + [w for w in range(1, 30) if w != 50]
+    assert parent[0].tolist() == [0] * M and token[0].tolist() == want[:M]
+    s, parent, token = kda.beam_select(x.cuda(), None, M)       # equal beams: the first one's all come first
+    torch.cuda.synchronize()
+    assert parent[0].tolist() == [0] * M and token[0].tolist() == want[:M]
