@@ -370,7 +370,8 @@ __global__ __launch_bounds__(kJoinThreads) void kda_select_join_kernel(const Sel
                         x = ~order_key(value);
                     }
                 }
-                if (s - s == 0.0) y = order_key(s);   // what is not finite is no continuation
+                const float rounded = (float)s;
+                if (rounded - rounded == 0.f) y = order_key(s);   // what is not finite in fp32 is no continuation
             }
             key[k * per + i] = y;
             token[k * per + i] = w;

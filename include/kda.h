@@ -662,11 +662,12 @@ kda_status kda_state_reorder(const void* state, void* out, const int* parent, in
  *            (a token, 0 .. V-1), with its score unchanged, whatever its logits are.
  *   scores_out [R,M] fp32, parent, token [R,M] int.  Where fewer than M continuations
  *            have a score above -infinity the rest is -infinity, -1, -1.
- * Logits of -infinity are no continuations; a beam with a NaN or +infinity has none.
- * Continuations are compared in 64 bits and their scores rounded once.  lse is good to
- * about 1e-7 (exponentials are fp32, sums of 32 of them and more 64 bits); at worst, where
- * many logits of one value make up a row's sum beside larger ones, it is off by 2e-6 (V up to
- * 2^20, 3e-6 up to 2^30).  K, M up to 64, V up to 2^30, R * K below 2^18.
+ * Logits of -infinity are no continuations, nor is one whose score fp32 rounds to
+ * -infinity; a beam with a NaN or +infinity has none.  Continuations are compared in 64
+ * bits and their scores rounded once.  lse is good to about 1e-7 (exponentials are fp32,
+ * sums of more than 32 of them 64 bits); at worst, where many logits of one value make up a
+ * row's sum beside larger ones, it is off by 2e-6 (V up to 2^20; 3e-6 up to 2^30).
+ * K, M up to 64, V up to 2^30, R * K below 2^18.
  *   workspace  kda_beam_select_workspace bytes, 256-byte aligned.
  * Outputs may overlap no other buffer.  Errors: KDA_ERR_DTYPE, KDA_ERR_SHAPE,
  * KDA_ERR_NULL, KDA_ERR_ALIGN, KDA_ERR_WORKSPACE, KDA_ERR_HIP. */

@@ -165,7 +165,8 @@ def beam_select(logits, scores, M, done=None, end=-1):
                 continue
             top = x.max()
             y = score + (x[at] - (top + np.log(np.exp(x[at] - top).sum())))
-            s.append(y), b.append(np.full(len(at), k)), w.append(at), l.append(x[at])
+            fits = np.abs(y) < 2.0 ** 128 - 2.0 ** 103      # what fp32 rounds to -infinity is none
+            s.append(y[fits]), b.append(np.full(fits.sum(), k)), w.append(at[fits]), l.append(x[at[fits]])
         if not s:
             continue
         s, b, w, l = np.concatenate(s), np.concatenate(b), np.concatenate(w), np.concatenate(l)

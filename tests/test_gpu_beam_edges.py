@@ -7,6 +7,7 @@ import pytest
 import torch
 
 from gated_delta_rule_82_amd import kda
+from tests.test_gpu_beam import check
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +91,17 @@ def test_logits_whose_scores_are_equal(dtype, V, M):
     s, parent, token = kda.beam_select(x.cuda(), None, M)       # equal beams: the first one's all come first
     torch.cuda.synchronize()
     assert parent[0].tolist() == [0] * M and token[0].tolist() == want[:M]
+
+
+def test_scores_past_the_range_of_fp32():
+    """A continuation whose score would be rounded to -infinity is none."""
+    x = torch.zeros(1, 2, 40)
+    x[0, :, 5:] = -2e38
+    x[0, 1, 5:9] = -5e37
+    s, parent, _ = check(x, torch.tensor([[-3e38, -2.5e38]]), 20)
+    assert int((parent >= 0).sum()) == 5 + 5 + 4 and bool(torch.isfinite(s[parent >= 0]).all())
+    for dtype in (F32, BF16):       # what the type's lowest value masks, twice
+        x = torch.full((1, 1, 40), torch.finfo(dtype).min, dtype=dtype)
+        x[0, 0, 3] = 1.0
+        s, parent, token = check(x, torch.tensor([[torch.finfo(F32).min]]), 4)
+        assert token[0].tolist() == [3, -1, -1, -1]
