@@ -177,7 +177,7 @@ template <typename T, int D, int NR> struct CacheRows {
         // the rows that see some.
         bool every = true;
 #pragma unroll
-        for (int n = 0; n < NR; ++n) every = every && lo[n] < k0 + kStepKeys && hi[n] >= k0;
+        for (int n = 0; n < NR; ++n) every = every && (hi[n] < 0 || (lo[n] < k0 + kStepKeys && hi[n] >= k0));   // < 0: a row that is not there
         if (!__all(every)) {
             uint32_t mine = 0;
 #pragma unroll

@@ -367,7 +367,17 @@ template <int D, int RB> struct WideRows {
         }
         if constexpr (SCORES) k_scale = k_pieces[kp].k_power;
         int valid = 16;
-        if (VALUES && !v_plain) valid = v_pieces[vp].there() ? end - v_first - 16 * h : 0;
+        int hidden = 0;         // some row that is there sees none of these keys
+        if (VALUES && !v_plain) {
+            valid = v_pieces[vp].there() ? end - v_first - 16 * h : 0;
+            bool none = false;
+#pragma unroll
+            for (int n = 0; n < RB; ++n) {
+                const int2 row = bounds[32 * n + r];
+                none = none || (row.y >= 0 && (row.x >= v_first + 32 || row.y < v_first));
+            }
+            hidden = __any(none) ? 1 : 0;
+        }
 #pragma unroll
         for (int k = 0; k < ND; ++k) {
             uint4 kw;
@@ -388,13 +398,16 @@ template <int D, int RB> struct WideRows {
                 if (!v_plain) {     // bytes past the end may be anything, NaN codes among them
                     asm volatile("" : "+v"(valid));
                     x = keep_bytes(x, valid);
-                    // left out for rows that see none of these keys, and noted for those that see some
-                    const uint64_t who = __ballot(drop_nan_codes(x));
-                    if (who != 0 && lane < 32) {
+                    // Zero times a NaN code is NaN too: left out for rows that see none of these keys, and noted for those
+                    // that see some.
+                    if (hidden) {
+                        const uint64_t who = __ballot(drop_nan_codes(x));
+                        if (who != 0 && lane < 32) {
 #pragma unroll
-                        for (int n = 0; n < RB; ++n) {
-                            const int2 row = bounds[32 * n + lane];
-                            if (row.x < v_first + 32 && row.y >= v_first) atomicOr(nans + (32 * n + lane) * ND + k, (uint32_t)(who | who >> 32));
+                            for (int n = 0; n < RB; ++n) {
+                                const int2 row = bounds[32 * n + lane];
+                                if (row.x < v_first + 32 && row.y >= v_first) atomicOr(nans + (32 * n + lane) * ND + k, (uint32_t)(who | who >> 32));
+                            }
                         }
                     }
                 }
