@@ -89,10 +89,10 @@ __device__ __forceinline__ bool beam_lives(const SelectArgs& a, int row) {
 // than M values, is ranked by counting.  Sums are relative to a maximum of the thread's own, in 64
 // bits beyond a group of loads: errors of equal terms do not cancel (one large logit above 2^20 equal
 // ones: up to 9e-6 off with fp32 sums and one factor for all threads' terms, 3e-7 at most now).
-// Bound by reading the logits: 512 rows of 131072 bf16 (134 MB) take 34 us, 4.0 TB/s over all
-// and 26 us at the rate of a copy; the rest is the start and the selection, which all
-// parts do at the same time.  An exponential with its argument's rounding carried along
-// costs twice the instructions of one difference and took 41 us, groups of eight loads
+// Bound by reading the logits: 512 rows of 131072 bf16 (134 MB) from memory take 34 us, 3.9 TB/s over all (30
+// where part of them is in the last-level cache) and 26 us at the rate of a copy; the rest is the start and
+// the selection, which all parts do at the same time.  An exponential with its argument's rounding carried along
+// costs twice the instructions of one difference (41 us when the kernel took 34 like now), groups of eight loads
 // a register too many for four workgroups a CU (48 us).  4 rows of 32000 fp32: 6.7 us.
 template <typename T>
 __global__ __launch_bounds__(kSelThreads) void kda_select_part_kernel(const SelectArgs a) {
@@ -310,7 +310,7 @@ __global__ __launch_bounds__(kSelThreads) void kda_select_part_kernel(const Sele
 // upper halves of their keys) and ranked by counting.  A wave has a beam: what a beam
 // that lives no longer, or one at its end, has in the parts is whatever was there before.
 // Bound by waits one after the other: 64 requests of 8 beams, 2 parts and 16 candidates
-// take 5 us, 64 beams of 64 candidates 15.  Sets by thread were sets by rank, of which
+// take 5 us, 64 beams of 64 candidates 17.  Sets by thread were sets by rank, of which
 // a few held all the best: a thousand candidates to rank instead of a hundred.
 __global__ __launch_bounds__(kJoinThreads) void kda_select_join_kernel(const SelectArgs a) {
     __shared__ uint64_t key[kSelectHeld];

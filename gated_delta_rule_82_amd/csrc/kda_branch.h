@@ -69,22 +69,42 @@ struct AttnSharedArgs {
 // How a call is divided: tiles of 64 or 128 rows of a group (bf16, D >= 32) over steps of
 // 128 keys copied into LDS, or of 16 or 32 rows whose keys four waves read for
 // themselves.  A wide tile reads and converts each key for more rows, but fills a
-// compute unit alone and pays its start and end once a workgroup: its workgroups have to
-// have enough steps.  In us, 32-row / 64-row / 128-row tiles, 8 key/value heads, D = 128:
-//   8 groups of 32 rows on 4096 keys     26   35   41     8 of 32 on 16384     59   72   88
-//   4 groups of 64 rows on 4096 keys     24   31   33     8 of 64 on 4096      45   43   47
-//   8 groups of 64 rows on 16384 keys    88   85   96     1 of 256 on 4096     24   30   34
-//   1 group of 128 rows on 32768 keys    48   48   46     1 of 256 on 32768    76   74   63
-// where the 64-row tiles' workgroups have 8, 32, 4, 8, 32, 4, 16 and 32 steps each.  Each part of a
-// prefix is written and read again once, so there are only as many as give every
-// compute unit a workgroup (8 groups of 32 rows on 4096 keys: 25 us with 4 parts, 31 with 8; on
-// 16384 keys 57 and 59); 32-row tiles that would have one or two get twice as many where each
-// keeps 1024 keys (32 groups on 4096 keys: 94 us with 1, 84 with 2; 16 on 16384: 156 with 2,
-// 126 with 4).
+// compute unit alone (D = 128) and pays its start and end once a workgroup: its workgroups
+// have to have enough steps.  Lengths are on the device: steps and parts are counted for
+// prefixes that fill the table, and for groups as large as the average.  In us a call, 32-row /
+// 64-row / 128-row tiles, 8 key/value heads, 200 own keys a sequence, tables as long as that:
+//   groups of rows on keys     D = 128           D = 64            D = 32
+//    8 of  32 on  4096       27   33            20   22           18   20
+//    8 of  32 on 16384       65   73            46   47           38   42
+//    4 of  64 on  4096       26   31   33       20   20   27      18   18   24
+//    8 of  64 on  4096       47   47   51       29   24   37      23   21   32
+//    8 of  64 on 16384       99   94  103       68   52   75      50   42   63
+//    1 of 128 on 32768       49   48   45       39   30   35      37   28   31
+//   16 of 128 on  4096      148  145  134       90   75   92      63   49   69
+//    1 of 256 on  4096       25   30   33       20   20   27      18   18   23
+//    1 of 256 on 16384       51   49   45       40   31   35      37   28   31
+//    1 of 256 on 32768       86   75   62       68   47   47      64   43   41
+//    4 of 256 on  4096       81   79   76       47   35   50      36   30   41
+//    4 of 256 on 16384      160  158  129      118   84   87      89   74   73
+// where the 64-row tiles' workgroups have 8, 32, 4, 8, 32, 16, 34, 4, 16, 32, 17 and 65 steps, 128-row tiles'
+// half as many where groups have more rows (12 is between the 8 and 16 steps of the D = 128 lines:
+// 8 would win up to 8 % there, and lose at D <= 64).  The rule is a compromise: 16 of 128 on 4096 at
+// D = 64 and 32 would be quicker on 64-row tiles.  A table far longer than the prefixes is taken for long
+// prefixes: 1 of 256 on 4096 takes 25 us with a table of 4608 tokens, 33 with one of 32768 or 131072.
+// Own keys, and groups of 16 rows or fewer, have 16-row blocks: 8 groups of 16 rows on 4096 keys 22 us (32-row
+// blocks 25), of 20 rows 28 (25); 64 samples of 20 own rows 96 (84).  Each part of a prefix is
+// written and read again once, so there are only as many as give every
+// compute unit a workgroup (8 groups of 32 rows on 4096 keys: 27 us with 4 parts, 33 with 8 or 2;
+// on 16384 keys 65, 67 and 98); 32-row tiles that would have one or two get twice as many where each
+// keeps 1024 keys (32 groups on 4096 keys, 60 own: 99 us with 1, 91 with 2, and 94 and 99 with 200 own; 16 on
+// 16384, 60 own: 145 with 2, 123 with 4, and 122 and 127 with 200 own).  Own keys get parts of at least 256 keys up
+// to two workgroups a compute unit: 512 own keys behind 32768 common ones 70 us, 71 with one workgroup, 76 with
+// four; but 2 groups of 8 sequences with 2000 own keys 31, 25 with one workgroup.  Parts of 128 or 512 keys: no
+// difference.
 struct SharedPlan {
     int wide;           // 0, or blocks of 32 rows of a tile: 2, 4
     int own_blocks;     // blocks of 16 rows of a sequence's own keys (of a tile too, if not wide)
-    int tiles, nprefix, nown;
+    int tiles, nprefix, nown;       // tiles: at most; one too many for each group whose rows fill its own
     long long blocks;   // workgroups, at most
 };
 inline SharedPlan shared_plan(int elem_bytes, int B, int Tq, int HK, int G, int D, int n_groups, int max_len) {
@@ -134,10 +154,9 @@ constexpr int select_part(int V, int n, int per_load) {
     const int step = kSelThreads * per_load, per = (V + n - 1) / n;
     return (per + step - 1) / step * step;
 }
-// Parts of a row: about 1024 workgroups (512 rows of 131072 bf16 take 54 us in 512, 43 in 1024,
-// 45 in 2048), at least 4096 elements each (32 rows of 65536 fp32 take 12 us, 15 with
-// twice as many parts of 2048), and no more
-// candidates than the join holds (a wave joins a beam's parts).
+// Parts of a row: about 1024 workgroups (512 rows of 131072 bf16 from memory take 53 us a call in 512, 40 in
+// 1024, 44 in 2048 and 47 in 4096), at least 4096 elements each (32 rows of 65536 fp32 take 16 us a call, 19 with
+// twice as many parts of 2048), and no more candidates than the join holds (a wave joins a beam's parts).
 inline int select_splits(int elem_bytes, int R, int K, int V, int M) {
     const long long rows = (long long)R * K;
     long long n = rows > 0 ? 1024 / rows : 1;

@@ -95,8 +95,8 @@ __device__ __forceinline__ bool group_of_tile(const AttnSharedArgs& a, int& tile
 // The number of a workgroup among those of the prefixes (common) or of own keys.  Half of the
 // latter go first and half last: all at once they are bound by memory, which the products
 // of prefixes leave idle for the most part.  With all of them behind the prefixes, 64 sequences
-// of 512 own keys on 32768 common ones took 78 us instead of 76, eight groups of eight 36
-// instead of 34.
+// of up to 512 own keys on 32768 common ones take 74 us instead of 71, eight groups of eight 30
+// instead of 26.
 __device__ __forceinline__ int block_of(const AttnSharedArgs& a, bool& common) {
     const int bid = blockIdx.x, early = ((int)gridDim.x - a.prefix_blocks) / 2;
     common = bid >= early && bid < early + a.prefix_blocks;
@@ -117,8 +117,8 @@ __device__ __forceinline__ bool work_of(const AttnSharedArgs& a, int lane, Work&
     if (w.common) {
         w.hk = bid % a.HK;
         bid /= a.HK;
-        // tiles go slowest: the ones past the last, of which there may be as many as groups,
-        // come after all others and leave no compute unit waiting
+        // tiles go slowest: the ones past the last, of which there may be as many as groups, come behind all
+        // others; half of the own keys' workgroups come behind them, and wait while they look for a group
         w.part = bid % a.nprefix;
         int tile = bid / a.nprefix;
         w.parts = a.nprefix;
@@ -526,9 +526,9 @@ __global__ __launch_bounds__(64 * kSharedWaves) void kda_attn_shared_kernel(cons
 // Bound by issue: a step of 128 keys for 128 rows of D = 128 is 64 products (2048 cycles of a
 // SIMD) beside as many cycles of conversions, exponentials and sums that the products of
 // the other wave hide in part only; it takes about 5000.  64 sequences of 4 heads on 32768
-// common keys (8 key/value heads, 512 own keys each): 69 us with the join, of which the steps
-// are 34 (the products alone would be 25 at the rate of a large product) and own keys 11.
-// On 32-row tiles 96 us.
+// common keys (8 key/value heads, up to 512 own keys each): 68 us and 7 of the join (70 a call among
+// others), of which the steps are 34 (the products alone would be 25 at the rate of a large product)
+// and own keys 11.  On 32-row tiles 96 us.
 // Two workgroups a compute unit where the LDS holds them (tiles of 64 rows, D = 32, and D = 64 with few own rows, which
 // have 128 registers a lane then): 8 groups of 64 rows on 16384 keys, D = 64, 52 us instead of 60.
 template <int D, int RB, int NR>

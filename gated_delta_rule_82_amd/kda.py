@@ -841,7 +841,8 @@ def attn_shared(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_len, g
                 scale=None, window=0, o=None, workspace=None):
     """kda_attn_shared: attn_step where the sequences group_first[g] .. group_first[g+1]-1
     (int32 [n_groups+1]) have their first prefix_len[g] tokens (int32 [n_groups]) in common:
-    their whole pages are read once a group, through its first sequence's row of block_table.
+    their whole pages are read once a group, through its first sequence's row of block_table,
+    which has to name them as long as any sequence of the group sees them.
     Returns o [B,Tq,H,D]."""
     B, Tq, H, D = q.shape
     _int32("window", window)
@@ -894,7 +895,7 @@ def beam_select_workspace_bytes(R, K, V, M, dtype=torch.bfloat16) -> int:
 def beam_select(logits, scores=None, M=None, *, done=None, end=-1, scores_out=None, parent=None, token=None, workspace=None):
     """kda_beam_select: the M (None: K) best continuations of each request over its K beams
     and V tokens, by scores [R,K] fp32 (None: 0) + log-softmax of logits [R,K,V] (whose rows
-    may lie further apart than V).  Equal ones are in the order of (beam, token).  done [R,K]
+    may lie further apart than V; the first one is 16-byte aligned).  Equal ones are in the order of (beam, token).  done [R,K]
     uint8: finished beams, which continue with `end` at no cost.  Returns (scores [R,M]
     fp32, parent [R,M], token [R,M] int32), -infinity, -1, -1 where there are fewer."""
     if logits.dim() != 3:
